@@ -100,6 +100,9 @@ typedef struct {
 #define PA_DEVERR_TIMEOUT     8u  /* a pipeline wait gave up after its bound          */
 #define PA_DEVERR_BLOCK_PAIR 16u  /* a copy pair named a block outside its cache       */
 #define PA_DEVERR_GROUP      32u  /* a shared-prefix group, member or length out of range */
+#define PA_DEVERR_POOL       64u  /* a step plan needed more free blocks than there are    */
+#define PA_DEVERR_SHARED    128u  /* a step plan would append into a shared tail block     */
+#define PA_DEVERR_TREE      256u  /* a draft-tree parent or leaf out of range              */
 
 /*
  * pa_write_kv -- cache write through slot_mapping.
@@ -431,6 +434,149 @@ pa_status pa_decode_no_alloc(const void* q, const void* k_cache, const void* v_c
  */
 pa_status pa_check_wait_timeout(int32_t expected, int32_t arrivals, int64_t limit_cycles,
                                 void* stream);
+
+/* ---- drafted (speculative) steps ------------------------------------------
+ *
+ * A verify step runs several drafted tokens of each sequence through the
+ * model at once and keeps those that hold.  How many hold is known on the
+ * device only, so the three calls below keep the step there: pa_plan_step
+ * takes blocks and slots for the drafted tokens, pa_decode_tree attends from
+ * them, pa_accept_tree keeps the accepted path.  Between them run the model's
+ * layers and the cache write (pa_write_kv with the plan's slots).  One such
+ * step can be captured in a CUDA graph and replayed: lengths, blocks held and
+ * the queue's front are device buffers that each call reads and leaves for
+ * the next.
+ */
+
+/*
+ * pa_plan_step -- block tables and slot mapping of a step, from the requests'
+ * lengths ("vLLM PagedAttention: from memory fragmentation to slot mapping"
+ * §3: slot = table[pos / B] * B + pos % B; §6: query start locations,
+ * positions and slots of the packed tokens; §4: blocks are taken from the front
+ * of the free queue, all or nothing).  It is BlockPool.grow for every sequence
+ * in order, on the device.
+ *
+ * Sequence i has C_i = seq_lens[i] cached tokens, gets n_i = new_tokens[i]
+ * more, and its table's first h_i = blocks_held[i] entries are its blocks
+ * (h_i >= ceil(C_i / B); blocks behind the cached tokens, such as those of
+ * rejected drafts, are used before fresh ones).  With
+ *   g_i = max(0, ceil((C_i + n_i) / B) - h_i)       blocks taken,
+ *   S_i, Q_i = sums of g and of n over the sequences before i,
+ *   F = *free_head:
+ *   block_tables[i][h_i + k] = free_blocks[F + S_i + k]   for k < g_i
+ *   seq_lens_out[i] = C_i + n_i, blocks_held_out[i] = h_i + g_i
+ *   query_start_loc[i] = Q_i, block_start[i] = S_i   (entry num_seqs: the sums)
+ *   *free_head_out = F + sum of g
+ * and the packed token t = Q_i + j (j < n_i) has seq_ids[t] = i,
+ * positions[t] = C_i + j and slot_mapping[t] = that position's slot.  Tokens
+ * from the sum of n up to max_tokens get -1 in all three (pa_write_kv skips
+ * them).  Other table entries are left as they were.
+ *
+ * All or nothing: when the step cannot be planned, every output is that of a
+ * step with n_i = 0 for all i (the tables, lengths, blocks held and the front
+ * stay, all tokens are -1) and a bit is raised: PA_DEVERR_POOL (F + sum of g >
+ * num_free, or F < 0), PA_DEVERR_SHARED (with ref_cnt: n_i > 0 and the partly
+ * filled tail block's count is above one: copy it first), PA_DEVERR_SEQ_LEN
+ * (C_i or n_i negative, C_i + n_i past the table or INT32_MAX, h_i outside
+ * [ceil(C_i / B), max_blocks_per_seq], or the sum of n above max_tokens).  A
+ * table entry or free block outside [0, num_blocks) gives its tokens slot -1
+ * (and a fresh entry -1) and PA_DEVERR_TABLE_ENTRY; the rest is planned.
+ *
+ * seq_lens, new_tokens, blocks_held  device or pinned int32 [num_seqs].
+ * free_blocks    device or pinned int32 [num_free], distinct, in queue order.
+ * free_head      device or pinned int32: index of the queue's front.
+ * ref_cnt        device int32 [num_blocks] or NULL: checked as above; blocks
+ *                taken get count 1.
+ * block_tables   device int32 [num_seqs][max_blocks_per_seq], updated.
+ * outputs        device or pinned; seq_lens_out, blocks_held_out and
+ *                free_head_out may be the input arrays themselves (no other
+ *                overlap).  positions and seq_ids may be NULL.
+ * num_seqs <= 65535, max_tokens < 2^31 - 2^20.
+ */
+pa_status pa_plan_step(const int32_t* seq_lens, const int32_t* new_tokens,
+                       const int32_t* blocks_held, int32_t num_seqs,
+                       const int32_t* free_blocks, int32_t num_free, const int32_t* free_head,
+                       int32_t* ref_cnt, int32_t num_blocks, int32_t block_size,
+                       int32_t* block_tables, int32_t max_blocks_per_seq,
+                       int32_t* seq_lens_out, int32_t* blocks_held_out, int32_t* free_head_out,
+                       int32_t* query_start_loc, int32_t* block_start, int64_t* slot_mapping,
+                       int32_t* positions, int32_t* seq_ids, int32_t max_tokens, void* stream);
+
+/*
+ * pa_decode_tree -- attention of a tree of drafted tokens over the cache.
+ *
+ * Sequence i owns the packed rows [query_start_loc[i], query_start_loc[i+1]):
+ * its n_i tree nodes, whose K/V are already in the cache at its last n_i
+ * positions (node j at C_i + j, C_i = T_i - n_i, T_i = seq_lens[i]).
+ * parents[r] is the node (0 .. n_i - 1, within the sequence) that row r's node
+ * continues, below the node itself; -1 for a node that continues the cached
+ * tokens.  A node sees the C_i cached tokens, its ancestors and itself:
+ *   out[r][h] = sum_{t visible} softmax_t(scale * q[r][h].k_t) v_t
+ * with kv heads, tables and lengths as in pa_prefill.  A chain (parents[j] =
+ * j - 1) is pa_prefill's causal chunk; n_i = 1 is pa_decode's row.  Keys a node
+ * does not see leave no trace in its row, whatever their K and V hold.
+ *
+ * q, out           device or pinned [total_q][num_q_heads][head_dim], cache dtype.
+ * query_start_loc  device or pinned int32 [num_seqs + 1], non-decreasing.  Rows
+ *                  from its last entry up to total_q are left as they were.
+ * parents          device or pinned int32 [total_q].
+ * max_q_len        host upper bound of n_i, at most PA_MAX_TREE_NODES.
+ * max_seq_len      host upper bound of T_i.
+ * workspace        device, >= pa_decode_tree_workspace_bytes(...) bytes, 256-byte
+ *                  aligned; may be NULL when that size is 0.  Two calls that may
+ *                  run at the same time need two workspaces.
+ * A sequence with n_i < 0 or above max_q_len, n_i > T_i, rows outside total_q
+ * or T_i out of range is reported (PA_DEVERR_SEQ_LEN) and its rows are left
+ * untouched.  A parent outside [-1, own node) is reported (PA_DEVERR_TREE)
+ * and read as -1.  A bad table entry is reported (PA_DEVERR_TABLE_ENTRY) and
+ * the rows of that sequence are undefined.
+ * The result is bitwise reproducible for fixed arguments on a fixed device.
+ */
+#define PA_MAX_TREE_NODES 256
+size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t total_q, int32_t num_q_heads,
+                                      int32_t max_q_len, int32_t max_seq_len,
+                                      const pa_cache_desc* cache);
+pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const int32_t* parents,
+                         int32_t total_q, int32_t max_q_len, const void* k_cache,
+                         const void* v_cache, const int32_t* block_tables,
+                         int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs,
+                         int32_t max_seq_len, int32_t num_q_heads, float scale, void* out,
+                         void* workspace, size_t workspace_bytes, const pa_cache_desc* cache,
+                         void* stream);
+
+/*
+ * pa_accept_tree -- keep the accepted path of each tree: its K/V rows move to
+ * the positions right behind the cached tokens, in every layer's caches.
+ *
+ * leaf[i] is the deepest accepted node of sequence i (-1: none).  With its
+ * path a_0 < a_1 < ... < a_{d-1} = leaf[i] (the node and its ancestors),
+ *   cache row at position C_i + j <- cache row at position C_i + a_j
+ * for j < d, K and V, every kv head and layer (as if all rows were read before
+ * any is written; bit-exact), and new_lens[i] = C_i + d.  The rows behind keep
+ * what they hold; their blocks stay the sequence's (pa_plan_step's
+ * blocks_held).  accepted_rows (or NULL) gets the packed rows of the path:
+ * accepted_rows[Q_i + j] = Q_i + a_j for j < d, -1 for the sequence's other
+ * rows.
+ *
+ * k_caches, v_caches  host arrays of num_layers (1 .. 1024) device caches, each
+ *                     of the geometry `cache`, all through the same tables;
+ *                     no two may share memory.
+ * parents, query_start_loc, seq_lens, tables  as pa_decode_tree.
+ * new_lens         device or pinned int32 [num_seqs]; must not be seq_lens.
+ * The blocks written must be the sequence's own (a shared one is copied first).
+ * A sequence with rows or a length out of range (as in pa_decode_tree) is
+ * reported (PA_DEVERR_SEQ_LEN): nothing moves, new_lens[i] = seq_lens[i].  A
+ * leaf outside [-1, n_i) or a bad parent on the path is reported
+ * (PA_DEVERR_TREE) and read as leaf -1.  A row behind a bad table entry is
+ * skipped and reported (PA_DEVERR_TABLE_ENTRY).
+ */
+pa_status pa_accept_tree(const int32_t* leaf, const int32_t* parents,
+                         const int32_t* query_start_loc, const int32_t* seq_lens,
+                         int32_t num_seqs, int32_t total_q, int32_t max_q_len,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         void* const* k_caches, void* const* v_caches, int32_t num_layers,
+                         int32_t* new_lens, int32_t* accepted_rows, const pa_cache_desc* cache,
+                         void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* pa_status_str(pa_status status);

@@ -24,6 +24,8 @@ from .block_pool import BlockPool, SharedTailWrite
 __all__ = ["write_kv", "write_kv_positions", "copy_blocks", "decode", "decode_append",
            "decode_shared_prefix", "prefix_groups", "PrefixGroups", "decode_shared_prefix_workspace_bytes",
            "decode_shared_prefix_mode", "prefill",
+           "plan_step", "StepPlan", "decode_tree", "decode_tree_workspace_bytes", "accept_tree",
+           "MAX_TREE_NODES",
            "decode_workspace_bytes", "decode_partition_tokens",
            "decode_path", "last_device_error", "PaError", "build", "BlockPool",
            "SharedTailWrite", "LIBRARY_PATH", "load_library", "CacheDesc"]
@@ -31,7 +33,8 @@ __all__ = ["write_kv", "write_kv_positions", "copy_blocks", "decode", "decode_ap
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA = range(5)
 PA_F32, PA_BF16 = 0, 1
 DEVERR_TABLE_ENTRY, DEVERR_SEQ_LEN, DEVERR_SLOT, DEVERR_TIMEOUT, DEVERR_BLOCK_PAIR = 1, 2, 4, 8, 16
-DEVERR_GROUP = 32
+DEVERR_GROUP, DEVERR_POOL, DEVERR_SHARED, DEVERR_TREE = 32, 64, 128, 256
+MAX_TREE_NODES = 256
 SHARED_AUTO, SHARED_ONCE, SHARED_PLAIN = 0, 1, 2
 
 
@@ -88,6 +91,16 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.pa_decode_shared_prefix_mode.argtypes = [I32, I32, I32, DP]
     lib.pa_decode_shared_prefix_mode.restype = I32
     lib.pa_decode_shared_prefix.restype = ctypes.c_int
+    lib.pa_plan_step.argtypes = [P, P, P, I32, P, I32, P, P, I32, I32, P, I32, P, P, P, P, P, P,
+                                 P, P, I32, P]
+    lib.pa_plan_step.restype = ctypes.c_int
+    lib.pa_decode_tree_workspace_bytes.argtypes = [I32, I32, I32, I32, I32, DP]
+    lib.pa_decode_tree_workspace_bytes.restype = SZ
+    lib.pa_decode_tree.argtypes = [P, P, P, I32, I32, P, P, P, I32, P, I32, I32, I32,
+                                   ctypes.c_float, P, P, SZ, DP, P]
+    lib.pa_decode_tree.restype = ctypes.c_int
+    lib.pa_accept_tree.argtypes = [P, P, P, P, I32, I32, I32, P, I32, P, P, I32, P, P, DP, P]
+    lib.pa_accept_tree.restype = ctypes.c_int
     lib.pa_decode_path.argtypes = [I32, DP]
     lib.pa_decode_path.restype = I32
     lib.pa_status_str.argtypes = [ctypes.c_int]
@@ -457,3 +470,220 @@ def prefill(q, query_start_loc, k_cache, v_cache, block_tables, seq_lens, max_q_
         hq, float(scale), _ptr(out), ctypes.byref(desc), _stream(stream))
     _check(st, "pa_prefill")
     return out
+
+
+# ---- drafted (speculative) steps ------------------------------------------------
+
+def _i32(**ts) -> None:
+    for name, t in ts.items():
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+
+
+def _on_device(device, *ts) -> None:
+    """Every CUDA tensor on the caches' (tables') device, the current one."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors live on {device}, not on the current device")
+    for t in ts:
+        if t is not None and t.is_cuda and t.device != device:
+            raise ValueError("tensors live on different devices")
+
+
+class StepPlan:
+    """What ``plan_step`` writes, all int32 but slot_mapping (int64):
+    ``seq_lens`` and ``blocks_held`` [N] after the step, ``free_head`` [1],
+    ``query_start_loc`` and ``block_start`` [N + 1], and per packed token
+    ``slot_mapping``, ``positions`` and ``seq_ids`` [max_tokens] (the last two
+    may be None).  A loop keeps one plan and passes it every step."""
+
+    __slots__ = ("seq_lens", "blocks_held", "free_head", "query_start_loc", "block_start",
+                 "slot_mapping", "positions", "seq_ids")
+
+    def __init__(self, seq_lens, blocks_held, free_head, query_start_loc, block_start,
+                 slot_mapping, positions=None, seq_ids=None):
+        self.seq_lens = seq_lens
+        self.blocks_held = blocks_held
+        self.free_head = free_head
+        self.query_start_loc = query_start_loc
+        self.block_start = block_start
+        self.slot_mapping = slot_mapping
+        self.positions = positions
+        self.seq_ids = seq_ids
+
+    @classmethod
+    def empty(cls, num_seqs: int, max_tokens: int, device="cuda") -> "StepPlan":
+        def i32(n):
+            return torch.empty(n, dtype=torch.int32, device=device)
+
+        return cls(i32(num_seqs), i32(num_seqs), i32(1), i32(num_seqs + 1), i32(num_seqs + 1),
+                   torch.empty(max_tokens, dtype=torch.int64, device=device), i32(max_tokens),
+                   i32(max_tokens))
+
+
+def plan_step(seq_lens, new_tokens, block_tables, blocks_held, free_blocks, free_head,
+              num_blocks: int, block_size: int, plan: StepPlan | None = None,
+              max_tokens: int | None = None, ref_cnt=None, stream=None) -> StepPlan:
+    """Block tables and slot mapping of a step from the requests' lengths, on
+    the device: ``BlockPool.grow`` for every sequence in order.
+
+    Sequence i has seq_lens[i] cached tokens, gets new_tokens[i] more and
+    holds the first blocks_held[i] entries of its row of ``block_tables``
+    [N, max_blocks] (updated in place); blocks come from the front of
+    ``free_blocks`` (int32, from index free_head[0]).  Writes ``plan`` (or a
+    new one for ``max_tokens`` tokens) and returns it; its seq_lens,
+    blocks_held and free_head may be the input tensors.  A step that does not
+    fit plans nothing and raises a bit of ``last_device_error``
+    (DEVERR_POOL, DEVERR_SHARED, DEVERR_SEQ_LEN).  ``ref_cnt`` (int32
+    [num_blocks]) adds the shared-tail check and the counts of taken blocks."""
+    _dev(block_tables)
+    _dev_or_pinned(seq_lens, new_tokens, blocks_held, free_blocks, free_head)
+    _i32(seq_lens=seq_lens, new_tokens=new_tokens, blocks_held=blocks_held,
+         free_blocks=free_blocks, free_head=free_head, block_tables=block_tables,
+         ref_cnt=ref_cnt)
+    n = seq_lens.numel()
+    if new_tokens.numel() != n or blocks_held.numel() != n or block_tables.dim() != 2 \
+            or block_tables.shape[0] != n or free_head.numel() != 1:
+        raise ValueError("seq_lens, new_tokens, blocks_held and block_tables disagree on the "
+                         "sequence count")
+    if plan is None:
+        if max_tokens is None:
+            raise ValueError("pass a plan or max_tokens")
+        plan = StepPlan.empty(n, max_tokens, block_tables.device)
+    outs = (plan.seq_lens, plan.blocks_held, plan.free_head, plan.query_start_loc,
+            plan.block_start, plan.positions, plan.seq_ids)
+    _dev_or_pinned(plan.slot_mapping, *(t for t in outs if t is not None))
+    _i32(**dict(zip(StepPlan.__slots__, outs[:5])), positions=plan.positions,
+         seq_ids=plan.seq_ids)
+    tokens = plan.slot_mapping.numel()
+    if plan.slot_mapping.dtype != torch.int64:
+        raise ValueError("slot_mapping must be int64")
+    if [t.numel() for t in outs[:5]] != [n, n, 1, n + 1, n + 1] \
+            or any(t is not None and t.numel() != tokens for t in outs[5:]) \
+            or (max_tokens is not None and max_tokens != tokens):
+        raise ValueError("the plan's buffers do not fit the step")
+    if ref_cnt is not None:
+        _dev(ref_cnt)
+        if ref_cnt.numel() != num_blocks:
+            raise ValueError("ref_cnt must have num_blocks entries")
+    _on_device(block_tables.device, seq_lens, new_tokens, blocks_held, free_blocks, free_head,
+               ref_cnt, plan.slot_mapping, *outs)
+    st = load_library().pa_plan_step(
+        _ptr(seq_lens), _ptr(new_tokens), _ptr(blocks_held), n, _ptr(free_blocks),
+        free_blocks.numel(), _ptr(free_head), _ptr(ref_cnt), num_blocks, block_size,
+        _ptr(block_tables), block_tables.shape[1], _ptr(plan.seq_lens), _ptr(plan.blocks_held),
+        _ptr(plan.free_head), _ptr(plan.query_start_loc), _ptr(plan.block_start),
+        _ptr(plan.slot_mapping), _ptr(plan.positions), _ptr(plan.seq_ids), tokens,
+        _stream(stream))
+    _check(st, "pa_plan_step")
+    return plan
+
+
+def decode_tree_workspace_bytes(num_seqs: int, total_q: int, num_q_heads: int, max_q_len: int,
+                                max_seq_len: int, k_cache) -> int:
+    desc = k_cache if isinstance(k_cache, CacheDesc) else cache_desc(k_cache)
+    return int(load_library().pa_decode_tree_workspace_bytes(
+        num_seqs, total_q, num_q_heads, max_q_len, max_seq_len, ctypes.byref(desc)))
+
+
+def decode_tree(q, query_start_loc, parents, k_cache, v_cache, block_tables, seq_lens,
+                max_q_len: int, max_seq_len: int, scale: float | None = None, out=None,
+                workspace=None, stream=None) -> torch.Tensor:
+    """Attention of trees of drafted tokens over the paged cache: sequence i's
+    packed rows query_start_loc[i]..query_start_loc[i+1] are its tree's nodes,
+    already in the cache at its last positions.  A node sees the cached
+    tokens, its ancestors (``parents`` [total_q]: the node it continues,
+    within its sequence, -1 for the cached tokens) and itself.  Returns out
+    [total_q, Hq, D] in the cache dtype; rows behind the last sequence are
+    left as they were (a missing ``out`` is allocated, not cleared)."""
+    _dev(k_cache, v_cache)
+    _dev_or_pinned(q, query_start_loc, parents, block_tables, seq_lens)
+    _i32(query_start_loc=query_start_loc, parents=parents, block_tables=block_tables,
+         seq_lens=seq_lens)
+    desc = cache_desc(k_cache)
+    if tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("k_cache and v_cache shapes differ")
+    if q.dim() != 3 or q.shape[2] != desc.head_dim:
+        raise ValueError(f"q must be [total_q, num_q_heads, {desc.head_dim}]")
+    total, hq, d = q.shape
+    n = seq_lens.numel()
+    if q.dtype != k_cache.dtype or v_cache.dtype != k_cache.dtype:
+        raise ValueError("q and caches must share one dtype")
+    if query_start_loc.numel() != n + 1 or parents.numel() != total \
+            or block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("query_start_loc, parents, block_tables and seq_lens disagree on the "
+                         "sequence or row count")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q, device=k_cache.device)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    _dev_or_pinned(out)
+    need = decode_tree_workspace_bytes(n, total, hq, max_q_len, max_seq_len, desc)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=k_cache.device)
+    if workspace is not None:
+        _dev(workspace)
+    _on_device(k_cache.device, v_cache, q, query_start_loc, parents, block_tables, seq_lens, out,
+               workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = load_library().pa_decode_tree(
+        _ptr(q), _ptr(query_start_loc), _ptr(parents), total, max_q_len, _ptr(k_cache),
+        _ptr(v_cache), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), n, max_seq_len,
+        hq, float(scale), _ptr(out), _ptr(workspace), ws_bytes, ctypes.byref(desc),
+        _stream(stream))
+    _check(st, "pa_decode_tree")
+    return out
+
+
+def accept_tree(leaf, parents, query_start_loc, seq_lens, k_caches, v_caches, block_tables,
+                max_q_len: int, new_lens=None, accepted_rows=None, stream=None):
+    """Keeps each tree's accepted path: leaf[i] is its deepest accepted node
+    (-1: none); the K/V rows of that node and its ancestors move to the
+    positions right behind the cached tokens, in every layer.  ``k_caches``
+    and ``v_caches`` are one cache each, a [layers, num_blocks, Hkv, B, D]
+    tensor, or a sequence of caches.  Returns (new_lens [N], accepted_rows
+    [total_q]): the lengths with the path, and per sequence the packed rows
+    of its path from its first row on, then -1 (rows behind the last sequence
+    are left as they were)."""
+    def layers(c):
+        if isinstance(c, torch.Tensor):
+            _dev(c)
+            return [c] if c.dim() == 4 else list(c.unbind(0))
+        return list(c)
+
+    k_caches, v_caches = layers(k_caches), layers(v_caches)
+    if not k_caches or len(k_caches) != len(v_caches):
+        raise ValueError("k_caches and v_caches must have the same number of layers")
+    first = k_caches[0]
+    for c in k_caches + v_caches:
+        if c.shape != first.shape or c.dtype != first.dtype or c.device != first.device:
+            raise ValueError("the caches must share one shape, dtype and device")
+    _dev(*k_caches, *v_caches)
+    _dev_or_pinned(leaf, parents, query_start_loc, seq_lens, block_tables)
+    _i32(leaf=leaf, parents=parents, query_start_loc=query_start_loc, seq_lens=seq_lens,
+         block_tables=block_tables)
+    desc = cache_desc(first)
+    n, total = seq_lens.numel(), parents.numel()
+    if leaf.numel() != n or query_start_loc.numel() != n + 1 or block_tables.dim() != 2 \
+            or block_tables.shape[0] != n:
+        raise ValueError("leaf, query_start_loc, block_tables and seq_lens disagree on the "
+                         "sequence count")
+    if new_lens is None:
+        new_lens = torch.empty(n, dtype=torch.int32, device=first.device)
+    if accepted_rows is None:
+        accepted_rows = torch.empty(total, dtype=torch.int32, device=first.device)
+    _dev_or_pinned(new_lens, accepted_rows)
+    _i32(new_lens=new_lens, accepted_rows=accepted_rows)
+    if new_lens.numel() != n or accepted_rows.numel() != total:
+        raise ValueError("new_lens must have N and accepted_rows total_q entries")
+    _on_device(first.device, leaf, parents, query_start_loc, seq_lens, block_tables, new_lens,
+               accepted_rows)
+    ptrs = ctypes.c_void_p * len(k_caches)
+    st = load_library().pa_accept_tree(
+        _ptr(leaf), _ptr(parents), _ptr(query_start_loc), _ptr(seq_lens), n, total, max_q_len,
+        _ptr(block_tables), block_tables.shape[1], ptrs(*map(_ptr, k_caches)),
+        ptrs(*map(_ptr, v_caches)), len(k_caches), _ptr(new_lens), _ptr(accepted_rows),
+        ctypes.byref(desc), _stream(stream))
+    _check(st, "pa_accept_tree")
+    return new_lens, accepted_rows

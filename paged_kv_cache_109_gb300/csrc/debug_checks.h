@@ -216,5 +216,41 @@ inline pa_status check_pairs(const int64_t* pairs, int32_t n, int32_t src_blocks
     return PA_OK;
 }
 
+// The free queue of a step plan: from its front, ids inside the pool, none
+// twice.
+inline pa_status check_free(const int32_t* free_blocks, int32_t num_free, const int32_t* head,
+                            int32_t num_blocks, cudaStream_t st) {
+    std::vector<int32_t> f, h;
+    if (!fetch(h, head, 1, st) || !fetch(f, free_blocks, (size_t)num_free, st)) return PA_ERR_CUDA;
+    std::vector<char> seen((size_t)num_blocks, 0);
+    for (int32_t j = std::max(0, h[0]); j < num_free; ++j) {
+        if (f[j] < 0 || f[j] >= num_blocks) return fail("free block outside the pool (entry, id)", j, f[j]);
+        if (seen[f[j]]++) return fail("block twice in the free queue (entry, id)", j, f[j]);
+    }
+    return PA_OK;
+}
+
+// Draft trees: rows in order and at most max_q_len a sequence, every parent a
+// node below its own or -1, and (with leaf) every leaf a node or -1.
+inline pa_status check_tree(const int32_t* query_start, int32_t num_seqs, const int32_t* parents,
+                            int32_t total_q, int32_t max_q_len, const int32_t* leaf,
+                            cudaStream_t st) {
+    std::vector<int32_t> qs, par, lf;
+    if (!fetch(qs, query_start, (size_t)num_seqs + 1, st) ||
+        !fetch(par, parents, (size_t)total_q, st) ||
+        (leaf && !fetch(lf, leaf, (size_t)num_seqs, st)))
+        return PA_ERR_CUDA;
+    for (int32_t i = 0; i < num_seqs; ++i) {
+        const int64_t n = (int64_t)qs[i + 1] - qs[i];
+        if (qs[i] < 0 || n < 0 || n > max_q_len || qs[i + 1] > total_q)
+            return fail("tree rows out of order (sequence, start)", i, qs[i]);
+        for (int32_t j = 0; j < n; ++j)
+            if (par[qs[i] + j] < -1 || par[qs[i] + j] >= j)
+                return fail("tree parent outside [-1, node) (row, parent)", qs[i] + j, par[qs[i] + j]);
+        if (leaf && (lf[i] < -1 || lf[i] >= n)) return fail("leaf outside the tree (sequence, leaf)", i, lf[i]);
+    }
+    return PA_OK;
+}
+
 }  // namespace debug
 }  // namespace pa

@@ -1,0 +1,280 @@
+// draft.cuh -- host side of the drafted (speculative) step's calls:
+// pa_plan_step, pa_decode_tree, pa_accept_tree.  Included by pa.cu, whose
+// argument helpers and launch it uses.
+#pragma once
+
+#include "accept_tree.cuh"
+#include "plan_step.cuh"
+#include "tree_args.cuh"
+#include "tree_generic.cuh"
+
+namespace pa {
+namespace {
+
+// Device memory of the current device (or managed memory).
+bool current_device_memory(const void* p) {
+    if (!p) return false;
+    cudaPointerAttributes at;
+    int dev = -1;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == dev);
+}
+
+// Arrays of na and nb bytes share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+pa_status plan_impl(PlanArgs a, cudaStream_t st) {
+    cudaError_t err = launch_pdl(plan_scan_kernel, dim3(1), dim3(kPlanScanThreads), 0, st, a);
+    if (err != cudaSuccess) return PA_ERR_CUDA;
+    // at most a token, and at most a fresh block a token, per thread and round
+    const int64_t sms = std::max(1, device_sm_count());
+    const int64_t want = ((int64_t)a.max_tokens + kPlanFillThreads - 1) / kPlanFillThreads;
+    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, sms * 8));
+    err = launch_pdl(plan_fill_kernel, dim3(grid), dim3(kPlanFillThreads), 0, st, a);
+    return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" {
+
+pa_status pa_plan_step(const int32_t* seq_lens, const int32_t* new_tokens,
+                       const int32_t* blocks_held, int32_t num_seqs,
+                       const int32_t* free_blocks, int32_t num_free, const int32_t* free_head,
+                       int32_t* ref_cnt, int32_t num_blocks, int32_t block_size,
+                       int32_t* block_tables, int32_t max_blocks_per_seq,
+                       int32_t* seq_lens_out, int32_t* blocks_held_out, int32_t* free_head_out,
+                       int32_t* query_start_loc, int32_t* block_start, int64_t* slot_mapping,
+                       int32_t* positions, int32_t* seq_ids, int32_t max_tokens, void* stream) {
+    const CallRange range("pa_plan_step");
+    constexpr int32_t kMost = INT32_MAX - (1 << 20);
+    if (num_seqs < 0 || num_free < 0 || num_blocks <= 0 || block_size <= 0 ||
+        max_blocks_per_seq < 0 || max_tokens < 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs > 65535 || max_tokens >= kMost || num_free >= kMost) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!seq_lens || !new_tokens || !blocks_held || !free_head || !block_tables ||
+        !seq_lens_out || !blocks_held_out || !free_head_out || !query_start_loc || !block_start ||
+        (max_tokens > 0 && !slot_mapping) || (num_free > 0 && !free_blocks))
+        return PA_ERR_INVALID_ARG;
+    PlanArgs a{seq_lens, new_tokens, blocks_held, free_blocks, free_head, ref_cnt, block_tables,
+               seq_lens_out, blocks_held_out, free_head_out, query_start_loc, block_start,
+               slot_mapping, positions, seq_ids, num_seqs, num_free, num_blocks, block_size,
+               max_blocks_per_seq, max_tokens};
+    // every output apart from every other array, but for the three that may be
+    // the inputs themselves
+    const size_t n = (size_t)num_seqs * 4, tok = (size_t)max_tokens * 4;
+    struct Span {
+        const void* p;
+        size_t bytes, align;
+    };
+    const Span in[] = {{seq_lens, n, 4}, {new_tokens, n, 4}, {blocks_held, n, 4},
+                       {free_blocks, (size_t)num_free * 4, 4}, {free_head, 4, 4}};
+    const Span out[] = {{seq_lens_out, n, 4}, {blocks_held_out, n, 4}, {free_head_out, 4, 4},
+                        {query_start_loc, n + 4, 4}, {block_start, n + 4, 4},
+                        {slot_mapping, 2 * tok, 8}, {positions, tok, 4}, {seq_ids, tok, 4},
+                        {block_tables, n * max_blocks_per_seq, 4},
+                        {ref_cnt, (size_t)num_blocks * 4, 4}};
+    for (const Span& x : in)
+        if (!aligned(x.p, x.align)) return PA_ERR_INVALID_ARG;
+    for (size_t x = 0; x < sizeof(out) / sizeof(out[0]); ++x) {
+        if (!aligned(out[x].p, out[x].align)) return PA_ERR_INVALID_ARG;
+        for (size_t y = 0; y < x; ++y)
+            if (overlap(out[x].p, out[x].bytes, out[y].p, out[y].bytes)) return PA_ERR_INVALID_ARG;
+        for (const Span& y : in) {
+            const bool same = out[x].p == y.p && ((out[x].p == seq_lens_out && y.p == seq_lens) ||
+                                                  (out[x].p == blocks_held_out && y.p == blocks_held) ||
+                                                  (out[x].p == free_head_out && y.p == free_head));
+            if (!same && overlap(out[x].p, out[x].bytes, y.p, y.bytes)) return PA_ERR_INVALID_ARG;
+        }
+    }
+    if (!map_step_arg(a.seq_lens) || !map_step_arg(a.new_tokens) || !map_step_arg(a.blocks_held) ||
+        !map_step_arg(a.free_blocks) || !map_step_arg(a.free_head) ||
+        !map_step_arg(a.seq_lens_out) || !map_step_arg(a.blocks_held_out) ||
+        !map_step_arg(a.free_head_out) || !map_step_arg(a.query_start) ||
+        !map_step_arg(a.block_start) || !map_step_arg(a.slot_mapping) ||
+        !map_step_arg(a.positions) || !map_step_arg(a.seq_ids) ||
+        !current_device_memory(block_tables) || (ref_cnt && !current_device_memory(ref_cnt)))
+        return PA_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (debug::enabled()) {
+        const pa_status r = debug::check_free(a.free_blocks, num_free, a.free_head, num_blocks, st);
+        if (r != PA_OK) return r;
+    }
+    return plan_impl(a, st);
+}
+
+size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t total_q, int32_t num_q_heads,
+                                      int32_t max_q_len, int32_t max_seq_len,
+                                      const pa_cache_desc* cache) {
+    (void)total_q;
+    (void)max_q_len;
+    if (pa_decode_path(num_q_heads, cache) < 0 || num_seqs < 0 || max_seq_len < 0) return 0;
+    return 0;
+}
+
+pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const int32_t* parents,
+                         int32_t total_q, int32_t max_q_len, const void* k_cache,
+                         const void* v_cache, const int32_t* block_tables,
+                         int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs,
+                         int32_t max_seq_len, int32_t num_q_heads, float scale, void* out,
+                         void* workspace, size_t workspace_bytes_given, const pa_cache_desc* cache,
+                         void* stream) {
+    const CallRange range("pa_decode_tree");
+    if (pa_decode_path(num_q_heads, cache) < 0 || num_seqs < 0 || total_q < 0 || max_q_len < 0 ||
+        max_seq_len < 0 || max_blocks_per_seq < 0 || max_q_len > max_seq_len)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_q == 0) return PA_OK;
+    if (!q || !query_start_loc || !parents || !k_cache || !v_cache || !block_tables ||
+        !seq_lens || !out)
+        return PA_ERR_INVALID_ARG;
+    if ((int64_t)max_blocks_per_seq * cache->block_size < max_seq_len) return PA_ERR_INVALID_ARG;
+    if (max_q_len > PA_MAX_TREE_NODES || num_seqs > 65535 || cache->num_kv_heads > 65535 ||
+        cache->head_dim > 32 * kTreeDimPerLane)
+        return PA_ERR_UNSUPPORTED;
+    const int eb = elem_bytes(cache);
+    if (!aligned(q, eb) || !aligned(out, eb) || !aligned(k_cache, eb) || !aligned(v_cache, eb) ||
+        !aligned(query_start_loc, 4) || !aligned(parents, 4) || !aligned(block_tables, 4) ||
+        !aligned(seq_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    if (!map_step_arg(q) || !map_step_arg(query_start_loc) || !map_step_arg(parents) ||
+        !map_step_arg(block_tables) || !map_step_arg(seq_lens) || !map_step_arg(out) ||
+        !current_device_memory(k_cache) || !current_device_memory(v_cache))
+        return PA_ERR_INVALID_ARG;
+    const size_t need = pa_decode_tree_workspace_bytes(num_seqs, total_q, num_q_heads, max_q_len,
+                                                       max_seq_len, cache);
+    if (need > 0 && (!workspace || workspace_bytes_given < need || !aligned(workspace, 256) ||
+                     !current_device_memory(workspace)))
+        return PA_ERR_WORKSPACE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (debug::enabled()) {
+        pa_status r = debug::check_tables(block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+                                          max_seq_len, query_start_loc, total_q, cache, st);
+        if (r == PA_OK)
+            r = debug::check_tree(query_start_loc, num_seqs, parents, total_q, max_q_len, nullptr, st);
+        if (r != PA_OK) return r;
+    }
+    TreeArgs a{};
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.query_start = query_start_loc;
+    a.parents = parents;
+    a.seq_lens = seq_lens;
+    a.block_tables = block_tables;
+    a.out = out;
+    a.num_seqs = num_seqs;
+    a.total_q = total_q;
+    a.max_q_len = max_q_len;
+    a.max_seq_len = max_seq_len;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = cache->num_blocks;
+    a.block_size = cache->block_size;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = cache->num_kv_heads;
+    a.group = num_q_heads / cache->num_kv_heads;
+    a.head_dim = cache->head_dim;
+    a.scale_log2 = scale * kLog2e;
+    const dim3 grid(total_q, cache->num_kv_heads);
+    const cudaError_t err =
+        cache->dtype == PA_F32
+            ? launch_pdl(tree_generic_kernel<float>, grid, dim3(128), 0, st, a)
+            : launch_pdl(tree_generic_kernel<__nv_bfloat16>, grid, dim3(128), 0, st, a);
+    return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_accept_tree(const int32_t* leaf, const int32_t* parents,
+                         const int32_t* query_start_loc, const int32_t* seq_lens,
+                         int32_t num_seqs, int32_t total_q, int32_t max_q_len,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         void* const* k_caches, void* const* v_caches, int32_t num_layers,
+                         int32_t* new_lens, int32_t* accepted_rows, const pa_cache_desc* cache,
+                         void* stream) {
+    const CallRange range("pa_accept_tree");
+    if (!desc_ok(cache) || num_seqs < 0 || total_q < 0 || max_q_len < 0 || num_layers < 1 ||
+        max_blocks_per_seq < 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (max_q_len > PA_MAX_TREE_NODES || num_layers > kAcceptMaxLayers) return PA_ERR_UNSUPPORTED;
+    if (!leaf || (!parents && total_q > 0) || !query_start_loc || !seq_lens || !block_tables ||
+        !k_caches || !v_caches || !new_lens)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(leaf, 4) || !aligned(parents, 4) || !aligned(query_start_loc, 4) ||
+        !aligned(seq_lens, 4) || !aligned(block_tables, 4) || !aligned(new_lens, 4) ||
+        !aligned(accepted_rows, 4))
+        return PA_ERR_INVALID_ARG;
+    // the outputs apart from the inputs and from one another
+    const size_t n = (size_t)num_seqs * 4, rows = (size_t)total_q * 4;
+    const size_t tab = n * max_blocks_per_seq;
+    if (overlap(new_lens, n, accepted_rows, rows)) return PA_ERR_INVALID_ARG;
+    const std::pair<const void*, size_t> in[] = {{leaf, n}, {parents, rows},
+                                                 {query_start_loc, n + 4}, {seq_lens, n},
+                                                 {block_tables, tab}};
+    for (const auto& x : in)
+        if (overlap(new_lens, n, x.first, x.second) ||
+            overlap(accepted_rows, rows, x.first, x.second))
+            return PA_ERR_INVALID_ARG;
+    AcceptArgs a{leaf, parents, query_start_loc, seq_lens, block_tables, new_lens, accepted_rows,
+                 total_q, max_q_len, max_blocks_per_seq, cache->num_blocks, cache->block_size,
+                 cache->num_kv_heads, cache->head_dim * elem_bytes(cache)};
+    if (!map_step_arg(a.leaf) || !map_step_arg(a.parents) || !map_step_arg(a.query_start) ||
+        !map_step_arg(a.seq_lens) || !map_step_arg(a.block_tables) ||
+        !map_step_arg(a.new_lens) || !map_step_arg(a.accepted_rows))
+        return PA_ERR_INVALID_ARG;
+    int vec = 16;
+    while (vec > 2 && a.row_bytes % vec) vec >>= 1;
+    // the caches, none of which may share a byte with another (their moves
+    // would race)
+    uintptr_t bases[2 * kAcceptMaxLayers];
+    for (int32_t l = 0; l < num_layers; ++l) {
+        for (int which = 0; which < 2; ++which) {
+            void* c = which ? v_caches[l] : k_caches[l];
+            if (!current_device_memory(c) || !aligned(c, elem_bytes(cache)))
+                return PA_ERR_INVALID_ARG;
+            while (vec > 2 && !aligned(c, vec)) vec >>= 1;
+            bases[2 * l + which] = reinterpret_cast<uintptr_t>(c);
+        }
+    }
+    std::sort(bases, bases + 2 * num_layers);
+    const size_t cache_bytes = (size_t)cache->num_blocks * cache->num_kv_heads *
+                               cache->block_size * (size_t)a.row_bytes;
+    for (int32_t x = 1; x < 2 * num_layers; ++x)
+        if (bases[x] - bases[x - 1] < cache_bytes) return PA_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (debug::enabled()) {
+        const pa_status r = debug::check_tree(a.query_start, num_seqs, a.parents, total_q,
+                                              max_q_len, a.leaf, st);
+        if (r != PA_OK) return r;
+    }
+    for (int32_t l0 = 0; l0 < num_layers; l0 += kAcceptLayers) {
+        const int32_t nl = std::min(kAcceptLayers, num_layers - l0);
+        AcceptCaches c{};
+        for (int32_t l = 0; l < nl; ++l) {
+            c.k[l] = static_cast<uint8_t*>(k_caches[l0 + l]);
+            c.v[l] = static_cast<uint8_t*>(v_caches[l0 + l]);
+        }
+        if (l0 > 0) a.new_lens = nullptr;        // written by the first launch
+        const dim3 grid(num_seqs, 2 * nl);
+        auto go = [&](auto kern) {
+            return launch_pdl(kern, grid, dim3(kAcceptThreads), 0, st, a, c);
+        };
+        cudaError_t err;
+        switch (vec) {
+            case 16: err = go(accept_tree_kernel<16>); break;
+            case 8: err = go(accept_tree_kernel<8>); break;
+            case 4: err = go(accept_tree_kernel<4>); break;
+            default: err = go(accept_tree_kernel<2>); break;
+        }
+        if (err != cudaSuccess) return PA_ERR_CUDA;
+    }
+    return PA_OK;
+}
+
+}  // extern "C"

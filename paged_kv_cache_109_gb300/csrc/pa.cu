@@ -1020,6 +1020,9 @@ int32_t pa_last_device_error(void) {
 
 }  // extern "C"
 
+// ---- drafted (speculative) steps: pa_plan_step, pa_decode_tree, pa_accept_tree ----
+#include "draft.cuh"
+
 // ---- decode without any caller-provided workspace -------------------------------
 //
 // Some callers cannot allocate device memory at the point where they run
