@@ -7,6 +7,7 @@
 #include "plan_step.cuh"
 #include "tree_args.cuh"
 #include "tree_generic.cuh"
+#include "tree_ws.cuh"
 
 namespace pa {
 namespace {
@@ -38,6 +39,94 @@ pa_status plan_impl(PlanArgs a, cudaStream_t st) {
     const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, sms * 8));
     err = launch_pdl(plan_fill_kernel, dim3(grid), dim3(kPlanFillThreads), 0, st, a);
     return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// ---- tree attention: kernel choice, work division, workspace ---------------------
+
+// Rows of a TMA box of the tcgen05 tree kernel: a box lies inside one block,
+// and 8 rows are one 128-byte swizzle atom.
+int32_t tree_box_rows(int32_t block_size) {
+    return block_size % 16 == 0 ? 16 : block_size % 8 == 0 ? 8 : 0;
+}
+
+// The tcgen05 kernel's shapes: bf16, head dims that are multiples of 16 up to
+// 128, block sizes that are multiples of 8.
+bool tree_ws_shape(const pa_cache_desc* c) {
+    return c->dtype == PA_BF16 && c->head_dim % 16 == 0 && c->head_dim <= 128 &&
+           tree_box_rows(c->block_size) > 0;
+}
+
+// A tile of `rows` (node, query head) rows, `tiles` of them a unit.
+TreeShape tree_shape(int32_t rows, int32_t tiles, int32_t keys, int32_t group) {
+    TreeShape s{};
+    s.rows = rows;
+    s.tiles = tiles;
+    s.heads = std::min(group, rows);
+    s.tokens = rows / s.heads;
+    s.sub_groups = (group + s.heads - 1) / s.heads;
+    s.keys = keys;
+    s.overhead = 1;
+    s.min_range = 3;
+    return s;
+}
+
+// CTAs of a call: `per_sm` a SM, fewer when the host's bounds say that less
+// work can be there.
+int32_t tree_ctas(const TreeShape& s, int32_t num_seqs, int32_t max_q_len, int32_t max_seq_len,
+                  int32_t num_kv_heads, int32_t per_sm) {
+    const int64_t per = (int64_t)s.tokens * s.tiles;
+    const int64_t units = (int64_t)num_seqs * num_kv_heads * s.sub_groups * ((max_q_len + per - 1) / per);
+    const int64_t cost = ((int64_t)max_seq_len + s.keys - 1) / s.keys + s.overhead;
+    const int64_t ctas = (units * cost + s.min_range - 1) / s.min_range;
+    return (int32_t)std::max<int64_t>(
+        1, std::min<int64_t>(ctas, (int64_t)std::max(1, device_sm_count()) * per_sm));
+}
+
+size_t tree_workspace(const TreeShape& s, int32_t ctas, int32_t num_seqs, int32_t head_dim) {
+    return 256 + align256(((size_t)num_seqs + 1) * 8) +
+           align256(2 * (size_t)ctas * tree_cell_floats(s, head_dim) * 4);
+}
+
+TreeShape tree_ws_tiling(int32_t group) { return tree_shape(128, 2, 128, group); }
+
+// As encode_cache_map, with boxes of `rows` rows.
+bool encode_tree_map(CUtensorMap* map, const void* base, const pa_cache_desc* c, int32_t rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->block_size,
+                          (cuuint64_t)c->num_blocks * (cuuint64_t)c->num_kv_heads};
+    cuuint64_t strides[2] = {(cuuint64_t)c->head_dim * 2,
+                             (cuuint64_t)c->head_dim * 2 * (cuuint64_t)c->block_size};
+    cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_tree_ws(const TreeArgs& a, const TreeWork& w, const pa_cache_desc* c,
+                           int32_t ctas, cudaStream_t st) {
+    using Cfg = TreeWsCfg<D>;
+    const int32_t rows = tree_box_rows(c->block_size);
+    CUtensorMap mk, mv;
+    if (!encode_tree_map(&mk, a.k_cache, c, rows) || !encode_tree_map(&mv, a.v_cache, c, rows))
+        return cudaErrorUnknown;
+    auto kern = tree_ws_kernel<D>;
+    if (!set_smem(kern, Cfg::smem_bytes())) return cudaErrorUnknown;
+    return launch_pdl(kern, dim3(ctas), dim3(Cfg::kThreads), Cfg::smem_bytes(), st, mk, mv, a, w,
+                      rows);
+}
+
+template <typename E>
+cudaError_t launch_tree_merge(const TreeArgs& a, const TreeWork& w, int32_t ctas, cudaStream_t st) {
+    if (ctas == 1) return cudaSuccess;
+    // one round of a thread per (row, eight columns) of the largest unit
+    const int32_t items = w.s.rows * w.s.tiles * ((a.head_dim + 7) / 8);
+    return launch_pdl(tree_merge_kernel<E>,
+                      dim3(ctas - 1, (items + kTreeMergeThreads - 1) / kTreeMergeThreads),
+                      dim3(kTreeMergeThreads), 0, st, a, w);
 }
 
 }  // namespace
@@ -114,10 +203,13 @@ pa_status pa_plan_step(const int32_t* seq_lens, const int32_t* new_tokens,
 size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t total_q, int32_t num_q_heads,
                                       int32_t max_q_len, int32_t max_seq_len,
                                       const pa_cache_desc* cache) {
-    (void)total_q;
-    (void)max_q_len;
-    if (pa_decode_path(num_q_heads, cache) < 0 || num_seqs < 0 || max_seq_len < 0) return 0;
-    return 0;
+    if (pa_decode_path(num_q_heads, cache) < 0 || num_seqs <= 0 || total_q <= 0 ||
+        max_q_len <= 0 || max_seq_len <= 0)
+        return 0;
+    if (!tree_ws_shape(cache)) return 0;
+    const TreeShape s = tree_ws_tiling(num_q_heads / cache->num_kv_heads);
+    const int32_t ctas = tree_ctas(s, num_seqs, max_q_len, max_seq_len, cache->num_kv_heads, 1);
+    return tree_workspace(s, ctas, num_seqs, cache->head_dim);
 }
 
 pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const int32_t* parents,
@@ -182,6 +274,22 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
     a.group = num_q_heads / cache->num_kv_heads;
     a.head_dim = cache->head_dim;
     a.scale_log2 = scale * kLog2e;
+    // the tcgen05 kernel takes a row's maximum before it scales: scale >= 0
+    const bool ws = tree_ws_shape(cache) && aligned(q, 16) && aligned(out, 16) &&
+                    aligned(k_cache, 16) && aligned(v_cache, 16) && scale >= 0.f;
+    if (ws) {
+        TreeWork w{};
+        w.s = tree_ws_tiling(a.group);
+        const int32_t ctas = tree_ctas(w.s, num_seqs, max_q_len, max_seq_len, a.num_kv_heads, 1);
+        uint8_t* base = static_cast<uint8_t*>(workspace);
+        w.header = reinterpret_cast<int64_t*>(base);
+        w.seq_cost = reinterpret_cast<int64_t*>(base + 256);
+        w.cells = reinterpret_cast<float*>(base + 256 + align256(((size_t)num_seqs + 1) * 8));
+        cudaError_t err = cache->head_dim > 64 ? launch_tree_ws<128>(a, w, cache, ctas, st)
+                                               : launch_tree_ws<64>(a, w, cache, ctas, st);
+        if (err == cudaSuccess) err = launch_tree_merge<__nv_bfloat16>(a, w, ctas, st);
+        return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
     const dim3 grid(total_q, cache->num_kv_heads);
     const cudaError_t err =
         cache->dtype == PA_F32

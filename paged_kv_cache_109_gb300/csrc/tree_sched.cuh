@@ -1,0 +1,264 @@
+// tree_sched.cuh -- how the draft-tree attention kernels divide their work, and
+// the merge of the parts.
+//
+// A unit is one (sequence, kv head, sub-group of query heads, tile of tree
+// tokens) with all its keys; its cost is its key blocks plus `overhead` for
+// its prologue and epilogue.  The units' costs laid end to end are cut into
+// equal ranges, one per CTA of a grid that fills the GPU once, so the load is
+// even whatever the lengths are: a CTA takes the tail of one unit, some whole
+// units and the head of another.  A unit inside one range is written to the
+// output at once.  Of a unit cut by a range's end every part leaves (acc, m,
+// l) in its CTA's workspace cells -- at most two a CTA: cell 0 the part that
+// continues an earlier CTA's, cell 1 the one that starts here -- and
+// tree_merge_kernel joins them by log-sum-exp:
+//   M = max_p m_p,  w_p = 2^(m_p - M),  out = sum w_p acc_p / sum w_p l_p.
+// The cells' number depends on the grid alone, not on the batch.
+#pragma once
+
+#include "tree_args.cuh"
+
+namespace pa {
+
+// Tiling of a kernel (host constants of a launch).
+struct TreeShape {
+    int32_t rows;           // rows of a tile: (token, query head) pairs, head fastest
+    int32_t tiles;          // tiles of a unit
+    int32_t heads;          // query heads of a tile: min(group, rows)
+    int32_t tokens;         // tokens of a tile: rows / heads
+    int32_t sub_groups;     // ceil(group / heads)
+    int32_t keys;           // keys of a block
+    int32_t overhead;       // cost of a unit beside its key blocks
+    int32_t min_range;      // least cost of a CTA's range
+    int32_t fixed_cost;     // > 0: every unit counts as this much, one unit a CTA
+};
+
+struct TreeWork {
+    TreeShape s;
+    int64_t* header;        // [0] total cost, [1] range per CTA
+    int64_t* seq_cost;      // [num_seqs + 1] running sums (nullptr: no merge follows)
+    float* cells;           // [2 * CTAs]: acc [D / 4][rows * tiles][4], then (m, l) [rows * tiles][2]
+};
+
+__host__ __device__ inline size_t tree_cell_floats(const TreeShape& s, int32_t head_dim) {
+    return (size_t)s.rows * s.tiles * (head_dim + 2);
+}
+
+__device__ __forceinline__ int32_t tree_units(const TreeArgs& a, const TreeShape& s, int32_t n) {
+    const int32_t per = s.tokens * s.tiles;
+    return n > 0 ? a.num_kv_heads * s.sub_groups * ((n + per - 1) / per) : 0;
+}
+
+__device__ __forceinline__ int32_t tree_cost(const TreeShape& s, int32_t T) {
+    return s.fixed_cost > 0 ? s.fixed_cost : (T + s.keys - 1) / s.keys + s.overhead;
+}
+
+// One unit's part within a CTA's range.
+struct TreeSeg {
+    int32_t i, q0, n, T, C;         // sequence, its rows, lengths (C: cached tokens)
+    int32_t g, sg;                  // kv head, sub-group
+    int32_t tok0, ntok;             // tokens (nodes) tok0 .. tok0 + ntok - 1
+    int32_t kb0, kb1, nb;           // key blocks of this part, of the unit
+};
+
+// Position in the cost line.
+struct TreeIter {
+    int64_t pos, end, seq0;         // next cost, range end, cost before sequence i
+    int32_t i;
+};
+
+// The next part of the range; false at its end.  Uniform over the threads
+// that call it with equal state.
+__device__ __forceinline__ bool tree_next(const TreeArgs& a, const TreeShape& sh, TreeIter& it,
+                                          TreeSeg& o) {
+    while (it.pos < it.end) {
+        const TreeSeq s = tree_seq(a, it.i, false);
+        const int32_t units = tree_units(a, sh, s.n);
+        const int32_t cost = tree_cost(sh, s.T);
+        const int64_t seq1 = it.seq0 + (int64_t)units * cost;
+        if (it.pos >= seq1) {
+            it.seq0 = seq1;
+            if (++it.i >= a.num_seqs) return false;
+            continue;
+        }
+        const int32_t u = (int32_t)((it.pos - it.seq0) / cost);
+        const int64_t u0 = it.seq0 + (int64_t)u * cost;
+        const int64_t stop = min(it.end, u0 + cost);
+        const int32_t from = (int32_t)(it.pos - u0), to = (int32_t)(stop - u0);
+        it.pos = stop;
+        o.nb = (s.T + sh.keys - 1) / sh.keys;
+        o.kb0 = min(o.nb, max(0, from - sh.overhead));
+        o.kb1 = min(o.nb, max(0, to - sh.overhead));
+        if (o.kb0 >= o.kb1) continue;
+        const int32_t per = sh.tokens * sh.tiles, tiles = (s.n + per - 1) / per;
+        const int32_t tile = u % tiles, hs = u / tiles;
+        o.i = it.i;
+        o.q0 = s.q0;
+        o.n = s.n;
+        o.T = s.T;
+        o.C = s.T - s.n;
+        o.g = hs / sh.sub_groups;
+        o.sg = hs - o.g * sh.sub_groups;
+        o.tok0 = tile * per;
+        o.ntok = min(per, s.n - o.tok0);
+        return true;
+    }
+    return false;
+}
+
+// This CTA's range: all threads of the block, `scratch` holding 2 + threads /
+// 32 values.  Every CTA sums the batch's costs; CTA 0 reports refused
+// sequences and writes the running sums for the merge.
+__device__ __forceinline__ TreeIter tree_begin(const TreeArgs& a, const TreeWork& w,
+                                               int64_t* scratch) {
+    const int32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t threads = blockDim.x, warps = threads / 32;
+    const int32_t chunk = (a.num_seqs + threads - 1) / threads;
+    const int32_t i0 = min(a.num_seqs, tid * chunk), i1 = min(a.num_seqs, i0 + chunk);
+    const bool first = blockIdx.x == 0;
+    int64_t sum = 0;
+    for (int32_t i = i0; i < i1; ++i) {
+        const TreeSeq s = tree_seq(a, i, first);
+        sum += (int64_t)tree_units(a, w.s, s.n) * tree_cost(w.s, s.T);
+    }
+    int64_t incl = sum;
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += x;
+    }
+    if (lane == 31) scratch[2 + warp] = incl;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int32_t x = 0; x < warps; ++x) {
+        const int64_t v = scratch[2 + x];
+        if (x < warp) before += v;
+        total += v;
+    }
+    int64_t at = before + incl - sum;           // cost before sequence i0
+    const int64_t range = w.s.fixed_cost > 0
+                              ? (int64_t)w.s.fixed_cost
+                              : max((total + gridDim.x - 1) / gridDim.x, (int64_t)w.s.min_range);
+    TreeIter it;
+    it.pos = min(total, range * blockIdx.x);
+    it.end = min(total, it.pos + range);
+    if (tid == 0) {
+        scratch[0] = 0;                         // read for an empty range only
+        scratch[1] = 0;
+        if (first && w.seq_cost != nullptr) {
+            w.header[0] = total;
+            w.header[1] = range;
+            w.seq_cost[a.num_seqs] = total;
+        }
+    }
+    __syncthreads();
+    // the thread whose sequences hold the range's start names the sequence
+    const bool mine = at <= it.pos && it.pos < at + sum;
+    if (mine || (first && w.seq_cost != nullptr)) {
+        for (int32_t i = i0; i < i1; ++i) {
+            const TreeSeq s = tree_seq(a, i, false);
+            const int64_t c = (int64_t)tree_units(a, w.s, s.n) * tree_cost(w.s, s.T);
+            if (first && w.seq_cost != nullptr) w.seq_cost[i] = at;
+            if (at <= it.pos && it.pos < at + c) {
+                scratch[0] = i;
+                scratch[1] = at;
+            }
+            at += c;
+        }
+    }
+    __syncthreads();
+    it.i = (int32_t)scratch[0];
+    it.seq0 = scratch[1];
+    return it;
+}
+
+// The cell of this CTA's part.
+__device__ __forceinline__ float* tree_cell(const TreeArgs& a, const TreeWork& w, const TreeSeg& s) {
+    return w.cells + (2 * (size_t)blockIdx.x + (s.kb0 == 0 ? 1 : 0)) * tree_cell_floats(w.s, a.head_dim);
+}
+
+// Joins the parts of the unit that range blockIdx.x starts and does not end.
+// A thread takes one row and eight columns at a time, lanes along the rows.
+constexpr int kTreeMergeThreads = 256;
+
+template <typename E>
+__global__ void __launch_bounds__(kTreeMergeThreads)
+tree_merge_kernel(const TreeArgs a, const TreeWork w) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const TreeShape& sh = w.s;
+    const int64_t total = w.header[0], range = w.header[1];
+    const int64_t x = range * ((int64_t)blockIdx.x + 1);       // where range blockIdx.x ends
+    if (x >= total) return;
+    int32_t lo = 0, hi = a.num_seqs - 1;                       // last i with seq_cost[i] <= x
+    while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) / 2;
+        if (w.seq_cost[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    const TreeSeq s = tree_seq(a, lo, false);
+    const int32_t cost = tree_cost(sh, s.T);
+    const int64_t seq0 = w.seq_cost[lo];
+    const int32_t u = (int32_t)((x - seq0) / cost);
+    const int64_t u0 = seq0 + (int64_t)u * cost;
+    const int64_t c0 = (u0 + sh.overhead) / range, c1 = (u0 + cost - 1) / range;
+    if (c0 != blockIdx.x || c1 == c0) return;
+    const int32_t per = sh.tokens * sh.tiles, tiles = (s.n + per - 1) / per;
+    const int32_t tile = u % tiles, hs = u / tiles;
+    const int32_t g = hs / sh.sub_groups, sg = hs - g * sh.sub_groups;
+    const int32_t tok0 = tile * per, ntok = min(per, s.n - tok0);
+    const int32_t heads = min(sh.heads, a.group - sg * sh.heads);
+    const int32_t D = a.head_dim, urows = sh.rows * sh.tiles;
+    const int32_t live = ntok <= sh.tokens ? sh.rows : urows;
+    const int32_t groups = (D + 7) / 8;
+    const size_t cell = tree_cell_floats(sh, D);
+    const float* first = w.cells + (2 * (size_t)c0 + 1) * cell;
+    const float* next = w.cells + 2 * (size_t)(c0 + 1) * cell;  // cell 0 of the CTAs behind
+    const int32_t parts = (int32_t)(c1 - c0);
+    E* out = static_cast<E*>(a.out);
+    for (int32_t at = blockIdx.y * kTreeMergeThreads + threadIdx.x; at < live * groups;
+         at += gridDim.y * kTreeMergeThreads) {
+        const int32_t row = at % live, col = (at / live) * 8;
+        const int32_t t = row / sh.rows, r = row - t * sh.rows;
+        const int32_t tok = t * sh.tokens + r / sh.heads, h = r % sh.heads;
+        if (r / sh.heads >= sh.tokens || tok >= ntok || h >= heads) continue;
+        const size_t ml = (size_t)D * urows + 2 * (size_t)row;
+        float M = first[ml];
+#pragma unroll 4
+        for (int32_t p = 0; p < parts; ++p) M = fmaxf(M, next[p * 2 * cell + ml]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float l = 0.f, o[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) o[c] = 0.f;
+        const bool wide = col + 4 < D;
+#pragma unroll 4
+        for (int32_t p = -1; p < parts; ++p) {
+            const float* c = p < 0 ? first : next + p * 2 * cell;
+            const float2 v = *reinterpret_cast<const float2*>(c + ml);
+            const float4 x0 = *reinterpret_cast<const float4*>(c + ((size_t)(col / 4) * urows + row) * 4);
+            float4 x1 = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (wide) x1 = *reinterpret_cast<const float4*>(c + ((size_t)(col / 4 + 1) * urows + row) * 4);
+            const float wp = exp2f(v.x - ref);                 // 0 for a part without visible keys
+            l += wp * v.y;
+            const float xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+            // (an infinite sum stays one under a weight that underflows)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] += fabsf(xs[e]) <= 3.4028235e38f ? wp * xs[e] : xs[e];
+        }
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        E* dst = out + ((int64_t)(s.q0 + tok0 + tok) * a.num_q_heads + (int64_t)g * a.group +
+                        sg * sh.heads + h) * D + col;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) o[c] *= inv;
+        if constexpr (sizeof(E) == 2) {
+            // rows are whole 8-byte pieces: the kernels with parts take head
+            // dims that are multiples of 4
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+            if (wide)
+                *reinterpret_cast<uint2*>(dst + 4) =
+                    make_uint2(pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+        } else {
+            *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+            if (wide) *reinterpret_cast<float4*>(dst + 4) = make_float4(o[4], o[5], o[6], o[7]);
+        }
+    }
+}
+
+}  // namespace pa
