@@ -43,10 +43,14 @@ pa_status plan_impl(PlanArgs a, cudaStream_t st) {
 
 // ---- tree attention: kernel choice, work division, workspace ---------------------
 
-// Rows of a TMA box of the tcgen05 tree kernel: a box lies inside one block,
-// and 8 rows are one 128-byte swizzle atom.
+// Rows of one copy of the tcgen05 tree kernel: it lies inside one block and
+// takes whole 8-row groups (a 128-byte swizzle atom); 0: the block size is
+// not a multiple of 8.
 int32_t tree_box_rows(int32_t block_size) {
-    return block_size % 16 == 0 ? 16 : block_size % 8 == 0 ? 8 : 0;
+    if (block_size % 8 != 0) return 0;
+    int32_t rows = 8;
+    while (rows < 128 && block_size % (2 * rows) == 0) rows *= 2;
+    return rows;
 }
 
 // The tcgen05 kernel's shapes: bf16, head dims that are multiples of 16 up to
@@ -82,24 +86,30 @@ int32_t tree_ctas(const TreeShape& s, int32_t num_seqs, int32_t max_q_len, int32
         1, std::min<int64_t>(ctas, (int64_t)std::max(1, device_sm_count()) * per_sm));
 }
 
-size_t tree_workspace(const TreeShape& s, int32_t ctas, int32_t num_seqs, int32_t head_dim) {
-    return 256 + align256(((size_t)num_seqs + 1) * 8) +
+size_t tree_workspace(const TreeShape& s, int32_t ctas, int32_t head_dim) {
+    return align256((size_t)ctas * sizeof(TreeCut)) +
            align256(2 * (size_t)ctas * tree_cell_floats(s, head_dim) * 4);
 }
 
 TreeShape tree_ws_tiling(int32_t group) { return tree_shape(128, 2, 128, group); }
 
-// As encode_cache_map, with boxes of `rows` rows.
+// Cache viewed as 5-D: (64 columns, 8 rows, 64-column halves, 8-row groups of
+// a block, num_blocks * Hkv); one box is `rows` rows of one (block, head) tile,
+// swizzled 128 B.  Head dims other than 64 and 128 have all their columns in
+// the first dimension and one "half" (a box takes 64 of the columns; those past
+// the head dim are filled with zeros).
 bool encode_tree_map(CUtensorMap* map, const void* base, const pa_cache_desc* c, int32_t rows) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->block_size,
+    const cuuint64_t halves = c->head_dim == 128 ? 2 : 1;
+    const cuuint64_t row = (cuuint64_t)c->head_dim * 2;
+    cuuint64_t dims[5] = {(cuuint64_t)c->head_dim / halves, 8, halves, (cuuint64_t)c->block_size / 8,
                           (cuuint64_t)c->num_blocks * (cuuint64_t)c->num_kv_heads};
-    cuuint64_t strides[2] = {(cuuint64_t)c->head_dim * 2,
-                             (cuuint64_t)c->head_dim * 2 * (cuuint64_t)c->block_size};
-    cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+    cuuint64_t strides[4] = {row, 128, 8 * row, row * (cuuint64_t)c->block_size};
+    if (halves == 1) strides[1] = row;               // one entry: any multiple of 16
+    cuuint32_t box[5] = {64, 8, (cuuint32_t)halves, (cuuint32_t)rows / 8, 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides,
               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
@@ -121,11 +131,9 @@ cudaError_t launch_tree_ws(const TreeArgs& a, const TreeWork& w, const pa_cache_
 
 template <typename E>
 cudaError_t launch_tree_merge(const TreeArgs& a, const TreeWork& w, int32_t ctas, cudaStream_t st) {
-    if (ctas == 1) return cudaSuccess;
-    // one round of a thread per (row, eight columns) of the largest unit
-    const int32_t items = w.s.rows * w.s.tiles * ((a.head_dim + 7) / 8);
-    return launch_pdl(tree_merge_kernel<E>,
-                      dim3(ctas - 1, (items + kTreeMergeThreads - 1) / kTreeMergeThreads),
+    if (w.cuts == nullptr || ctas == 1) return cudaSuccess;
+    // (the last CTA's range ends with the work)
+    return launch_pdl(tree_merge_kernel<E>, dim3(ctas - 1, kTreeMergeSplit),
                       dim3(kTreeMergeThreads), 0, st, a, w);
 }
 
@@ -209,7 +217,7 @@ size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t total_q, int32_t
     if (!tree_ws_shape(cache)) return 0;
     const TreeShape s = tree_ws_tiling(num_q_heads / cache->num_kv_heads);
     const int32_t ctas = tree_ctas(s, num_seqs, max_q_len, max_seq_len, cache->num_kv_heads, 1);
-    return tree_workspace(s, ctas, num_seqs, cache->head_dim);
+    return tree_workspace(s, ctas, cache->head_dim);
 }
 
 pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const int32_t* parents,
@@ -274,17 +282,17 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
     a.group = num_q_heads / cache->num_kv_heads;
     a.head_dim = cache->head_dim;
     a.scale_log2 = scale * kLog2e;
-    // the tcgen05 kernel takes a row's maximum before it scales: scale >= 0
+    // the tcgen05 kernel takes a row's maximum before it scales, and masks with
+    // -inf: scale > 0
     const bool ws = tree_ws_shape(cache) && aligned(q, 16) && aligned(out, 16) &&
-                    aligned(k_cache, 16) && aligned(v_cache, 16) && scale >= 0.f;
+                    aligned(k_cache, 16) && aligned(v_cache, 16) && scale > 0.f;
     if (ws) {
         TreeWork w{};
         w.s = tree_ws_tiling(a.group);
         const int32_t ctas = tree_ctas(w.s, num_seqs, max_q_len, max_seq_len, a.num_kv_heads, 1);
         uint8_t* base = static_cast<uint8_t*>(workspace);
-        w.header = reinterpret_cast<int64_t*>(base);
-        w.seq_cost = reinterpret_cast<int64_t*>(base + 256);
-        w.cells = reinterpret_cast<float*>(base + 256 + align256(((size_t)num_seqs + 1) * 8));
+        w.cuts = reinterpret_cast<TreeCut*>(base);
+        w.cells = reinterpret_cast<float*>(base + align256((size_t)ctas * sizeof(TreeCut)));
         cudaError_t err = cache->head_dim > 64 ? launch_tree_ws<128>(a, w, cache, ctas, st)
                                                : launch_tree_ws<64>(a, w, cache, ctas, st);
         if (err == cudaSuccess) err = launch_tree_merge<__nv_bfloat16>(a, w, ctas, st);

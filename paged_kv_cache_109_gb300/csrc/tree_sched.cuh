@@ -32,10 +32,16 @@ struct TreeShape {
     int32_t fixed_cost;     // > 0: every unit counts as this much, one unit a CTA
 };
 
+// A unit cut by the end of a CTA's range, for the merge: written by the CTA
+// that starts it.  parts: the CTAs behind that hold the rest (0: none).
+struct TreeCut {
+    int32_t row0, ntok, g, sg;      // packed row of its first token, tokens, heads
+    int32_t parts, pad[3];
+};
+
 struct TreeWork {
     TreeShape s;
-    int64_t* header;        // [0] total cost, [1] range per CTA
-    int64_t* seq_cost;      // [num_seqs + 1] running sums (nullptr: no merge follows)
+    TreeCut* cuts;          // [CTAs] (nullptr: no unit can be cut, no merge follows)
     float* cells;           // [2 * CTAs]: acc [D / 4][rows * tiles][4], then (m, l) [rows * tiles][2]
 };
 
@@ -58,11 +64,14 @@ struct TreeSeg {
     int32_t g, sg;                  // kv head, sub-group
     int32_t tok0, ntok;             // tokens (nodes) tok0 .. tok0 + ntok - 1
     int32_t kb0, kb1, nb;           // key blocks of this part, of the unit
+    int32_t parts;                  // of a unit that starts here: the CTAs behind with the rest
+    int32_t pad[3];
 };
 
 // Position in the cost line.
 struct TreeIter {
     int64_t pos, end, seq0;         // next cost, range end, cost before sequence i
+    int64_t range;                  // cost of a CTA's range
     int32_t i;
 };
 
@@ -72,6 +81,7 @@ __device__ __forceinline__ bool tree_next(const TreeArgs& a, const TreeShape& sh
                                           TreeSeg& o) {
     while (it.pos < it.end) {
         const TreeSeq s = tree_seq(a, it.i, false);
+        // (a sequence's cost stays in 32 bits: the launch refuses others)
         const int32_t units = tree_units(a, sh, s.n);
         const int32_t cost = tree_cost(sh, s.T);
         const int64_t seq1 = it.seq0 + (int64_t)units * cost;
@@ -80,23 +90,24 @@ __device__ __forceinline__ bool tree_next(const TreeArgs& a, const TreeShape& sh
             if (++it.i >= a.num_seqs) return false;
             continue;
         }
-        const int32_t u = (int32_t)((it.pos - it.seq0) / cost);
-        const int64_t u0 = it.seq0 + (int64_t)u * cost;
-        const int64_t stop = min(it.end, u0 + cost);
-        const int32_t from = (int32_t)(it.pos - u0), to = (int32_t)(stop - u0);
-        it.pos = stop;
+        const int32_t at = (int32_t)(it.pos - it.seq0);
+        const int32_t u = at / cost, from = at - u * cost;
+        const int32_t to = (int32_t)min((int64_t)cost, from + (it.end - it.pos));
+        it.pos += to - from;
         o.nb = (s.T + sh.keys - 1) / sh.keys;
         o.kb0 = min(o.nb, max(0, from - sh.overhead));
         o.kb1 = min(o.nb, max(0, to - sh.overhead));
         if (o.kb0 >= o.kb1) continue;
+        const int32_t left = cost - to;           // of the unit, behind this range
+        o.parts = left > 0 ? (int32_t)((left + it.range - 1) / it.range) : 0;
         const int32_t per = sh.tokens * sh.tiles, tiles = (s.n + per - 1) / per;
-        const int32_t tile = u % tiles, hs = u / tiles;
+        const int32_t hs = tiles == 1 ? u : u / tiles, tile = u - hs * tiles;
         o.i = it.i;
         o.q0 = s.q0;
         o.n = s.n;
         o.T = s.T;
         o.C = s.T - s.n;
-        o.g = hs / sh.sub_groups;
+        o.g = sh.sub_groups == 1 ? hs : hs / sh.sub_groups;
         o.sg = hs - o.g * sh.sub_groups;
         o.tok0 = tile * per;
         o.ntok = min(per, s.n - o.tok0);
@@ -107,25 +118,29 @@ __device__ __forceinline__ bool tree_next(const TreeArgs& a, const TreeShape& sh
 
 // This CTA's range: all threads of the block, `scratch` holding 2 + threads /
 // 32 values.  Every CTA sums the batch's costs; CTA 0 reports refused
-// sequences and writes the running sums for the merge.
+// sequences.
 __device__ __forceinline__ TreeIter tree_begin(const TreeArgs& a, const TreeWork& w,
                                                int64_t* scratch) {
     const int32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t threads = blockDim.x, warps = threads / 32;
     const int32_t chunk = (a.num_seqs + threads - 1) / threads;
     const int32_t i0 = min(a.num_seqs, tid * chunk), i1 = min(a.num_seqs, i0 + chunk);
-    const bool first = blockIdx.x == 0;
     int64_t sum = 0;
     for (int32_t i = i0; i < i1; ++i) {
-        const TreeSeq s = tree_seq(a, i, first);
+        const TreeSeq s = tree_seq(a, i, blockIdx.x == 0);
         sum += (int64_t)tree_units(a, w.s, s.n) * tree_cost(w.s, s.T);
     }
     int64_t incl = sum;
+#pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += x;
     }
     if (lane == 31) scratch[2 + warp] = incl;
+    if (tid == 0) {
+        scratch[0] = 0;                         // read for an empty range only
+        scratch[1] = 0;
+    }
     __syncthreads();
     int64_t before = 0, total = 0;
     for (int32_t x = 0; x < warps; ++x) {
@@ -134,35 +149,26 @@ __device__ __forceinline__ TreeIter tree_begin(const TreeArgs& a, const TreeWork
         total += v;
     }
     int64_t at = before + incl - sum;           // cost before sequence i0
-    const int64_t range = w.s.fixed_cost > 0
-                              ? (int64_t)w.s.fixed_cost
-                              : max((total + gridDim.x - 1) / gridDim.x, (int64_t)w.s.min_range);
+    const uint32_t ctas = gridDim.x;
     TreeIter it;
-    it.pos = min(total, range * blockIdx.x);
-    it.end = min(total, it.pos + range);
-    if (tid == 0) {
-        scratch[0] = 0;                         // read for an empty range only
-        scratch[1] = 0;
-        if (first && w.seq_cost != nullptr) {
-            w.header[0] = total;
-            w.header[1] = range;
-            w.seq_cost[a.num_seqs] = total;
-        }
-    }
-    __syncthreads();
+    it.range = total <= 0x7fffffff ? (int64_t)(((uint32_t)total + ctas - 1) / ctas)
+                                   : (total + ctas - 1) / ctas;
+    it.range = w.s.fixed_cost > 0 ? (int64_t)w.s.fixed_cost : max(it.range, (int64_t)w.s.min_range);
+    it.pos = min(total, it.range * blockIdx.x);
+    it.end = min(total, it.pos + it.range);
     // the thread whose sequences hold the range's start names the sequence
-    const bool mine = at <= it.pos && it.pos < at + sum;
-    if (mine || (first && w.seq_cost != nullptr)) {
-        for (int32_t i = i0; i < i1; ++i) {
-            const TreeSeq s = tree_seq(a, i, false);
-            const int64_t c = (int64_t)tree_units(a, w.s, s.n) * tree_cost(w.s, s.T);
-            if (first && w.seq_cost != nullptr) w.seq_cost[i] = at;
-            if (at <= it.pos && it.pos < at + c) {
-                scratch[0] = i;
-                scratch[1] = at;
+    if (at <= it.pos && it.pos < at + sum) {
+        int32_t i = i0;
+        if (chunk > 1) {
+            for (;; ++i) {
+                const TreeSeq s = tree_seq(a, i, false);
+                const int64_t c = (int64_t)tree_units(a, w.s, s.n) * tree_cost(w.s, s.T);
+                if (it.pos < at + c) break;
+                at += c;
             }
-            at += c;
         }
+        scratch[0] = i;
+        scratch[1] = at;
     }
     __syncthreads();
     it.i = (int32_t)scratch[0];
@@ -175,9 +181,11 @@ __device__ __forceinline__ float* tree_cell(const TreeArgs& a, const TreeWork& w
     return w.cells + (2 * (size_t)blockIdx.x + (s.kb0 == 0 ? 1 : 0)) * tree_cell_floats(w.s, a.head_dim);
 }
 
-// Joins the parts of the unit that range blockIdx.x starts and does not end.
-// A thread takes one row and eight columns at a time, lanes along the rows.
+// Joins the parts of the unit that CTA blockIdx.x of the attention kernel
+// starts and does not end.  A thread takes one row and eight columns at a
+// time, lanes along the rows.
 constexpr int kTreeMergeThreads = 256;
+constexpr int kTreeMergeSplit = 8;      // CTAs per cut
 
 template <typename E>
 __global__ void __launch_bounds__(kTreeMergeThreads)
@@ -185,51 +193,33 @@ tree_merge_kernel(const TreeArgs a, const TreeWork w) {
     griddep_wait();
     griddep_launch_dependents();
     const TreeShape& sh = w.s;
-    const int64_t total = w.header[0], range = w.header[1];
-    const int64_t x = range * ((int64_t)blockIdx.x + 1);       // where range blockIdx.x ends
-    if (x >= total) return;
-    int32_t lo = 0, hi = a.num_seqs - 1;                       // last i with seq_cost[i] <= x
-    while (lo < hi) {
-        const int32_t mid = (lo + hi + 1) / 2;
-        if (w.seq_cost[mid] <= x) lo = mid; else hi = mid - 1;
-    }
-    const TreeSeq s = tree_seq(a, lo, false);
-    const int32_t cost = tree_cost(sh, s.T);
-    const int64_t seq0 = w.seq_cost[lo];
-    const int32_t u = (int32_t)((x - seq0) / cost);
-    const int64_t u0 = seq0 + (int64_t)u * cost;
-    const int64_t c0 = (u0 + sh.overhead) / range, c1 = (u0 + cost - 1) / range;
-    if (c0 != blockIdx.x || c1 == c0) return;
-    const int32_t per = sh.tokens * sh.tiles, tiles = (s.n + per - 1) / per;
-    const int32_t tile = u % tiles, hs = u / tiles;
-    const int32_t g = hs / sh.sub_groups, sg = hs - g * sh.sub_groups;
-    const int32_t tok0 = tile * per, ntok = min(per, s.n - tok0);
-    const int32_t heads = min(sh.heads, a.group - sg * sh.heads);
+    const TreeCut cut = w.cuts[blockIdx.x];
+    if (cut.parts == 0) return;
+    const int32_t heads = min(sh.heads, a.group - cut.sg * sh.heads);
     const int32_t D = a.head_dim, urows = sh.rows * sh.tiles;
-    const int32_t live = ntok <= sh.tokens ? sh.rows : urows;
+    const int32_t live = cut.ntok <= sh.tokens ? cut.ntok * sh.heads : urows;
     const int32_t groups = (D + 7) / 8;
     const size_t cell = tree_cell_floats(sh, D);
-    const float* first = w.cells + (2 * (size_t)c0 + 1) * cell;
-    const float* next = w.cells + 2 * (size_t)(c0 + 1) * cell;  // cell 0 of the CTAs behind
-    const int32_t parts = (int32_t)(c1 - c0);
+    const float* first = w.cells + (2 * (size_t)blockIdx.x + 1) * cell;
+    const float* next = w.cells + 2 * ((size_t)blockIdx.x + 1) * cell;  // cell 0 of the CTAs behind
     E* out = static_cast<E*>(a.out);
     for (int32_t at = blockIdx.y * kTreeMergeThreads + threadIdx.x; at < live * groups;
          at += gridDim.y * kTreeMergeThreads) {
         const int32_t row = at % live, col = (at / live) * 8;
         const int32_t t = row / sh.rows, r = row - t * sh.rows;
-        const int32_t tok = t * sh.tokens + r / sh.heads, h = r % sh.heads;
-        if (r / sh.heads >= sh.tokens || tok >= ntok || h >= heads) continue;
+        const int32_t tk = r / sh.heads, h = r - tk * sh.heads, tok = t * sh.tokens + tk;
+        if (tk >= sh.tokens || tok >= cut.ntok || h >= heads) continue;
         const size_t ml = (size_t)D * urows + 2 * (size_t)row;
         float M = first[ml];
 #pragma unroll 4
-        for (int32_t p = 0; p < parts; ++p) M = fmaxf(M, next[p * 2 * cell + ml]);
+        for (int32_t p = 0; p < cut.parts; ++p) M = fmaxf(M, next[p * 2 * cell + ml]);
         const float ref = M == -INFINITY ? 0.f : M;
         float l = 0.f, o[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) o[c] = 0.f;
         const bool wide = col + 4 < D;
 #pragma unroll 4
-        for (int32_t p = -1; p < parts; ++p) {
+        for (int32_t p = -1; p < cut.parts; ++p) {
             const float* c = p < 0 ? first : next + p * 2 * cell;
             const float2 v = *reinterpret_cast<const float2*>(c + ml);
             const float4 x0 = *reinterpret_cast<const float4*>(c + ((size_t)(col / 4) * urows + row) * 4);
@@ -243,8 +233,8 @@ tree_merge_kernel(const TreeArgs a, const TreeWork w) {
             for (int e = 0; e < 8; ++e) o[e] += fabsf(xs[e]) <= 3.4028235e38f ? wp * xs[e] : xs[e];
         }
         const float inv = l != 0.f ? 1.f / l : 0.f;
-        E* dst = out + ((int64_t)(s.q0 + tok0 + tok) * a.num_q_heads + (int64_t)g * a.group +
-                        sg * sh.heads + h) * D + col;
+        E* dst = out + ((int64_t)(cut.row0 + tok) * a.num_q_heads + (int64_t)cut.g * a.group +
+                        cut.sg * sh.heads + h) * D + col;
 #pragma unroll
         for (int c = 0; c < 8; ++c) o[c] *= inv;
         if constexpr (sizeof(E) == 2) {
