@@ -115,18 +115,34 @@ bool encode_tree_map(CUtensorMap* map, const void* base, const pa_cache_desc* c,
            CUDA_SUCCESS;
 }
 
-template <int D>
+// Queries [total_q][Hq][D] as 3-D; one box is a tile's (token, head) rows, 64
+// columns of them.
+bool encode_tree_q(CUtensorMap* map, const TreeArgs& a, const TreeShape& s) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t row = (cuuint64_t)a.head_dim * 2;
+    cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.num_q_heads, (cuuint64_t)a.total_q};
+    cuuint64_t strides[2] = {row, row * (cuuint64_t)a.num_q_heads};
+    cuuint32_t box[3] = {64, (cuuint32_t)s.heads, (cuuint32_t)s.tokens};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+template <int D, bool SPLIT>
 cudaError_t launch_tree_ws(const TreeArgs& a, const TreeWork& w, const pa_cache_desc* c,
                            int32_t ctas, cudaStream_t st) {
     using Cfg = TreeWsCfg<D>;
     const int32_t rows = tree_box_rows(c->block_size);
-    CUtensorMap mk, mv;
-    if (!encode_tree_map(&mk, a.k_cache, c, rows) || !encode_tree_map(&mv, a.v_cache, c, rows))
+    CUtensorMap mq, mk, mv;
+    if (!encode_tree_q(&mq, a, w.s) || !encode_tree_map(&mk, a.k_cache, c, rows) || !encode_tree_map(&mv, a.v_cache, c, rows))
         return cudaErrorUnknown;
-    auto kern = tree_ws_kernel<D>;
+    auto kern = tree_ws_kernel<D, SPLIT>;
     if (!set_smem(kern, Cfg::smem_bytes())) return cudaErrorUnknown;
-    return launch_pdl(kern, dim3(ctas), dim3(Cfg::kThreads), Cfg::smem_bytes(), st, mk, mv, a, w,
-                      rows);
+    return launch_pdl(kern, dim3(ctas), dim3(Cfg::kThreads), Cfg::smem_bytes(), st, mq, mk, mv,
+                      a, w, rows);
 }
 
 template <typename E>
@@ -283,9 +299,9 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
     a.head_dim = cache->head_dim;
     a.scale_log2 = scale * kLog2e;
     // the tcgen05 kernel takes a row's maximum before it scales, and masks with
-    // -inf: scale > 0
-    const bool ws = tree_ws_shape(cache) && aligned(q, 16) && aligned(out, 16) &&
-                    aligned(k_cache, 16) && aligned(v_cache, 16) && scale > 0.f;
+    // -inf: scale > 0; its copies of q are TMA, from device memory
+    const bool ws = tree_ws_shape(cache) && aligned(q, 16) && current_device_memory(q) &&
+                    aligned(out, 16) && aligned(k_cache, 16) && aligned(v_cache, 16) && scale > 0.f;
     if (ws) {
         TreeWork w{};
         w.s = tree_ws_tiling(a.group);
@@ -293,8 +309,9 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
         uint8_t* base = static_cast<uint8_t*>(workspace);
         w.cuts = reinterpret_cast<TreeCut*>(base);
         w.cells = reinterpret_cast<float*>(base + align256((size_t)ctas * sizeof(TreeCut)));
-        cudaError_t err = cache->head_dim > 64 ? launch_tree_ws<128>(a, w, cache, ctas, st)
-                                               : launch_tree_ws<64>(a, w, cache, ctas, st);
+        cudaError_t err = cache->head_dim == 128 ? launch_tree_ws<128, false>(a, w, cache, ctas, st)
+                          : cache->head_dim > 64 ? launch_tree_ws<128, true>(a, w, cache, ctas, st)
+                                                 : launch_tree_ws<64, false>(a, w, cache, ctas, st);
         if (err == cudaSuccess) err = launch_tree_merge<__nv_bfloat16>(a, w, ctas, st);
         return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }

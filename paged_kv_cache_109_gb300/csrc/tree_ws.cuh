@@ -31,8 +31,7 @@
 //                   that do not see the node) and noted; the rows that do see
 //                   such a node add its values at the end.
 //   warp 10         the range's parts, handed to the other warps through a
-//                   short queue; Q (16-byte cp.async) and the nodes' parents
-//                   of the next part
+//                   short queue; Q (TMA) and the nodes' parents of the next part
 //
 // A copy of K or V covers up to a whole cache block and both 64-column halves:
 // the tensor map's dimensions are (64 columns, 8 rows, halves, groups of 8
@@ -53,7 +52,6 @@
 
 #include <type_traits>
 
-#include "cp_async.cuh"
 #include "tree_sched.cuh"
 
 namespace pa {
@@ -108,9 +106,11 @@ __device__ __forceinline__ uint32_t bf16x2_clean(uint32_t x) {
     return x;
 }
 
-template <int D>
+// SPLIT: head dims between 64 and 128 (D = 128), copied half by half.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(TreeWsCfg<D>::kThreads, 1)
-tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_k,
+tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
+               const __grid_constant__ CUtensorMap tmap_k,
                const __grid_constant__ CUtensorMap tmap_v, const TreeArgs a, const TreeWork w,
                const int32_t box_rows) {
     // box_rows: rows of a copy, a multiple of 8 that divides the block size
@@ -150,7 +150,7 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_init(o_half(t), 1);
             mbar_init(o_done(t), 1);
         }
-        mbar_init(q_full, 1);
+        mbar_init(q_full, 2);                             // the copies', the parents'
         mbar_init(q_free, 1);
         mbar_init(o_free, C::kSoftmaxWarps);
         mbar_init(ml_ready, C::kSoftmaxWarps);
@@ -163,6 +163,7 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
     if (warp == C::kKWarp && lane == 0) prefetch_tmap(&tmap_k);
     if (warp == C::kVWarp && lane == 0) prefetch_tmap(&tmap_v);
+    if (warp == C::kPlanWarp && lane == 0) prefetch_tmap(&tmap_q);
     if (warp == C::kMmaWarp) tmem_alloc(smem_u32(tslot), C::kTmemCols);
     griddep_wait();
     // (the ring is not in use yet: its start serves the range's search)
@@ -176,8 +177,7 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const int32_t G = a.group, BS = a.block_size, hd = a.head_dim;
     const int32_t HT = w.s.heads, tpt = w.s.tokens;
     // bytes from one 8-row group of K or V to the next, and between halves
-    const bool split = D == 128 && hd < 128;
-    const int32_t gs = split ? 1024 : C::kGroup, ho = split ? C::kKeys * 128 : 1024;
+    constexpr int32_t gs = SPLIT ? 1024 : C::kGroup, ho = SPLIT ? C::kKeys * 128 : 1024;
     // a bounded wait whose outcome is the same in every lane of the warp
     auto warp_wait = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitLimitCycles)) != 0;
@@ -256,7 +256,8 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (b0.has) {
                     const uint32_t dst = sm_u + C::kSlotOff + s * C::kItem + lane * box_step;
                     tma_load_5d(dst, map, 0, 0, 0, b0.row >> 3, z, kv_full(s));
-                    if (split) tma_load_5d(dst + ho, map, 64, 0, 0, b0.row >> 3, z, kv_full(s));
+                    if constexpr (SPLIT)
+                        tma_load_5d(dst + ho, map, 64, 0, 0, b0.row >> 3, z, kv_full(s));
                 }
                 if (lane == s) mine = item;
                 b0 = b1;
@@ -334,7 +335,7 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const uint32_t s_t = tmem + t * C::kTileCols;
                     if (has_v) {
                         const bool fresh = x < (lag == 1 ? 2 : 4);   // O's first block
-#pragma unroll 1
+#pragma unroll
                         for (int32_t hf = 0; hf < 2; ++hf) {
                             if (!warp_wait(hf ? p_full(t) : p_half(t), done[t] & 1)) {
                                 ok = false;
@@ -344,12 +345,16 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             if (leader) {
                                 // half hf: hi at columns 64 hf .. 64 hf + 31,
                                 // lo at the next 32; 16 keys = 8 columns per step
-                                const int32_t steps = min(4, (vkeys - hf * 64 + 15) >> 4);
+                                // (unrolled: descriptors from a loop's counter
+                                // take 130 cycles an instruction)
+#pragma unroll
                                 for (int32_t lo = 0; lo < 2; ++lo)
-                                    for (int32_t k = 0; k < steps; ++k)
-                                        umma_bf16_ts(s_t + C::kOCol, s_t + hf * 64 + lo * 32 + k * 8,
-                                                     vdesc + (uint64_t)((hf * 4 + k) * (gs >> 3)), kIdO,
-                                                     (!fresh || hf > 0 || lo > 0 || k > 0) ? 1u : 0u);
+#pragma unroll
+                                    for (int32_t k = 0; k < 4; ++k)
+                                        if ((hf * 4 + k) * 16 < vkeys)
+                                            umma_bf16_ts(s_t + C::kOCol, s_t + hf * 64 + lo * 32 + k * 8,
+                                                         vdesc + (uint64_t)((hf * 4 + k) * (gs >> 3)), kIdO,
+                                                         (!fresh || hf > 0 || lo > 0 || k > 0) ? 1u : 0u);
                                 umma_commit(hf ? o_done(t) : o_half(t));
                             }
                             __syncwarp();
@@ -361,10 +366,12 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         // S(x) = Q K(x)^T over the columns P(x - lag) occupied,
                         // k-steps of the head dim only
                         const uint64_t qdesc = qdesc0 + (uint64_t)(lag == 1 ? t * (C::kQTile >> 4) : 0);
-                        for (int32_t k = 0; k < hd / 16; ++k)
-                            umma_bf16(s_t, qdesc + (uint64_t)((k >> 2) * (C::kRows * 8) + (k & 3) * 2),
-                                      kdesc + (uint64_t)((k >> 2) * (ho >> 4) + (k & 3) * 2), kIdS,
-                                      k > 0 ? 1u : 0u);
+#pragma unroll
+                        for (int32_t k = 0; k < D / 16; ++k)
+                            if (k < hd / 16)
+                                umma_bf16(s_t, qdesc + (uint64_t)((k >> 2) * (C::kRows * 8) + (k & 3) * 2),
+                                          kdesc + (uint64_t)((k >> 2) * (ho >> 4) + (k & 3) * 2), kIdS,
+                                          k > 0 ? 1u : 0u);
                         umma_commit(s_full(t));
                     }
                     __syncwarp();
@@ -388,7 +395,6 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_k,
         if (!ok && lane == 0) raise_error(PA_DEVERR_TIMEOUT);
     } else if (warp == C::kPlanWarp) {
         // ---- the range's parts; Q and parents of each ------------------------
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
         TreeCut cut{};
         bool was_one = false, more = true;
         int32_t said = 0;                                 // parts announced
@@ -418,45 +424,32 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // output has been written
             if (ok && tiles == 2 && was_one) ok = warp_wait(o_free, (seg - 1) & 1);
             if (!ok) break;
-            // Rows in use only: an idle row's scores reach no other row.
-            // Consecutive lanes copy consecutive 16-byte pieces of a row.
-            const int32_t heads = min(HT, G - sg.sg * HT);
-            const int32_t per = hd / 8;                   // pieces of a row
-            const int32_t c = lane & (D / 8 - 1);
-            int32_t r = lane / (D / 8), tk = r / HT, head = r - tk * HT;
-            const __nv_bfloat16* src = q + ((int64_t)(sg.q0 + sg.tok0) * a.num_q_heads +
-                                            (int64_t)sg.g * G + sg.sg * HT) * hd + c * 8;
-            const uint32_t dst = sm_u + (c >> 3) * (C::kRows * 128);
-            for (int32_t tok0 = 0; tok0 < sg.ntok; tok0 += tpt) {
-                const int32_t nt = min(tpt, sg.ntok - tok0);
-                const uint32_t base = dst + (tok0 > 0 ? C::kQTile : 0);
-                int32_t rr = r, k = tk, h = head;
-#pragma unroll 4
-                for (; k < nt; rr += 256 / D) {
-                    if (c < per && h < heads)
-                        cp_async16(base + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
-                                   src + ((int64_t)(tok0 + k) * a.num_q_heads + h) * hd, 16u);
-                    h += 256 / D;
-                    while (h >= HT) {
-                        h -= HT;
-                        ++k;
-                    }
-                }
+            // Q: a copy per tile and half of `tokens` x `heads` rows in place.  Rows
+            // behind the part's last node (or head) hold whatever comes there:
+            // a row's scores reach no other row.
+            const uint32_t q_bytes = (uint32_t)(tpt * HT) * 128u * C::kHalves * tiles;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(q_full, q_bytes);
+                for (int32_t t = 0; t < tiles; ++t)
+                    for (int32_t h = 0; h < C::kHalves; ++h)
+                        tma_load_3d(sm_u + t * C::kQTile + h * (C::kRows * 128), &tmap_q, h * 64,
+                                    sg.g * G + sg.sg * HT, sg.q0 + sg.tok0 + t * tpt, q_full);
             }
             for (int32_t j = lane; j < sg.n; j += 32) {
                 const int32_t p = tree_parent(a.parents[sg.q0 + j], j, true);
                 parents[(seg % C::kBufs) * PA_MAX_TREE_NODES + j] = (uint8_t)(p + 1);
             }
-            cp_async_commit();
-            cp_async_wait<0>();
-            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
+            if (lane == 0) mbar_arrive(q_full);           // the parents are there
             was_one = tiles == 1;
             ++seg;
         }
         if (w.cuts != nullptr && lane == 0) w.cuts[blockIdx.x] = cut;
-        if (!ok && lane == 0) raise_error(PA_DEVERR_TIMEOUT);
+        if (!ok) {
+            // (the MMA warp waits for every Q; after a failure this warp does)
+            if (seg > 0) mbar_wait_bounded(q_full, (seg - 1) & 1, kWaitLimitCycles);
+            if (lane == 0) raise_error(PA_DEVERR_TIMEOUT);
+        }
     } else {
         // ---- softmax of accumulator wg, lane r -------------------------------
         const int32_t wg = warp >> 2, r = tid & (C::kRows - 1);
