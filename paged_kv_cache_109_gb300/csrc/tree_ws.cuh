@@ -21,17 +21,18 @@
 //
 //   warps 0-3, 4-7  softmax of accumulator 0, 1: thread t owns tensor-memory
 //                   lane t (one row); output or workspace cells at the end
-//   warps 8, 11     producers of K and of V: block-table lookups, TMA copies
-//   warp 9          MMA issue: S = Q K^T, O += P V (P from tensor memory as
-//                   two bf16 parts, hi + lo: about 16 significant bits of each
-//                   weight, as in the prefill kernel).  Before a block's V is
-//                   used that not every row may see (tree nodes, rows behind
-//                   the last key): rows behind are cleared, and values that
+//   warps 8, 10     producers of K and of V: block-table lookups, TMA copies.
+//                   The K warp walks the range and hands its parts to the
+//                   other warps through a short queue, with Q (TMA) and the
+//                   nodes' parents.  The V warp checks the blocks that not
+//                   every row may see (tree nodes, rows behind the last key)
+//                   before their use: rows behind are cleared, and values that
 //                   are not finite are taken out (0 times NaN would reach rows
 //                   that do not see the node) and noted; the rows that do see
-//                   such a node add its values at the end.
-//   warp 10         the range's parts, handed to the other warps through a
-//                   short queue; Q (TMA) and the nodes' parents of the next part
+//                   such a node add its values at the end
+//   warp 9          MMA issue: S = Q K^T, O += P V (P from tensor memory as
+//                   two bf16 parts, hi + lo: about 16 significant bits of each
+//                   weight, as in the prefill kernel)
 //
 // A copy of K or V covers up to a whole cache block and both 64-column halves:
 // the tensor map's dimensions are (64 columns, 8 rows, halves, groups of 8
@@ -58,9 +59,9 @@ namespace pa {
 
 template <int D>
 struct TreeWsCfg {
-    static constexpr int kThreads = 384;
+    static constexpr int kThreads = 352;
     static constexpr int kSoftmaxWarps = 8;
-    static constexpr int kKWarp = 8, kMmaWarp = 9, kPlanWarp = 10, kVWarp = 11;
+    static constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10;
     static constexpr int kRows = 128;                     // rows per tile = tensor-memory lanes
     static constexpr int kKeys = 128;
     static constexpr int kHalves = D / 64;                // 64-column (128-byte) slices
@@ -72,10 +73,10 @@ struct TreeWsCfg {
     static constexpr int kExtra = 2000;                   // barriers and the small arrays below
     static constexpr int kSlots = (kSmemMax - 1024 - kExtra - kSlotOff) / kItem;
     static constexpr int kBarOff = kSlotOff + kSlots * kItem;
-    // K/V full, K/V empty; per accumulator S full, P half 0, P full, O half 0,
-    // O done; Q full, Q free, O free, (m, l) ready, final; queue full, empty
+    // K/V full, K/V empty; per accumulator S full, P full, O done; Q full, Q free,
+    // O free, (m, l) ready, V to check, V checked, final; queue full, empty
     static constexpr int kQueue = 4;                      // parts announced at once
-    static constexpr int kBars = 2 * kSlots + 15 + 2 * kQueue;
+    static constexpr int kBars = 2 * kSlots + 13 + 2 * kQueue;
     // parents (as parent + 1, a byte each) and flags of V rows with values taken
     // out, of the last four parts (a part's output is read while the part
     // behind it is under way)
@@ -95,6 +96,12 @@ struct TreeWsCfg {
     static_assert(kSlots >= 5, "ring");
     static_assert(sizeof(TreeSeg) % 16 == 0, "queue entries");
 };
+
+// A shared-memory matrix descriptor from its low word (start address, LBO) and
+// its high word (SBO, version, swizzle).
+__device__ __forceinline__ uint64_t umma_desc(uint32_t lo, uint32_t hi) {
+    return (uint64_t)hi << 32 | lo;
+}
 
 // Any of the two bf16 values not finite (exponent all ones).
 __device__ __forceinline__ bool bf16x2_odd(uint32_t x) {
@@ -124,14 +131,13 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
     auto kv_empty = [&](int32_t s) { return bar0 + 8u * (C::kSlots + s); };
     const uint32_t bar1 = bar0 + 8u * (2 * C::kSlots);
     auto s_full = [&](int32_t t) { return bar1 + 8u * t; };
-    auto p_half = [&](int32_t t) { return bar1 + 8u * (2 + t); };
-    auto p_full = [&](int32_t t) { return bar1 + 8u * (4 + t); };
-    auto o_half = [&](int32_t t) { return bar1 + 8u * (6 + t); };
-    auto o_done = [&](int32_t t) { return bar1 + 8u * (8 + t); };
-    const uint32_t q_full = bar1 + 8u * 10, q_free = bar1 + 8u * 11, o_free = bar1 + 8u * 12;
-    const uint32_t ml_ready = bar1 + 8u * 13, bar_fin = bar1 + 8u * 14;
-    auto seg_full = [&](int32_t s) { return bar1 + 8u * (15 + s); };
-    auto seg_empty = [&](int32_t s) { return bar1 + 8u * (15 + C::kQueue + s); };
+    auto p_full = [&](int32_t t) { return bar1 + 8u * (2 + t); };
+    auto o_done = [&](int32_t t) { return bar1 + 8u * (4 + t); };
+    const uint32_t q_full = bar1 + 8u * 6, q_free = bar1 + 8u * 7, o_free = bar1 + 8u * 8;
+    const uint32_t ml_ready = bar1 + 8u * 9, v_go = bar1 + 8u * 10, v_ok = bar1 + 8u * 11;
+    const uint32_t bar_fin = bar1 + 8u * 12;
+    auto seg_full = [&](int32_t s) { return bar1 + 8u * (13 + s); };
+    auto seg_empty = [&](int32_t s) { return bar1 + 8u * (13 + C::kQueue + s); };
     uint8_t* parents = sm + C::kParentOff;
     uint32_t* flags = reinterpret_cast<uint32_t*>(sm + C::kFlagOff);
     TreeSeg* queue = reinterpret_cast<TreeSeg*>(sm + C::kQueueOff);
@@ -145,25 +151,25 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
         for (int32_t t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
-            mbar_init(p_half(t), 4);                      // one arrival per softmax warp
-            mbar_init(p_full(t), 4);
-            mbar_init(o_half(t), 1);
+            mbar_init(p_full(t), 4);                      // one arrival per softmax warp
             mbar_init(o_done(t), 1);
         }
         mbar_init(q_full, 2);                             // the copies', the parents'
         mbar_init(q_free, 1);
         mbar_init(o_free, C::kSoftmaxWarps);
         mbar_init(ml_ready, C::kSoftmaxWarps);
+        mbar_init(v_go, 1);
+        mbar_init(v_ok, 1);
         mbar_init(bar_fin, 1);
         for (int32_t s = 0; s < C::kQueue; ++s) {
             mbar_init(seg_full(s), 1);
-            mbar_init(seg_empty(s), C::kSoftmaxWarps + 3);
+            mbar_init(seg_empty(s), C::kSoftmaxWarps + 2);
         }
         mbar_fence_init();
     }
     if (warp == C::kKWarp && lane == 0) prefetch_tmap(&tmap_k);
     if (warp == C::kVWarp && lane == 0) prefetch_tmap(&tmap_v);
-    if (warp == C::kPlanWarp && lane == 0) prefetch_tmap(&tmap_q);
+    if (warp == C::kMmaWarp && lane == 0) prefetch_tmap(&tmap_q);
     if (warp == C::kMmaWarp) tmem_alloc(smem_u32(tslot), C::kTmemCols);
     griddep_wait();
     // (the ring is not in use yet: its start serves the range's search)
@@ -213,8 +219,86 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const uint32_t box_bytes = (uint32_t)(box_rows / 8) * C::kGroup;
         const int32_t dcol = C::kKeys / BS, drow = C::kKeys - dcol * BS;
         int32_t mine = -1;                                // lane s: this warp's latest item in slot s
-        while (ok && next_part()) {
+        int32_t checked = 0;                              // V blocks checked so far
+        TreeCut cut{};
+        bool was_one = false;                             // the part before used one tile
+        // K's warp finds the parts and announces them (n = 0: there are no more)
+        auto announce = [&]() {
+            if (!tree_next(a, w.s, it, sg)) sg.n = 0;
+            const int32_t s = seg % C::kQueue;
+            if (seg >= C::kQueue) ok = warp_wait(seg_empty(s), ((seg / C::kQueue) - 1) & 1);
+            if (!ok) return false;
+            if (lane == 0) queue[s] = sg;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(seg_full(s));
+            if (sg.n > 0 && sg.kb0 == 0 && sg.parts > 0)
+                cut = TreeCut{sg.q0 + sg.tok0, sg.ntok, sg.g, sg.sg, sg.parts, {0, 0, 0}};
+            return sg.n > 0;
+        };
+        // Q: a copy per tile and half of `tokens` x `heads` rows in place (rows
+        // behind the part's last node or head hold whatever comes there: a
+        // row's scores reach no other row), and the nodes' parents.
+        auto load_q = [&]() {
+            const int32_t tiles = sg.ntok > tpt ? 2 : 1;
+            if (seg > 0) ok = warp_wait(q_free, (seg - 1) & 1);
+            // tile 1's rows hold the (m, l) of a part with one tile until its
+            // output has been written
+            if (ok && tiles == 2 && was_one) ok = warp_wait(o_free, (seg - 1) & 1);
+            if (!ok) return;
+            was_one = tiles == 1;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(q_full, (uint32_t)(tpt * HT) * 128u * C::kHalves * tiles);
+                for (int32_t t = 0; t < tiles; ++t)
+                    for (int32_t h = 0; h < C::kHalves; ++h)
+                        tma_load_3d(sm_u + t * C::kQTile + h * (C::kRows * 128), &tmap_q, h * 64,
+                                    sg.g * G + sg.sg * HT, sg.q0 + sg.tok0 + t * tpt, q_full);
+            }
+            for (int32_t j = lane; j < sg.n; j += 32) {
+                const int32_t p = tree_parent(a.parents[sg.q0 + j], j, true);
+                parents[(seg % C::kBufs) * PA_MAX_TREE_NODES + j] = (uint8_t)(p + 1);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);           // the parents are there
+        };
+        while (ok && (is_v ? next_part() : announce())) {
             const int32_t n = sg.kb1 - sg.kb0, lag = sg.ntok > tpt ? 1 : 2;
+            uint32_t* noted = flags + (seg % C::kBufs) * (PA_MAX_TREE_NODES / 32);
+            if (is_v && lane < PA_MAX_TREE_NODES / 32) noted[lane] = 0;
+            // V's block y, if it reaches past the cached tokens: rows of tree
+            // nodes, and rows behind the last key up to the end of its 16-key
+            // step (the later steps are left out)
+            auto check = [&](int32_t y) {
+                const int32_t key0 = (sg.kb0 + y) * C::kKeys;
+                if (!ok || y < 0 || key0 + C::kKeys <= sg.C) return;
+                // (the MMA warp says when the block is there)
+                if (!(ok = warp_wait(v_go, checked++ & 1))) return;
+                const int32_t vkeys = min(C::kKeys, sg.T - key0);
+                const int32_t r0 = max(0, sg.C - key0), r1 = (vkeys + 15) & ~15;
+                uint8_t* vt = sm + C::kSlotOff + (item0 + v_item(y, lag, n)) % C::kSlots * C::kItem;
+                for (int32_t p0 = r0 * 8 + lane; p0 < r1 * 8; p0 += 32) {
+                    const int32_t row = p0 >> 3;
+#pragma unroll
+                    for (int32_t h = 0; h < C::kHalves; ++h) {
+                        uint4* p = reinterpret_cast<uint4*>(vt + (row >> 3) * gs + h * ho +
+                                                            (p0 & 63) * 16);
+                        if (row >= vkeys) {
+                            *p = make_uint4(0u, 0u, 0u, 0u);
+                        } else {
+                            const uint4 v = *p;
+                            if (bf16x2_odd(v.x) || bf16x2_odd(v.y) || bf16x2_odd(v.z) ||
+                                bf16x2_odd(v.w)) {
+                                *p = make_uint4(bf16x2_clean(v.x), bf16x2_clean(v.y),
+                                                bf16x2_clean(v.z), bf16x2_clean(v.w));
+                                const int32_t node = key0 + row - sg.C;
+                                atomicOr(noted + (node >> 5), 1u << (node & 31));
+                            }
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_ok);
+            };
             const int32_t* table = a.block_tables + (int64_t)sg.i * a.max_blocks;
             // this lane's box of block x: its table entry (read two blocks ahead
             // of use) and its row in the block
@@ -262,121 +346,111 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 if (lane == s) mine = item;
                 b0 = b1;
                 b1 = b2;
+                // (one block behind the copies: a later copy may wait for a slot
+                // that this block's use frees)
+                if (is_v)
+                    check(x - 1);
+                else if (x == min(n - 1, 1))              // with the part's first keys under way
+                    load_q();
             }
+            if (is_v) check(n - 1);
             item0 += 2 * n;
             ++seg;
         }
         // every copy has landed before the CTA may end: the MMA warp waits for
         // each, and after a failure this warp does
+        if (!is_v && w.cuts != nullptr && lane == 0) w.cuts[blockIdx.x] = cut;
         if (!ok) {
             if (mine >= 0)
                 mbar_wait_bounded(kv_full(lane), (mine / C::kSlots) & 1, kWaitLimitCycles);
+            if (!is_v && seg > 0) mbar_wait_bounded(q_full, (seg - 1) & 1, kWaitLimitCycles);
             if (lane == 0) raise_error(PA_DEVERR_TIMEOUT);
         }
     } else if (warp == C::kMmaWarp) {
         // ---- MMA issue -----------------------------------------------------
         constexpr uint32_t kIdS = umma_idesc_bf16(128, C::kKeys, 0);
         const uint32_t kIdO = umma_idesc_bf16(128, hd, 1);   // the head dim's columns only
-        const uint64_t qdesc0 = umma_sdesc(sm_u, 16, 1024, 2);
+        // Descriptors as two words: a k-step adds its offset / 16 to the low one
+        // (addresses stay below 2^18, so the field never carries), the high
+        // one is a constant.
+        constexpr uint32_t kQHi = (uint32_t)(1024 >> 4) | 1u << 14 | 2u << 29;
+        constexpr uint32_t kKvHi = (uint32_t)(gs >> 4) | 1u << 14 | 2u << 29;
+        constexpr uint32_t kKLbo = 1u << 16, kVLbo = (uint32_t)(ho >> 4) << 16;   // (K: not used)
+        const uint32_t q_lo = sm_u >> 4 | kKLbo;
+        const uint32_t slot_lo = (sm_u + C::kSlotOff) >> 4;
         const bool leader = elect_one();
-        int32_t done[2] = {0, 0};                         // P V products of earlier blocks
+        uint32_t turn[2] = {0, 0};                        // parity of each accumulator's next block
+        int32_t checked = 0;                              // V blocks checked so far
         while (ok && next_part()) {
             const int32_t n = sg.kb1 - sg.kb0, lag = sg.ntok > tpt ? 1 : 2;
-            uint32_t* noted = flags + (seg % C::kBufs) * (PA_MAX_TREE_NODES / 32);
-            if (lane < PA_MAX_TREE_NODES / 32) noted[lane] = 0;
-            __syncwarp();
             ok = warp_wait(q_full, seg & 1);
             for (int32_t x = 0; ok && x < n + lag; ++x) {
                 const bool has_k = x < n, has_v = x >= lag;
                 const int32_t ki = item0 + k_item(x, lag), vi = item0 + v_item(x - lag, lag, n);
                 const int32_t ks = ki % C::kSlots, vs = has_v ? vi % C::kSlots : 0;
-                // K: K-major, 128-byte swizzle; V: MN-major, 64-column atoms ho
-                // bytes apart (LBO)
-                const uint64_t kdesc = umma_sdesc(sm_u + C::kSlotOff + ks * C::kItem, 16, gs, 2);
-                const uint64_t vdesc = umma_sdesc(sm_u + C::kSlotOff + vs * C::kItem, ho, gs, 2);
+                // K: K-major, 128-byte swizzle; V: MN-major, 64-column atoms
+                // ho bytes apart (LBO)
+                const uint32_t k_lo = (slot_lo + (uint32_t)ks * (C::kItem >> 4)) | kKLbo;
+                const uint32_t v_lo = (slot_lo + (uint32_t)vs * (C::kItem >> 4)) | kVLbo;
                 int32_t vkeys = C::kKeys;                 // keys of V's block
-                if (has_k) ok = warp_wait(kv_full(ks), (ki / C::kSlots) & 1);
-                if (ok && has_v) {
-                    ok = warp_wait(kv_full(vs), (vi / C::kSlots) & 1);
+                if (has_v) {
+                    if (!(ok = warp_wait(kv_full(vs), (vi / C::kSlots) & 1))) break;
                     const int32_t key0 = (sg.kb0 + x - lag) * C::kKeys;
-                    if (ok && key0 + C::kKeys > sg.C) {
-                        // rows of tree nodes, and rows behind the last key up to
-                        // the end of its 16-key step (later steps are left out)
+                    if (key0 + C::kKeys > sg.C) {
                         vkeys = min(C::kKeys, sg.T - key0);
-                        const int32_t r0 = max(0, sg.C - key0), r1 = (vkeys + 15) & ~15;
-                        uint8_t* vt = sm + C::kSlotOff + vs * C::kItem;
-                        for (int32_t y = r0 * 8 + lane; y < r1 * 8; y += 32) {
-                            const int32_t row = y >> 3;
-#pragma unroll
-                            for (int32_t h = 0; h < C::kHalves; ++h) {
-                                uint4* p = reinterpret_cast<uint4*>(vt + (row >> 3) * gs + h * ho +
-                                                                    (y & 63) * 16);
-                                if (row >= vkeys) {
-                                    *p = make_uint4(0u, 0u, 0u, 0u);
-                                } else {
-                                    const uint4 v = *p;
-                                    if (bf16x2_odd(v.x) || bf16x2_odd(v.y) || bf16x2_odd(v.z) ||
-                                        bf16x2_odd(v.w)) {
-                                        *p = make_uint4(bf16x2_clean(v.x), bf16x2_clean(v.y),
-                                                        bf16x2_clean(v.z), bf16x2_clean(v.w));
-                                        const int32_t node = key0 + row - sg.C;
-                                        atomicOr(noted + (node >> 5), 1u << (node & 31));
-                                    }
-                                }
-                            }
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
+                        if (lane == 0) mbar_arrive(v_go);
+                        if (!(ok = warp_wait(v_ok, checked++ & 1))) break;
                     }
                     // the output of the part before this one has left O
-                    if (ok && x == lag && seg > 0) ok = warp_wait(o_free, (seg - 1) & 1);
+                    if (x == lag && seg > 0 && !(ok = warp_wait(o_free, (seg - 1) & 1))) break;
                 }
-                for (int32_t t = lag == 1 ? 0 : x & 1; ok && t < (lag == 1 ? 2 : (x & 1) + 1); ++t) {
+#pragma unroll
+                for (int32_t t = 0; t < 2; ++t) {
+                    if (lag == 2 && t != (x & 1)) continue;
                     const uint32_t s_t = tmem + t * C::kTileCols;
                     if (has_v) {
                         const bool fresh = x < (lag == 1 ? 2 : 4);   // O's first block
+                        if (!(ok = warp_wait(p_full(t), turn[t]))) break;
+                        turn[t] ^= 1u;
+                        tc_fence_after();
+                        if (leader) {
+                            // O += P V: half hf of the keys has hi at columns
+                            // 64 hf .. 64 hf + 31 and lo at the next 32, 16 keys =
+                            // 8 columns per step (unrolled: descriptors from a
+                            // loop's counter took 130 cycles an instruction)
 #pragma unroll
-                        for (int32_t hf = 0; hf < 2; ++hf) {
-                            if (!warp_wait(hf ? p_full(t) : p_half(t), done[t] & 1)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            if (leader) {
-                                // half hf: hi at columns 64 hf .. 64 hf + 31,
-                                // lo at the next 32; 16 keys = 8 columns per step
-                                // (unrolled: descriptors from a loop's counter
-                                // take 130 cycles an instruction)
+                            for (int32_t k = 0; k < 8; ++k)
 #pragma unroll
                                 for (int32_t lo = 0; lo < 2; ++lo)
-#pragma unroll
-                                    for (int32_t k = 0; k < 4; ++k)
-                                        if ((hf * 4 + k) * 16 < vkeys)
-                                            umma_bf16_ts(s_t + C::kOCol, s_t + hf * 64 + lo * 32 + k * 8,
-                                                         vdesc + (uint64_t)((hf * 4 + k) * (gs >> 3)), kIdO,
-                                                         (!fresh || hf > 0 || lo > 0 || k > 0) ? 1u : 0u);
-                                umma_commit(hf ? o_done(t) : o_half(t));
-                            }
-                            __syncwarp();
+                                    if (k * 16 < vkeys)
+                                        umma_bf16_ts(s_t + C::kOCol, s_t + (k >> 2) * 64 + lo * 32 + (k & 3) * 8,
+                                                     umma_desc(v_lo + k * (gs >> 3), kKvHi), kIdO,
+                                                     (!fresh || lo > 0 || k > 0) ? 1u : 0u);
+                            umma_commit(o_done(t));
                         }
-                        if (!ok) break;
-                        if (t == 0) ++done[0]; else ++done[1];
+                        __syncwarp();
                     }
-                    if (has_k && leader) {
-                        // S(x) = Q K(x)^T over the columns P(x - lag) occupied,
-                        // k-steps of the head dim only
-                        const uint64_t qdesc = qdesc0 + (uint64_t)(lag == 1 ? t * (C::kQTile >> 4) : 0);
+                    if (has_k) {
+                        if ((lag == 2 || t == 0) &&
+                            !(ok = warp_wait(kv_full(ks), (ki / C::kSlots) & 1)))
+                            break;
+                        if (leader) {
+                            // S(x) = Q K(x)^T over the columns P(x - lag) occupied,
+                            // k-steps of the head dim only
+                            const uint32_t q_t = q_lo + (lag == 1 ? t * (C::kQTile >> 4) : 0);
 #pragma unroll
-                        for (int32_t k = 0; k < D / 16; ++k)
-                            if (k < hd / 16)
-                                umma_bf16(s_t, qdesc + (uint64_t)((k >> 2) * (C::kRows * 8) + (k & 3) * 2),
-                                          kdesc + (uint64_t)((k >> 2) * (ho >> 4) + (k & 3) * 2), kIdS,
-                                          k > 0 ? 1u : 0u);
-                        umma_commit(s_full(t));
+                            for (int32_t k = 0; k < D / 16; ++k)
+                                if (k < hd / 16)
+                                    umma_bf16(s_t, umma_desc(q_t + (k >> 2) * (C::kRows * 8) + (k & 3) * 2, kQHi),
+                                              umma_desc(k_lo + (k >> 2) * (ho >> 4) + (k & 3) * 2, kKvHi), kIdS,
+                                              k > 0 ? 1u : 0u);
+                            umma_commit(s_full(t));
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
-                if (ok && leader) {
+                if (!ok) break;
+                if (leader) {
                     if (has_k) umma_commit(kv_empty(ks));
                     if (has_v) umma_commit(kv_empty(vs));
                     // every S of the part is issued, and the output of the part
@@ -393,63 +467,6 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
         __syncwarp();
         mbar_wait_bounded(bar_fin, 0, kWaitLimitCycles);
         if (!ok && lane == 0) raise_error(PA_DEVERR_TIMEOUT);
-    } else if (warp == C::kPlanWarp) {
-        // ---- the range's parts; Q and parents of each ------------------------
-        TreeCut cut{};
-        bool was_one = false, more = true;
-        int32_t said = 0;                                 // parts announced
-        TreeSeg ahead;
-        // announce the next part (n = 0: there is none)
-        auto announce = [&]() {
-            if (!more) return;
-            more = tree_next(a, w.s, it, ahead);
-            if (!more) ahead.n = 0;
-            const int32_t s = said % C::kQueue;
-            if (said >= C::kQueue) ok = warp_wait(seg_empty(s), ((said / C::kQueue) - 1) & 1);
-            if (!ok) return;
-            if (lane == 0) queue[s] = ahead;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(seg_full(s));
-            ++said;
-            if (more && ahead.kb0 == 0 && ahead.parts > 0)
-                cut = TreeCut{ahead.q0 + ahead.tok0, ahead.ntok, ahead.g, ahead.sg, ahead.parts, {0, 0, 0}};
-        };
-        announce();
-        while (ok && more) {
-            sg = ahead;
-            announce();                                   // one part ahead of Q
-            const int32_t tiles = sg.ntok > tpt ? 2 : 1;
-            if (ok && seg > 0) ok = warp_wait(q_free, (seg - 1) & 1);
-            // tile 1's rows hold the (m, l) of a part with one tile until its
-            // output has been written
-            if (ok && tiles == 2 && was_one) ok = warp_wait(o_free, (seg - 1) & 1);
-            if (!ok) break;
-            // Q: a copy per tile and half of `tokens` x `heads` rows in place.  Rows
-            // behind the part's last node (or head) hold whatever comes there:
-            // a row's scores reach no other row.
-            const uint32_t q_bytes = (uint32_t)(tpt * HT) * 128u * C::kHalves * tiles;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(q_full, q_bytes);
-                for (int32_t t = 0; t < tiles; ++t)
-                    for (int32_t h = 0; h < C::kHalves; ++h)
-                        tma_load_3d(sm_u + t * C::kQTile + h * (C::kRows * 128), &tmap_q, h * 64,
-                                    sg.g * G + sg.sg * HT, sg.q0 + sg.tok0 + t * tpt, q_full);
-            }
-            for (int32_t j = lane; j < sg.n; j += 32) {
-                const int32_t p = tree_parent(a.parents[sg.q0 + j], j, true);
-                parents[(seg % C::kBufs) * PA_MAX_TREE_NODES + j] = (uint8_t)(p + 1);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);           // the parents are there
-            was_one = tiles == 1;
-            ++seg;
-        }
-        if (w.cuts != nullptr && lane == 0) w.cuts[blockIdx.x] = cut;
-        if (!ok) {
-            // (the MMA warp waits for every Q; after a failure this warp does)
-            if (seg > 0) mbar_wait_bounded(q_full, (seg - 1) & 1, kWaitLimitCycles);
-            if (lane == 0) raise_error(PA_DEVERR_TIMEOUT);
-        }
     } else {
         // ---- softmax of accumulator wg, lane r -------------------------------
         const int32_t wg = warp >> 2, r = tid & (C::kRows - 1);
@@ -492,16 +509,17 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     __syncwarp();
                 }
                 const bool first = x == mine0;            // O holds nothing of this part yet
-                // One 64-key half of S at a time: load it, mask it, take its
-                // maximum, move this row's reference if that exceeds it by more
-                // than 8 (so O is rescaled rarely; p <= 2^8), p = 2^(s c - m),
-                // P as hi + lo over the half's own 64 columns of S, rescale O if
-                // the reference moved, publish the half.  (The loop is not
-                // unrolled: the kernel's first pass is bound by instruction
-                // fetches.)
-#pragma unroll 1
-                for (int32_t hh = 0; hh < 2; ++hh) {
-                    uint32_t sr[2][32];
+                // 64 keys of S at a time: mask them and take their maximum; move
+                // this row's reference m if the block's exceeds it by more than 8
+                // (so O is rescaled rarely; p <= 2^8); then again 64 at a time p =
+                // 2^(s c - m), as hi + lo over the same columns of S.  (The loops are
+                // not unrolled: a call's first pass is bound by instruction
+                // fetches.  Publishing P by halves, so that its products begin
+                // beside the second half's softmax, cost the MMA warp more in waits
+                // than it gave.)
+                uint32_t sr[2][32];
+                float mx = -INFINITY;
+                auto load = [&](int32_t hh) {
                     tmem_ld32_async(s_tm + hh * 64, sr[0]);
                     tmem_ld32_async(s_tm + hh * 64 + 32, sr[1]);
                     tmem_wait_ld();
@@ -515,21 +533,27 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
                             if (!(bits[j >> 5] >> (j & 31) & 1u))
                                 sr[j >> 5][j & 31] = __float_as_uint(-INFINITY);
                     }
-                    float mp[4];
-#pragma unroll
-                    for (int32_t u = 0; u < 4; ++u) mp[u] = -INFINITY;
+                };
+#pragma unroll 1
+                for (int32_t hh = 0; hh < 2; ++hh) {
+                    load(hh);
+                    float mp[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int32_t jj = 0; jj < 32; ++jj)
                         mp[jj & 3] = fmax3(mp[jj & 3], __uint_as_float(sr[(2 * jj) >> 5][(2 * jj) & 31]),
                                            __uint_as_float(sr[(2 * jj + 1) >> 5][(2 * jj + 1) & 31]));
-                    const float mx = fmaxf(fmax3(mp[0], mp[1], mp[2]), mp[3]) * c;
-                    const bool moved = mx > m_ref + 8.f;
-                    const float al = moved ? ex2_approx(m_ref - mx) : 1.f;   // 0 when m_ref = -inf
-                    if (moved) m_ref = mx;
-                    l *= al;
-                    const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-                    const float2 c2 = make_float2(c, c), nm2 = make_float2(-ref, -ref);
-                    float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    mx = fmaxf(fmax3(mp[0], mp[1], mp[2]), mp[3]);
+                }
+                mx *= c;
+                const bool moved = mx > m_ref + 8.f;
+                const float al = moved ? ex2_approx(m_ref - mx) : 1.f;   // 0 when m_ref = -inf
+                if (moved) m_ref = mx;
+                const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+                const float2 c2 = make_float2(c, c), nm2 = make_float2(-ref, -ref);
+                float2 rs[2] = {make_float2(l * al, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                for (int32_t hh = 1; hh >= 0; --hh) {     // (the second half's are in registers)
+                    if (hh == 0) load(0);
                     uint32_t pk[32], plo[32];             // hi and lo parts of P
 #pragma unroll
                     for (int32_t jj = 0; jj < 32; ++jj) {
@@ -541,32 +565,28 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         rs[jj & 1] = __fadd2_rn(rs[jj & 1], pp);
                         split_bf16x2(pp.x, pp.y, pk[jj], plo[jj]);
                     }
-                    // this half's 64 columns of S are in registers: hi and lo
-                    // take them
                     tmem_st32_async(s_tm + hh * 64, pk);
                     tmem_st32_async(s_tm + hh * 64 + 32, plo);
-                    l += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
-                    // O holds the P V of every earlier half: rescale it once
-                    // that has finished, before this half is published
-                    if ((!first || hh > 0) && __any_sync(0xffffffffu, moved)) {
-                        ok = hh == 0 ? warp_wait(o_done(wg), (blocks - 1) & 1)
-                                     : warp_wait(o_half(wg), blocks & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int32_t cc = 0; cc < D / 32; ++cc) {
-                            float ov[32];
-                            tmem_ld32(o_tm + cc * 32, ov);
-#pragma unroll
-                            for (int32_t j = 0; j < 32; ++j) ov[j] *= al;
-                            tmem_st32(o_tm + cc * 32, ov);
-                        }
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(hh == 0 ? p_half(wg) : p_full(wg));
                 }
+                l = (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
+                // O holds the P V of the earlier blocks: rescale it once that has
+                // finished, before this block is published
+                if (!first && __any_sync(0xffffffffu, moved)) {
+                    if (!(ok = warp_wait(o_done(wg), (blocks - 1) & 1))) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int32_t cc = 0; cc < D / 32; ++cc) {
+                        float ov[32];
+                        tmem_ld32(o_tm + cc * 32, ov);
+#pragma unroll
+                        for (int32_t j = 0; j < 32; ++j) ov[j] *= al;
+                        tmem_st32(o_tm + cc * 32, ov);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(wg));
                 ++blocks;
             }
             if (!ok) break;
