@@ -275,21 +275,39 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const int32_t vkeys = min(C::kKeys, sg.T - key0);
                 const int32_t r0 = max(0, sg.C - key0), r1 = (vkeys + 15) & ~15;
                 uint8_t* vt = sm + C::kSlotOff + (item0 + v_item(y, lag, n)) % C::kSlots * C::kItem;
-                for (int32_t p0 = r0 * 8 + lane; p0 < r1 * 8; p0 += 32) {
-                    const int32_t row = p0 >> 3;
+                // 16-byte pieces x of the block's rows in shared memory: row x / 8
+                auto piece = [&](int32_t x, int32_t h) {
+                    return reinterpret_cast<uint4*>(vt + (x >> 6) * gs + h * ho + (x & 63) * 16);
+                };
+                for (int32_t x = vkeys * 8 + lane; x < r1 * 8; x += 32)
+#pragma unroll
+                    for (int32_t h = 0; h < C::kHalves; ++h) *piece(x, h) = make_uint4(0u, 0u, 0u, 0u);
+                // 0 x is NaN for a value that is not finite: one product and sum
+                // per pair says whether there is any
+                __nv_bfloat162 sum = __float2bfloat162_rn(0.f);
+#pragma unroll 4
+                for (int32_t x = r0 * 8 + lane; x < vkeys * 8; x += 32) {
 #pragma unroll
                     for (int32_t h = 0; h < C::kHalves; ++h) {
-                        uint4* p = reinterpret_cast<uint4*>(vt + (row >> 3) * gs + h * ho +
-                                                            (p0 & 63) * 16);
-                        if (row >= vkeys) {
-                            *p = make_uint4(0u, 0u, 0u, 0u);
-                        } else {
-                            const uint4 v = *p;
-                            if (bf16x2_odd(v.x) || bf16x2_odd(v.y) || bf16x2_odd(v.z) ||
-                                bf16x2_odd(v.w)) {
-                                *p = make_uint4(bf16x2_clean(v.x), bf16x2_clean(v.y),
-                                                bf16x2_clean(v.z), bf16x2_clean(v.w));
-                                const int32_t node = key0 + row - sg.C;
+                        const uint4 v = *piece(x, h);
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int32_t e = 0; e < 4; ++e)
+                            sum = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u[e]),
+                                          __float2bfloat162_rn(0.f), sum);
+                    }
+                }
+                const bool odd = __isnan(__low2float(sum)) || __isnan(__high2float(sum));
+                if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+                    for (int32_t x = r0 * 8 + lane; x < vkeys * 8; x += 32) {
+#pragma unroll 1
+                        for (int32_t h = 0; h < C::kHalves; ++h) {
+                            const uint4 v = *piece(x, h);
+                            if (bf16x2_odd(v.x) || bf16x2_odd(v.y) || bf16x2_odd(v.z) || bf16x2_odd(v.w)) {
+                                *piece(x, h) = make_uint4(bf16x2_clean(v.x), bf16x2_clean(v.y),
+                                                          bf16x2_clean(v.z), bf16x2_clean(v.w));
+                                const int32_t node = key0 + (x >> 3) - sg.C;
                                 atomicOr(noted + (node >> 5), 1u << (node & 31));
                             }
                         }
@@ -630,6 +648,18 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
                                  ((int64_t)(sg.q0 + node) * a.num_q_heads + (int64_t)sg.g * G +
                                   sg.sg * HT + rhead) * hd;
+            // a whole unit's rows are stored 64 bytes at a time by groups of four
+            // lanes: after a 4 x 4 transpose lane b of a group has piece b of each
+            // of its rows (a row a lane made 32 partial lines a store)
+            __nv_bfloat16* dst[4];
+#pragma unroll
+            for (int32_t k = 0; k < 4; ++k) {
+                const int32_t from = (lane & ~3) + k;
+                const uint64_t p = reinterpret_cast<uint64_t>(row_ok ? out : nullptr);
+                const uint64_t hi = __shfl_sync(0xffffffffu, (uint32_t)(p >> 32), from);
+                dst[k] = reinterpret_cast<__nv_bfloat16*>(
+                    hi << 32 | __shfl_sync(0xffffffffu, (uint32_t)p, from));
+            }
             const int32_t c0 = two ? 0 : wg * (D / 64), c1 = two ? D / 32 : c0 + D / 64;
             const bool both = !two && n > 1;
 #pragma unroll 1
@@ -663,26 +693,39 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         }
                     }
                 }
-                if (row_ok) {
-                    if (whole) {
+                if (whole) {
+                    uint32_t pc[4][4];                    // 16-byte pieces of this lane's row
 #pragma unroll
-                        for (int32_t q4 = 0; q4 < 4; ++q4) {
-                            if (cc * 32 + q4 * 8 >= hd) break;   // past the head dim
-                            uint4 v;
-                            v.x = pack_bf16x2(ov[q4 * 8 + 0], ov[q4 * 8 + 1]);
-                            v.y = pack_bf16x2(ov[q4 * 8 + 2], ov[q4 * 8 + 3]);
-                            v.z = pack_bf16x2(ov[q4 * 8 + 4], ov[q4 * 8 + 5]);
-                            v.w = pack_bf16x2(ov[q4 * 8 + 6], ov[q4 * 8 + 7]);
-                            *reinterpret_cast<uint4*>(out + cc * 32 + q4 * 8) = v;
-                        }
-                    } else {
+                    for (int32_t q = 0; q < 16; ++q)
+                        pc[q >> 2][q & 3] = pack_bf16x2(ov[2 * q], ov[2 * q + 1]);
+                    __syncwarp();
 #pragma unroll
-                        for (int32_t q4 = 0; q4 < 8; ++q4) {
-                            if (cc * 32 + q4 * 4 >= hd) break;
-                            *reinterpret_cast<float4*>(
-                                cell + ((size_t)(cc * 8 + q4) * 2 * C::kRows + urow) * 4) =
-                                make_float4(ov[q4 * 4], ov[q4 * 4 + 1], ov[q4 * 4 + 2], ov[q4 * 4 + 3]);
+                    for (int32_t e = 0; e < 4; ++e) {
+#pragma unroll
+                        for (int32_t s = 1; s < 4; s <<= 1) {
+#pragma unroll
+                            for (int32_t k = 0; k < 4; ++k) {
+                                if (k & s) continue;
+                                const bool up1 = lane & s;
+                                const uint32_t got = __shfl_xor_sync(
+                                    0xffffffffu, up1 ? pc[k][e] : pc[k + s][e], s);
+                                if (up1) pc[k][e] = got; else pc[k + s][e] = got;
+                            }
                         }
+                    }
+                    const int32_t col = cc * 32 + (lane & 3) * 8;
+#pragma unroll
+                    for (int32_t k = 0; k < 4; ++k)
+                        if (dst[k] != nullptr && col < hd)
+                            *reinterpret_cast<uint4*>(dst[k] + col) =
+                                make_uint4(pc[k][0], pc[k][1], pc[k][2], pc[k][3]);
+                } else if (row_ok) {
+#pragma unroll
+                    for (int32_t q4 = 0; q4 < 8; ++q4) {
+                        if (cc * 32 + q4 * 4 >= hd) break;   // past the head dim
+                        *reinterpret_cast<float4*>(
+                            cell + ((size_t)(cc * 8 + q4) * 2 * C::kRows + urow) * 4) =
+                            make_float4(ov[q4 * 4], ov[q4 * 4 + 1], ov[q4 * 4 + 2], ov[q4 * 4 + 3]);
                     }
                 }
             }
