@@ -2,8 +2,10 @@
 // the merge of the parts.
 //
 // A unit is one (sequence, kv head, sub-group of query heads, tile of tree
-// tokens) with all its keys; its cost is its key blocks plus `overhead` for
-// its prologue and epilogue.  The units' costs laid end to end are cut into
+// tokens) with all its keys; its cost is `overhead` for its prologue and
+// epilogue, and for each key block one weight or the other by whether its
+// sequence's units have one tile of rows or more.  A block belongs to the range
+// that its cost begins in.  The units' costs laid end to end are cut into
 // equal ranges, one per CTA of a grid that fills the GPU once, so the load is
 // even whatever the lengths are: a CTA takes the tail of one unit, some whole
 // units and the head of another.  A unit inside one range is written to the
@@ -27,6 +29,7 @@ struct TreeShape {
     int32_t tokens;         // tokens of a tile: rows / heads
     int32_t sub_groups;     // ceil(group / heads)
     int32_t keys;           // keys of a block
+    int32_t block_one, block_more;   // cost of a key block, with one tile in use or more
     int32_t overhead;       // cost of a unit beside its key blocks
     int32_t min_range;      // least cost of a CTA's range
     int32_t fixed_cost;     // > 0: every unit counts as this much, one unit a CTA
@@ -54,8 +57,13 @@ __device__ __forceinline__ int32_t tree_units(const TreeArgs& a, const TreeShape
     return n > 0 ? a.num_kv_heads * s.sub_groups * ((n + per - 1) / per) : 0;
 }
 
-__device__ __forceinline__ int32_t tree_cost(const TreeShape& s, int32_t T) {
-    return s.fixed_cost > 0 ? s.fixed_cost : (T + s.keys - 1) / s.keys + s.overhead;
+__device__ __forceinline__ int32_t tree_weight(const TreeShape& s, int32_t n) {
+    return n > s.tokens ? s.block_more : s.block_one;
+}
+
+__device__ __forceinline__ int32_t tree_cost(const TreeShape& s, int32_t n, int32_t T) {
+    return s.fixed_cost > 0 ? s.fixed_cost
+                            : (T + s.keys - 1) / s.keys * tree_weight(s, n) + s.overhead;
 }
 
 // One unit's part within a CTA's range.
@@ -83,7 +91,7 @@ __device__ __forceinline__ bool tree_next(const TreeArgs& a, const TreeShape& sh
         const TreeSeq s = tree_seq(a, it.i, false);
         // (a sequence's cost stays in 32 bits: the launch refuses others)
         const int32_t units = tree_units(a, sh, s.n);
-        const int32_t cost = tree_cost(sh, s.T);
+        const int32_t cost = tree_cost(sh, s.n, s.T);
         const int64_t seq1 = it.seq0 + (int64_t)units * cost;
         if (it.pos >= seq1) {
             it.seq0 = seq1;
@@ -95,11 +103,14 @@ __device__ __forceinline__ bool tree_next(const TreeArgs& a, const TreeShape& sh
         const int32_t to = (int32_t)min((int64_t)cost, from + (it.end - it.pos));
         it.pos += to - from;
         o.nb = (s.T + sh.keys - 1) / sh.keys;
-        o.kb0 = min(o.nb, max(0, from - sh.overhead));
-        o.kb1 = min(o.nb, max(0, to - sh.overhead));
+        const int32_t wt = tree_weight(sh, s.n);
+        // blocks whose cost begins in [from, to)
+        o.kb0 = max(0, from - sh.overhead + wt - 1) / wt;
+        o.kb1 = to == cost ? o.nb : min(o.nb, max(0, to - sh.overhead + wt - 1) / wt);
         if (o.kb0 >= o.kb1) continue;
-        const int32_t left = cost - to;           // of the unit, behind this range
-        o.parts = left > 0 ? (int32_t)((left + it.range - 1) / it.range) : 0;
+        // the ranges behind that hold the unit's other blocks
+        const int32_t left = sh.overhead + (o.nb - 1) * wt - to;
+        o.parts = o.kb1 < o.nb ? (int32_t)(left / it.range) + 1 : 0;
         const int32_t per = sh.tokens * sh.tiles, tiles = (s.n + per - 1) / per;
         const int32_t hs = tiles == 1 ? u : u / tiles, tile = u - hs * tiles;
         o.i = it.i;
@@ -128,7 +139,7 @@ __device__ __forceinline__ TreeIter tree_begin(const TreeArgs& a, const TreeWork
     int64_t sum = 0;
     for (int32_t i = i0; i < i1; ++i) {
         const TreeSeq s = tree_seq(a, i, blockIdx.x == 0);
-        sum += (int64_t)tree_units(a, w.s, s.n) * tree_cost(w.s, s.T);
+        sum += (int64_t)tree_units(a, w.s, s.n) * tree_cost(w.s, s.n, s.T);
     }
     int64_t incl = sum;
 #pragma unroll
@@ -162,7 +173,7 @@ __device__ __forceinline__ TreeIter tree_begin(const TreeArgs& a, const TreeWork
         if (chunk > 1) {
             for (;; ++i) {
                 const TreeSeq s = tree_seq(a, i, false);
-                const int64_t c = (int64_t)tree_units(a, w.s, s.n) * tree_cost(w.s, s.T);
+                const int64_t c = (int64_t)tree_units(a, w.s, s.n) * tree_cost(w.s, s.n, s.T);
                 if (it.pos < at + c) break;
                 at += c;
             }
