@@ -473,20 +473,36 @@ def prefill(q, query_start_loc, k_cache, v_cache, block_tables, seq_lens, max_q_
 
 
 # ---- drafted (speculative) steps ------------------------------------------------
+#
+# These calls run once a layer or a step with little work on the GPU, so their
+# checks stay few and plain: one pass over the tensors, no copies.
 
-def _i32(**ts) -> None:
-    for name, t in ts.items():
-        if t is not None and t.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
-
-
-def _on_device(device, *ts) -> None:
-    """Every CUDA tensor on the caches' (tables') device, the current one."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors live on {device}, not on the current device")
+def _step_args(device: int, *ts) -> None:
+    """Contiguous tensors on CUDA device ``device`` or in page-locked memory."""
     for t in ts:
-        if t is not None and t.is_cuda and t.device != device:
-            raise ValueError("tensors live on different devices")
+        if t.is_cuda:
+            if t.get_device() != device:
+                raise ValueError("tensors live on different devices")
+        elif not t.is_pinned():
+            raise ValueError("tensors must be on a CUDA device or in page-locked host memory")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+
+
+def _current(t) -> int:
+    """Index of ``t``'s device, which must be the current one."""
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    device = t.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors live on device {device}, which is not the current one")
+    return device
+
+
+def _raw_stream(stream, device: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream)
 
 
 class StepPlan:
@@ -535,46 +551,52 @@ def plan_step(seq_lens, new_tokens, block_tables, blocks_held, free_blocks, free
     fit plans nothing and raises a bit of ``last_device_error``
     (DEVERR_POOL, DEVERR_SHARED, DEVERR_SEQ_LEN).  ``ref_cnt`` (int32
     [num_blocks]) adds the shared-tail check and the counts of taken blocks."""
-    _dev(block_tables)
-    _dev_or_pinned(seq_lens, new_tokens, blocks_held, free_blocks, free_head)
-    _i32(seq_lens=seq_lens, new_tokens=new_tokens, blocks_held=blocks_held,
-         free_blocks=free_blocks, free_head=free_head, block_tables=block_tables,
-         ref_cnt=ref_cnt)
+    device = _current(block_tables)
     n = seq_lens.numel()
-    if new_tokens.numel() != n or blocks_held.numel() != n or block_tables.dim() != 2 \
-            or block_tables.shape[0] != n or free_head.numel() != 1:
+    if block_tables.dim() != 2 or block_tables.shape[0] != n or new_tokens.numel() != n \
+            or blocks_held.numel() != n or free_head.numel() != 1:
         raise ValueError("seq_lens, new_tokens, blocks_held and block_tables disagree on the "
                          "sequence count")
     if plan is None:
         if max_tokens is None:
             raise ValueError("pass a plan or max_tokens")
         plan = StepPlan.empty(n, max_tokens, block_tables.device)
-    outs = (plan.seq_lens, plan.blocks_held, plan.free_head, plan.query_start_loc,
-            plan.block_start, plan.positions, plan.seq_ids)
-    _dev_or_pinned(plan.slot_mapping, *(t for t in outs if t is not None))
-    _i32(**dict(zip(StepPlan.__slots__, outs[:5])), positions=plan.positions,
-         seq_ids=plan.seq_ids)
-    tokens = plan.slot_mapping.numel()
-    if plan.slot_mapping.dtype != torch.int64:
-        raise ValueError("slot_mapping must be int64")
-    if [t.numel() for t in outs[:5]] != [n, n, 1, n + 1, n + 1] \
-            or any(t is not None and t.numel() != tokens for t in outs[5:]) \
+    lens_out, held_out, head_out = plan.seq_lens, plan.blocks_held, plan.free_head
+    start, taken, slots = plan.query_start_loc, plan.block_start, plan.slot_mapping
+    positions, seq_ids = plan.positions, plan.seq_ids
+    tokens = slots.numel()
+    if lens_out.numel() != n or held_out.numel() != n or head_out.numel() != 1 \
+            or start.numel() != n + 1 or taken.numel() != n + 1 \
+            or (positions is not None and positions.numel() != tokens) \
+            or (seq_ids is not None and seq_ids.numel() != tokens) \
             or (max_tokens is not None and max_tokens != tokens):
         raise ValueError("the plan's buffers do not fit the step")
+    ints = (seq_lens, new_tokens, blocks_held, free_blocks, free_head, block_tables, lens_out,
+            held_out, head_out, start, taken)
+    if positions is not None:
+        ints += (positions,)
+    if seq_ids is not None:
+        ints += (seq_ids,)
     if ref_cnt is not None:
-        _dev(ref_cnt)
-        if ref_cnt.numel() != num_blocks:
-            raise ValueError("ref_cnt must have num_blocks entries")
-    _on_device(block_tables.device, seq_lens, new_tokens, blocks_held, free_blocks, free_head,
-               ref_cnt, plan.slot_mapping, *outs)
+        ints += (ref_cnt,)
+        if not ref_cnt.is_cuda or ref_cnt.numel() != num_blocks:
+            raise ValueError("ref_cnt must be a device tensor of num_blocks entries")
+    i32 = torch.int32
+    for t in ints:
+        if t.dtype is not i32:
+            raise ValueError("all but slot_mapping must be int32")
+    if slots.dtype is not torch.int64:
+        raise ValueError("slot_mapping must be int64")
+    _step_args(device, slots, *ints)
     st = load_library().pa_plan_step(
-        _ptr(seq_lens), _ptr(new_tokens), _ptr(blocks_held), n, _ptr(free_blocks),
-        free_blocks.numel(), _ptr(free_head), _ptr(ref_cnt), num_blocks, block_size,
-        _ptr(block_tables), block_tables.shape[1], _ptr(plan.seq_lens), _ptr(plan.blocks_held),
-        _ptr(plan.free_head), _ptr(plan.query_start_loc), _ptr(plan.block_start),
-        _ptr(plan.slot_mapping), _ptr(plan.positions), _ptr(plan.seq_ids), tokens,
-        _stream(stream))
-    _check(st, "pa_plan_step")
+        seq_lens.data_ptr(), new_tokens.data_ptr(), blocks_held.data_ptr(), n,
+        free_blocks.data_ptr(), free_blocks.numel(), free_head.data_ptr(), _ptr(ref_cnt),
+        num_blocks, block_size, block_tables.data_ptr(), block_tables.shape[1],
+        lens_out.data_ptr(), held_out.data_ptr(), head_out.data_ptr(), start.data_ptr(),
+        taken.data_ptr(), slots.data_ptr(), _ptr(positions), _ptr(seq_ids), tokens,
+        _raw_stream(stream, device))
+    if st != PA_OK:
+        raise PaError(st, "pa_plan_step")
     return plan
 
 
@@ -595,19 +617,23 @@ def decode_tree(q, query_start_loc, parents, k_cache, v_cache, block_tables, seq
     within its sequence, -1 for the cached tokens) and itself.  Returns out
     [total_q, Hq, D] in the cache dtype; rows behind the last sequence are
     left as they were (a missing ``out`` is allocated, not cleared)."""
-    _dev(k_cache, v_cache)
-    _dev_or_pinned(q, query_start_loc, parents, block_tables, seq_lens)
-    _i32(query_start_loc=query_start_loc, parents=parents, block_tables=block_tables,
-         seq_lens=seq_lens)
+    device = _current(k_cache)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache are [num_blocks, num_kv_heads, block_size, "
+                         "head_dim], of one shape")
     desc = cache_desc(k_cache)
-    if tuple(v_cache.shape) != tuple(k_cache.shape):
-        raise ValueError("k_cache and v_cache shapes differ")
-    if q.dim() != 3 or q.shape[2] != desc.head_dim:
-        raise ValueError(f"q must be [total_q, num_q_heads, {desc.head_dim}]")
-    total, hq, d = q.shape
+    d = desc.head_dim
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q must be [total_q, num_q_heads, {d}]")
+    total, hq, _ = q.shape
     n = seq_lens.numel()
-    if q.dtype != k_cache.dtype or v_cache.dtype != k_cache.dtype:
+    dtype = k_cache.dtype
+    if q.dtype is not dtype or v_cache.dtype is not dtype:
         raise ValueError("q and caches must share one dtype")
+    i32 = torch.int32
+    if query_start_loc.dtype is not i32 or parents.dtype is not i32 \
+            or block_tables.dtype is not i32 or seq_lens.dtype is not i32:
+        raise ValueError("query_start_loc, parents, block_tables and seq_lens must be int32")
     if query_start_loc.numel() != n + 1 or parents.numel() != total \
             or block_tables.dim() != 2 or block_tables.shape[0] != n:
         raise ValueError("query_start_loc, parents, block_tables and seq_lens disagree on the "
@@ -616,24 +642,52 @@ def decode_tree(q, query_start_loc, parents, k_cache, v_cache, block_tables, seq
         scale = 1.0 / math.sqrt(d)
     if out is None:
         out = torch.empty_like(q, device=k_cache.device)
-    elif out.shape != q.shape or out.dtype != q.dtype:
+    elif out.shape != q.shape or out.dtype is not dtype:
         raise ValueError("out must have q's shape and dtype")
-    _dev_or_pinned(out)
-    need = decode_tree_workspace_bytes(n, total, hq, max_q_len, max_seq_len, desc)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=k_cache.device)
-    if workspace is not None:
+    lib = load_library()
+    ref = ctypes.byref(desc)
+    if workspace is None:
+        ws_bytes = lib.pa_decode_tree_workspace_bytes(n, total, hq, max_q_len, max_seq_len, ref)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=k_cache.device)
+    else:
         _dev(workspace)
-    _on_device(k_cache.device, v_cache, q, query_start_loc, parents, block_tables, seq_lens, out,
-               workspace)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = load_library().pa_decode_tree(
-        _ptr(q), _ptr(query_start_loc), _ptr(parents), total, max_q_len, _ptr(k_cache),
-        _ptr(v_cache), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), n, max_seq_len,
-        hq, float(scale), _ptr(out), _ptr(workspace), ws_bytes, ctypes.byref(desc),
-        _stream(stream))
-    _check(st, "pa_decode_tree")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _step_args(device, k_cache, v_cache, q, query_start_loc, parents, block_tables, seq_lens, out)
+    st = lib.pa_decode_tree(
+        q.data_ptr(), query_start_loc.data_ptr(), parents.data_ptr(), total, max_q_len,
+        k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+        seq_lens.data_ptr(), n, max_seq_len, hq, scale, out.data_ptr(), _ptr(workspace),
+        ws_bytes, ref, _raw_stream(stream, device))
+    if st != PA_OK:
+        raise PaError(st, "pa_decode_tree")
     return out
+
+
+def _layer_caches(caches):
+    """(first layer's cache, addresses of all layers) of one cache, a stack
+    of them, or a sequence."""
+    if isinstance(caches, torch.Tensor):
+        if not caches.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        base = caches.data_ptr()
+        if caches.dim() == 4:
+            return caches, [base]
+        if caches.dim() != 5 or caches.shape[0] < 1:
+            raise ValueError("caches are [num_blocks, num_kv_heads, block_size, head_dim], with "
+                             "a leading dimension of layers or in a sequence")
+        step = caches.stride(0) * caches.element_size()
+        return caches[0], list(range(base, base + step * caches.shape[0], step))
+    caches = list(caches)
+    if not caches:
+        raise ValueError("no caches")
+    first = caches[0]
+    for c in caches:
+        if c.shape != first.shape or c.dtype is not first.dtype or c.device != first.device \
+                or not c.is_contiguous():
+            raise ValueError("the caches must share one shape, dtype and device, and be "
+                             "contiguous")
+    return first, [c.data_ptr() for c in caches]
 
 
 def accept_tree(leaf, parents, query_start_loc, seq_lens, k_caches, v_caches, block_tables,
@@ -646,24 +700,12 @@ def accept_tree(leaf, parents, query_start_loc, seq_lens, k_caches, v_caches, bl
     [total_q]): the lengths with the path, and per sequence the packed rows
     of its path from its first row on, then -1 (rows behind the last sequence
     are left as they were)."""
-    def layers(c):
-        if isinstance(c, torch.Tensor):
-            _dev(c)
-            return [c] if c.dim() == 4 else list(c.unbind(0))
-        return list(c)
-
-    k_caches, v_caches = layers(k_caches), layers(v_caches)
-    if not k_caches or len(k_caches) != len(v_caches):
-        raise ValueError("k_caches and v_caches must have the same number of layers")
-    first = k_caches[0]
-    for c in k_caches + v_caches:
-        if c.shape != first.shape or c.dtype != first.dtype or c.device != first.device:
-            raise ValueError("the caches must share one shape, dtype and device")
-    _dev(*k_caches, *v_caches)
-    _dev_or_pinned(leaf, parents, query_start_loc, seq_lens, block_tables)
-    _i32(leaf=leaf, parents=parents, query_start_loc=query_start_loc, seq_lens=seq_lens,
-         block_tables=block_tables)
-    desc = cache_desc(first)
+    first, keys = _layer_caches(k_caches)
+    other, values = _layer_caches(v_caches)
+    device = _current(first)
+    if len(keys) != len(values) or other.shape != first.shape or other.dtype is not first.dtype \
+            or other.get_device() != device:
+        raise ValueError("k_caches and v_caches must have the same layers, shape and dtype")
     n, total = seq_lens.numel(), parents.numel()
     if leaf.numel() != n or query_start_loc.numel() != n + 1 or block_tables.dim() != 2 \
             or block_tables.shape[0] != n:
@@ -673,17 +715,20 @@ def accept_tree(leaf, parents, query_start_loc, seq_lens, k_caches, v_caches, bl
         new_lens = torch.empty(n, dtype=torch.int32, device=first.device)
     if accepted_rows is None:
         accepted_rows = torch.empty(total, dtype=torch.int32, device=first.device)
-    _dev_or_pinned(new_lens, accepted_rows)
-    _i32(new_lens=new_lens, accepted_rows=accepted_rows)
     if new_lens.numel() != n or accepted_rows.numel() != total:
         raise ValueError("new_lens must have N and accepted_rows total_q entries")
-    _on_device(first.device, leaf, parents, query_start_loc, seq_lens, block_tables, new_lens,
-               accepted_rows)
-    ptrs = ctypes.c_void_p * len(k_caches)
+    ints = (leaf, parents, query_start_loc, seq_lens, block_tables, new_lens, accepted_rows)
+    i32 = torch.int32
+    for t in ints:
+        if t.dtype is not i32:
+            raise ValueError("all arguments but the caches must be int32")
+    _step_args(device, *ints)
+    ptrs = ctypes.c_void_p * len(keys)
     st = load_library().pa_accept_tree(
-        _ptr(leaf), _ptr(parents), _ptr(query_start_loc), _ptr(seq_lens), n, total, max_q_len,
-        _ptr(block_tables), block_tables.shape[1], ptrs(*map(_ptr, k_caches)),
-        ptrs(*map(_ptr, v_caches)), len(k_caches), _ptr(new_lens), _ptr(accepted_rows),
-        ctypes.byref(desc), _stream(stream))
-    _check(st, "pa_accept_tree")
+        leaf.data_ptr(), parents.data_ptr(), query_start_loc.data_ptr(), seq_lens.data_ptr(), n,
+        total, max_q_len, block_tables.data_ptr(), block_tables.shape[1], ptrs(*keys),
+        ptrs(*values), len(keys), new_lens.data_ptr(), accepted_rows.data_ptr(),
+        ctypes.byref(cache_desc(first)), _raw_stream(stream, device))
+    if st != PA_OK:
+        raise PaError(st, "pa_accept_tree")
     return new_lens, accepted_rows
