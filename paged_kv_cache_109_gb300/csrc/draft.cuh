@@ -7,6 +7,8 @@
 #include "plan_step.cuh"
 #include "tree_args.cuh"
 #include "tree_generic.cuh"
+#include "tree_mma.cuh"
+#include "tree_tiled.cuh"
 #include "tree_ws.cuh"
 
 namespace pa {
@@ -75,15 +77,20 @@ TreeShape tree_shape(int32_t rows, int32_t tiles, int32_t keys, int32_t group) {
     return s;
 }
 
+// Most that a unit can cost.
+int64_t tree_most(const TreeShape& s, int32_t max_q_len, int32_t max_seq_len) {
+    return ((int64_t)max_seq_len + s.keys - 1) / s.keys *
+               (max_q_len > s.tokens ? s.block_more : s.block_one) +
+           s.overhead;
+}
+
 // CTAs of a call: `per_sm` a SM, fewer when the host's bounds say that less
 // work can be there.
 int32_t tree_ctas(const TreeShape& s, int32_t num_seqs, int32_t max_q_len, int32_t max_seq_len,
                   int32_t num_kv_heads, int32_t per_sm) {
     const int64_t per = (int64_t)s.tokens * s.tiles;
     const int64_t units = (int64_t)num_seqs * num_kv_heads * s.sub_groups * ((max_q_len + per - 1) / per);
-    const int64_t cost = ((int64_t)max_seq_len + s.keys - 1) / s.keys *
-                             (max_q_len > s.tokens ? s.block_more : s.block_one) +
-                         s.overhead;
+    const int64_t cost = tree_most(s, max_q_len, max_seq_len);
     const int64_t ctas = (units * cost + s.min_range - 1) / s.min_range;
     return (int32_t)std::max<int64_t>(
         1, std::min<int64_t>(ctas, (int64_t)std::max(1, device_sm_count()) * per_sm));
@@ -103,6 +110,109 @@ TreeShape tree_ws_tiling(int32_t group) {
     s.overhead = 4;
     s.min_range = 8;
     return s;
+}
+
+// The mma.sync kernel: 64 rows, 64-key chunks up to 128 columns, 32-key ones
+// up to 256.
+bool tree_mma_shape(const pa_cache_desc* c) {
+    return c->dtype == PA_BF16 && c->head_dim % 16 == 0 && c->head_dim <= 256;
+}
+TreeShape tree_mma_tiling(int32_t head_dim, int32_t group) {
+    TreeShape s = tree_shape(kTreeMmaRows, 1, head_dim <= 128 ? 64 : 32, group);
+    s.overhead = 2;
+    s.min_range = 8;
+    return s;
+}
+
+// The CUDA-core kernel: 16, 32 or 64 rows by what a sequence can have (up to 32
+// above 128 columns); 32-key chunks up to 128 columns, 16-key ones up to 256.
+int32_t tree_tiled_rpt(int32_t head_dim, int32_t group, int32_t max_q_len) {
+    const int64_t rows = (int64_t)group * max_q_len;
+    return rows <= 16 ? 1 : rows <= 32 || head_dim > 128 ? 2 : 4;
+}
+TreeShape tree_tiled_tiling(int32_t head_dim, int32_t group, int32_t max_q_len) {
+    TreeShape s = tree_shape(16 * tree_tiled_rpt(head_dim, group, max_q_len), 1,
+                             head_dim <= 128 ? 32 : 16, group);
+    s.overhead = 2;
+    s.min_range = 8;
+    return s;
+}
+
+// CTAs of `kern` one SM holds, per instance (0-6) and head dim (which sets its
+// shared memory).
+template <typename Kern>
+int32_t tree_per_sm(int instance, Kern kern, int threads, size_t smem, int32_t head_dim) {
+    static std::atomic<int> table[7][257];
+    std::atomic<int>* cached = table[instance];
+    int n = cached[head_dim].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (set_smem(kern, smem) && cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                                    &n, kern, threads, smem) == cudaSuccess && n > 0) {
+        cached[head_dim].store(n, std::memory_order_relaxed);
+        return n;
+    }
+    cudaGetLastError();
+    return 1;
+}
+
+// Calls f(kernel, threads, shared bytes) with the mma.sync instance of a head dim.
+template <typename F>
+auto with_tree_mma(int32_t head_dim, F f) {
+    if (head_dim <= 128)
+        return f(tree_mma_kernel<128, 64>, kTreeMmaThreads, TreeMmaCfg<128, 64>::smem_bytes(head_dim));
+    return f(tree_mma_kernel<256, 32>, kTreeMmaThreads, TreeMmaCfg<256, 32>::smem_bytes(head_dim));
+}
+
+// The same with the CUDA-core instance.
+template <typename E, typename F>
+auto with_tree_tiled_rows(int32_t head_dim, int32_t rpt, F f) {
+    constexpr int32_t e = (int32_t)sizeof(E);
+    if (head_dim > 128)
+        return rpt == 1 ? f(tree_tiled_kernel<E, 1, 8, 16>, kTreeTiledThreads,
+                            TreeTiledCfg<1, 8, 16>::smem_bytes(head_dim, e))
+                        : f(tree_tiled_kernel<E, 2, 8, 16>, kTreeTiledThreads,
+                            TreeTiledCfg<2, 8, 16>::smem_bytes(head_dim, e));
+    if (rpt == 1)
+        return f(tree_tiled_kernel<E, 1, 4, 32>, kTreeTiledThreads,
+                 TreeTiledCfg<1, 4, 32>::smem_bytes(head_dim, e));
+    if (rpt == 2)
+        return f(tree_tiled_kernel<E, 2, 4, 32>, kTreeTiledThreads,
+                 TreeTiledCfg<2, 4, 32>::smem_bytes(head_dim, e));
+    return f(tree_tiled_kernel<E, 4, 4, 32>, kTreeTiledThreads,
+             TreeTiledCfg<4, 4, 32>::smem_bytes(head_dim, e));
+}
+template <typename F>
+auto with_tree_tiled(const pa_cache_desc* c, int32_t rpt, F f) {
+    return c->dtype == PA_F32 ? with_tree_tiled_rows<float>(c->head_dim, rpt, f)
+                              : with_tree_tiled_rows<__nv_bfloat16>(c->head_dim, rpt, f);
+}
+
+// A kernel's tiling and CTAs for a call.
+enum TreeKernel { kTreeWs, kTreeMma, kTreeTiled };
+struct TreeLaunch {
+    TreeShape s;
+    int32_t ctas;
+};
+TreeLaunch tree_launch(TreeKernel k, const pa_cache_desc* c, int32_t group, int32_t num_seqs,
+                       int32_t max_q_len, int32_t max_seq_len) {
+    TreeLaunch t{};
+    int32_t per_sm = 1, instance = 0;
+    auto resident = [&](auto kern, int threads, size_t smem) {
+        return tree_per_sm(instance, kern, threads, smem, c->head_dim);
+    };
+    if (k == kTreeWs) {
+        t.s = tree_ws_tiling(group);
+    } else if (k == kTreeMma) {
+        t.s = tree_mma_tiling(c->head_dim, group);
+        per_sm = with_tree_mma(c->head_dim, resident);
+    } else {
+        t.s = tree_tiled_tiling(c->head_dim, group, max_q_len);
+        const int32_t rpt = tree_tiled_rpt(c->head_dim, group, max_q_len);
+        instance = 1 + (c->dtype == PA_F32 ? 0 : 3) + rpt / 2;
+        per_sm = with_tree_tiled(c, rpt, resident);
+    }
+    t.ctas = tree_ctas(t.s, num_seqs, max_q_len, max_seq_len, c->num_kv_heads, per_sm);
+    return t;
 }
 
 // Cache viewed as 5-D: (64 columns, 8 rows, 64-column halves, 8-row groups of
@@ -242,10 +352,19 @@ size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t total_q, int32_t
     if (pa_decode_path(num_q_heads, cache) < 0 || num_seqs <= 0 || total_q <= 0 ||
         max_q_len <= 0 || max_seq_len <= 0)
         return 0;
-    if (!tree_ws_shape(cache)) return 0;
-    const TreeShape s = tree_ws_tiling(num_q_heads / cache->num_kv_heads);
-    const int32_t ctas = tree_ctas(s, num_seqs, max_q_len, max_seq_len, cache->num_kv_heads, 1);
-    return tree_workspace(s, ctas, cache->head_dim);
+    // the largest of the kernels that the call's pointers may select
+    const int32_t group = num_q_heads / cache->num_kv_heads;
+    size_t most = 0;
+    auto take = [&](TreeKernel k) {
+        const TreeLaunch t = tree_launch(k, cache, group, num_seqs, max_q_len, max_seq_len);
+        most = std::max(most, tree_workspace(t.s, t.ctas, cache->head_dim));
+    };
+    if (tree_ws_shape(cache)) take(kTreeWs);
+    if (tree_mma_shape(cache))
+        take(kTreeMma);
+    else if (tiled_shape(cache))
+        take(kTreeTiled);
+    return most;
 }
 
 pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const int32_t* parents,
@@ -314,17 +433,39 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
     // -inf: scale > 0; its copies of q are TMA, from device memory
     const bool ws = tree_ws_shape(cache) && aligned(q, 16) && current_device_memory(q) &&
                     aligned(out, 16) && aligned(k_cache, 16) && aligned(v_cache, 16) && scale > 0.f;
-    if (ws) {
+    const bool caches16 = aligned(k_cache, 16) && aligned(v_cache, 16);
+    const bool mma = !ws && tree_mma_shape(cache) && caches16;
+    const bool tiled = !ws && !mma && !tree_mma_shape(cache) && tiled_shape(cache) && caches16 &&
+                       aligned(out, 16);
+    if (ws || mma || tiled) {
+        const TreeKernel kernel = ws ? kTreeWs : mma ? kTreeMma : kTreeTiled;
+        const TreeLaunch t = tree_launch(kernel, cache, a.group, num_seqs, max_q_len, max_seq_len);
+        // unit costs are 32-bit in the kernels
+        const int64_t per = (int64_t)t.s.tokens * t.s.tiles;
+        if ((int64_t)a.num_kv_heads * t.s.sub_groups * ((max_q_len + per - 1) / per) *
+                tree_most(t.s, max_q_len, max_seq_len) > INT32_MAX)
+            return PA_ERR_UNSUPPORTED;
         TreeWork w{};
-        w.s = tree_ws_tiling(a.group);
-        const int32_t ctas = tree_ctas(w.s, num_seqs, max_q_len, max_seq_len, a.num_kv_heads, 1);
+        w.s = t.s;
         uint8_t* base = static_cast<uint8_t*>(workspace);
         w.cuts = reinterpret_cast<TreeCut*>(base);
-        w.cells = reinterpret_cast<float*>(base + align256((size_t)ctas * sizeof(TreeCut)));
-        cudaError_t err = cache->head_dim == 128 ? launch_tree_ws<128, false>(a, w, cache, ctas, st)
-                          : cache->head_dim > 64 ? launch_tree_ws<128, true>(a, w, cache, ctas, st)
-                                                 : launch_tree_ws<64, false>(a, w, cache, ctas, st);
-        if (err == cudaSuccess) err = launch_tree_merge<__nv_bfloat16>(a, w, ctas, st);
+        w.cells = reinterpret_cast<float*>(base + align256((size_t)t.ctas * sizeof(TreeCut)));
+        auto go = [&](auto kern, int threads, size_t smem) {
+            if (!set_smem(kern, smem)) return cudaErrorUnknown;
+            return launch_pdl(kern, dim3(t.ctas), dim3(threads), smem, st, a, w);
+        };
+        cudaError_t err;
+        if (mma)
+            err = with_tree_mma(a.head_dim, go);
+        else if (tiled)
+            err = with_tree_tiled(cache, tree_tiled_rpt(a.head_dim, a.group, max_q_len), go);
+        else
+            err = cache->head_dim == 128 ? launch_tree_ws<128, false>(a, w, cache, t.ctas, st)
+                  : cache->head_dim > 64 ? launch_tree_ws<128, true>(a, w, cache, t.ctas, st)
+                                         : launch_tree_ws<64, false>(a, w, cache, t.ctas, st);
+        if (err == cudaSuccess)
+            err = cache->dtype == PA_F32 ? launch_tree_merge<float>(a, w, t.ctas, st)
+                                         : launch_tree_merge<__nv_bfloat16>(a, w, t.ctas, st);
         return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
     const dim3 grid(total_q, cache->num_kv_heads);

@@ -214,6 +214,7 @@ tree_merge_kernel(const TreeArgs a, const TreeWork w) {
     const float* first = w.cells + (2 * (size_t)blockIdx.x + 1) * cell;
     const float* next = w.cells + 2 * ((size_t)blockIdx.x + 1) * cell;  // cell 0 of the CTAs behind
     E* out = static_cast<E*>(a.out);
+    const bool vec = (reinterpret_cast<uintptr_t>(a.out) & (4 * sizeof(E) - 1)) == 0;
     for (int32_t at = blockIdx.y * kTreeMergeThreads + threadIdx.x; at < live * groups;
          at += gridDim.y * kTreeMergeThreads) {
         const int32_t row = at % live, col = (at / live) * 8;
@@ -248,9 +249,11 @@ tree_merge_kernel(const TreeArgs a, const TreeWork w) {
                         cut.sg * sh.heads + h) * D + col;
 #pragma unroll
         for (int c = 0; c < 8; ++c) o[c] *= inv;
-        if constexpr (sizeof(E) == 2) {
-            // rows are whole 8-byte pieces: the kernels with parts take head
-            // dims that are multiples of 4
+        // (head dims with parts are multiples of 4; an output may be aligned to
+        // its elements only)
+        if (!vec) {
+            for (int c = 0; c < 8 && col + c < D; ++c) dst[c] = Elem<E>::from_float(o[c]);
+        } else if constexpr (sizeof(E) == 2) {
             *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
             if (wide)
                 *reinterpret_cast<uint2*>(dst + 4) =
