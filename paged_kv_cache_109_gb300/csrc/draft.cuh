@@ -8,6 +8,7 @@
 #include "tree_args.cuh"
 #include "tree_generic.cuh"
 #include "tree_mma.cuh"
+#include "tree_tf32.cuh"
 #include "tree_tiled.cuh"
 #include "tree_ws.cuh"
 
@@ -124,7 +125,17 @@ TreeShape tree_mma_tiling(int32_t head_dim, int32_t group) {
     return s;
 }
 
-// The CUDA-core kernel: 16, 32 or 64 rows by what a sequence can have (up to 32
+// The tf32 kernel of fp32 caches: 64 rows, 32-key chunks up to 128 columns,
+// 16-key ones up to 256.
+bool tree_tf_shape(const pa_cache_desc* c) { return c->dtype == PA_F32 && tiled_shape(c); }
+TreeShape tree_tf_tiling(int32_t head_dim, int32_t group) {
+    TreeShape s = tree_shape(kTreeTfRows, 1, head_dim <= 128 ? 32 : 16, group);
+    s.overhead = 2;
+    s.min_range = 8;
+    return s;
+}
+
+// The CUDA-core kernel of the other bf16 shapes: 16, 32 or 64 rows by what a sequence can have (up to 32
 // above 128 columns); 32-key chunks up to 128 columns, 16-key ones up to 256.
 int32_t tree_tiled_rpt(int32_t head_dim, int32_t group, int32_t max_q_len) {
     const int64_t rows = (int64_t)group * max_q_len;
@@ -138,11 +149,11 @@ TreeShape tree_tiled_tiling(int32_t head_dim, int32_t group, int32_t max_q_len) 
     return s;
 }
 
-// CTAs of `kern` one SM holds, per instance (0-6) and head dim (which sets its
+// CTAs of `kern` one SM holds, per instance (0-4) and head dim (which sets its
 // shared memory).
 template <typename Kern>
 int32_t tree_per_sm(int instance, Kern kern, int threads, size_t smem, int32_t head_dim) {
-    static std::atomic<int> table[7][257];
+    static std::atomic<int> table[5][257];
     std::atomic<int>* cached = table[instance];
     int n = cached[head_dim].load(std::memory_order_relaxed);
     if (n > 0) return n;
@@ -163,32 +174,34 @@ auto with_tree_mma(int32_t head_dim, F f) {
     return f(tree_mma_kernel<256, 32>, kTreeMmaThreads, TreeMmaCfg<256, 32>::smem_bytes(head_dim));
 }
 
-// The same with the CUDA-core instance.
-template <typename E, typename F>
-auto with_tree_tiled_rows(int32_t head_dim, int32_t rpt, F f) {
-    constexpr int32_t e = (int32_t)sizeof(E);
+// The same with the tf32 instance, and with the CUDA-core one.
+template <typename F>
+auto with_tree_tf(int32_t head_dim, F f) {
+    if (head_dim <= 128)
+        return f(tree_tf32_kernel<128, 32>, kTreeTfThreads, TreeTfCfg<128, 32>::smem_bytes(head_dim));
+    return f(tree_tf32_kernel<256, 16>, kTreeTfThreads, TreeTfCfg<256, 16>::smem_bytes(head_dim));
+}
+
+template <typename F>
+auto with_tree_tiled(int32_t head_dim, int32_t rpt, F f) {
+    using E = __nv_bfloat16;
     if (head_dim > 128)
         return rpt == 1 ? f(tree_tiled_kernel<E, 1, 8, 16>, kTreeTiledThreads,
-                            TreeTiledCfg<1, 8, 16>::smem_bytes(head_dim, e))
+                            TreeTiledCfg<1, 8, 16>::smem_bytes(head_dim, 2))
                         : f(tree_tiled_kernel<E, 2, 8, 16>, kTreeTiledThreads,
-                            TreeTiledCfg<2, 8, 16>::smem_bytes(head_dim, e));
+                            TreeTiledCfg<2, 8, 16>::smem_bytes(head_dim, 2));
     if (rpt == 1)
         return f(tree_tiled_kernel<E, 1, 4, 32>, kTreeTiledThreads,
-                 TreeTiledCfg<1, 4, 32>::smem_bytes(head_dim, e));
+                 TreeTiledCfg<1, 4, 32>::smem_bytes(head_dim, 2));
     if (rpt == 2)
         return f(tree_tiled_kernel<E, 2, 4, 32>, kTreeTiledThreads,
-                 TreeTiledCfg<2, 4, 32>::smem_bytes(head_dim, e));
+                 TreeTiledCfg<2, 4, 32>::smem_bytes(head_dim, 2));
     return f(tree_tiled_kernel<E, 4, 4, 32>, kTreeTiledThreads,
-             TreeTiledCfg<4, 4, 32>::smem_bytes(head_dim, e));
-}
-template <typename F>
-auto with_tree_tiled(const pa_cache_desc* c, int32_t rpt, F f) {
-    return c->dtype == PA_F32 ? with_tree_tiled_rows<float>(c->head_dim, rpt, f)
-                              : with_tree_tiled_rows<__nv_bfloat16>(c->head_dim, rpt, f);
+             TreeTiledCfg<4, 4, 32>::smem_bytes(head_dim, 2));
 }
 
 // A kernel's tiling and CTAs for a call.
-enum TreeKernel { kTreeWs, kTreeMma, kTreeTiled };
+enum TreeKernel { kTreeWs, kTreeMma, kTreeTf, kTreeTiled };
 struct TreeLaunch {
     TreeShape s;
     int32_t ctas;
@@ -205,11 +218,15 @@ TreeLaunch tree_launch(TreeKernel k, const pa_cache_desc* c, int32_t group, int3
     } else if (k == kTreeMma) {
         t.s = tree_mma_tiling(c->head_dim, group);
         per_sm = with_tree_mma(c->head_dim, resident);
+    } else if (k == kTreeTf) {
+        t.s = tree_tf_tiling(c->head_dim, group);
+        instance = 1;
+        per_sm = with_tree_tf(c->head_dim, resident);
     } else {
         t.s = tree_tiled_tiling(c->head_dim, group, max_q_len);
         const int32_t rpt = tree_tiled_rpt(c->head_dim, group, max_q_len);
-        instance = 1 + (c->dtype == PA_F32 ? 0 : 3) + rpt / 2;
-        per_sm = with_tree_tiled(c, rpt, resident);
+        instance = 2 + rpt / 2;
+        per_sm = with_tree_tiled(c->head_dim, rpt, resident);
     }
     t.ctas = tree_ctas(t.s, num_seqs, max_q_len, max_seq_len, c->num_kv_heads, per_sm);
     return t;
@@ -362,6 +379,8 @@ size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t total_q, int32_t
     if (tree_ws_shape(cache)) take(kTreeWs);
     if (tree_mma_shape(cache))
         take(kTreeMma);
+    else if (tree_tf_shape(cache))
+        take(kTreeTf);
     else if (tiled_shape(cache))
         take(kTreeTiled);
     return most;
@@ -435,10 +454,11 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
                     aligned(out, 16) && aligned(k_cache, 16) && aligned(v_cache, 16) && scale > 0.f;
     const bool caches16 = aligned(k_cache, 16) && aligned(v_cache, 16);
     const bool mma = !ws && tree_mma_shape(cache) && caches16;
-    const bool tiled = !ws && !mma && !tree_mma_shape(cache) && tiled_shape(cache) && caches16 &&
-                       aligned(out, 16);
-    if (ws || mma || tiled) {
-        const TreeKernel kernel = ws ? kTreeWs : mma ? kTreeMma : kTreeTiled;
+    const bool tf = tree_tf_shape(cache) && caches16 && aligned(out, 16);
+    const bool tiled = cache->dtype == PA_BF16 && !tree_mma_shape(cache) && tiled_shape(cache) &&
+                       caches16 && aligned(out, 16);
+    if (ws || mma || tf || tiled) {
+        const TreeKernel kernel = ws ? kTreeWs : mma ? kTreeMma : tf ? kTreeTf : kTreeTiled;
         const TreeLaunch t = tree_launch(kernel, cache, a.group, num_seqs, max_q_len, max_seq_len);
         // unit costs are 32-bit in the kernels
         const int64_t per = (int64_t)t.s.tokens * t.s.tiles;
@@ -457,8 +477,10 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
         cudaError_t err;
         if (mma)
             err = with_tree_mma(a.head_dim, go);
+        else if (tf)
+            err = with_tree_tf(a.head_dim, go);
         else if (tiled)
-            err = with_tree_tiled(cache, tree_tiled_rpt(a.head_dim, a.group, max_q_len), go);
+            err = with_tree_tiled(a.head_dim, tree_tiled_rpt(a.head_dim, a.group, max_q_len), go);
         else
             err = cache->head_dim == 128 ? launch_tree_ws<128, false>(a, w, cache, t.ctas, st)
                   : cache->head_dim > 64 ? launch_tree_ws<128, true>(a, w, cache, t.ctas, st)

@@ -32,7 +32,7 @@ constexpr int kTreeMmaRows = 64;      // 16 rows a warp
 
 template <int DMAX, int KC>
 struct TreeMmaCfg {
-    static_assert(DMAX % 16 == 0 && KC % 16 == 0, "tile shape");
+    static_assert(DMAX % 16 == 0 && KC % 32 == 0, "tile shape");
     // dynamic shared bytes: q [64][row + 16] | K, V double buffer [KC][row + 16]
     // | visible nodes [64][8] words | parents | odd rows of the chunk
     static size_t smem_bytes(int32_t head_dim) {
@@ -63,7 +63,6 @@ tree_mma_kernel(const TreeArgs a, const TreeWork w) {
     int32_t* odd = up + PA_MAX_TREE_NODES;                      // [KC] key's V had values taken out
     const uint32_t q_u = smem_u32(qsm), kv_u = smem_u32(kvs);
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-    const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(a.k_cache);
     const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(a.v_cache);
 
     TreeIter it = tree_begin(a, w, reinterpret_cast<int64_t*>(sm_tm));
@@ -93,31 +92,27 @@ tree_mma_kernel(const TreeArgs a, const TreeWork w) {
                 for (int32_t e = 0; e < 8; ++e) dst[e] = ok ? src[e] : __float2bfloat16(0.f);
             }
         }
-        auto issue = [&](int32_t c) {
-            const uint32_t kb = kv_u + (c & 1) * 2 * KC * stride;
-            const uint32_t vb = kb + KC * stride;
-            for (int32_t x = tid; x < KC * ppr; x += kTreeMmaThreads) {
-                const int32_t k = x / ppr, piece = x - k * ppr;
-                const int32_t t = c * KC + k;
-                int32_t id = -1;
-                if (t < sg.T) {
-                    id = table[t / BS];
-                    if (id < 0 || id >= a.num_blocks) {
-                        raise_error(PA_DEVERR_TABLE_ENTRY);
-                        id = -1;
-                    }
-                }
-                const int64_t off =
-                    id >= 0 ? (((int64_t)id * a.num_kv_heads + sg.g) * BS + t % BS) * D : 0;
-                const uint32_t bytes = id >= 0 ? 16u : 0u;
-                cp_async16(kb + k * stride + piece * 16,
-                           reinterpret_cast<const uint8_t*>(kc + off) + piece * 16, bytes);
-                cp_async16(vb + k * stride + piece * 16,
-                           reinterpret_cast<const uint8_t*>(vc + off) + piece * 16, bytes);
-            }
+        // Copies of chunk c (keys c KC ..) into buffer c & 1, 32 keys at a time;
+        // keys past the last and keys behind a bad table entry are filled with
+        // zeros.
+        constexpr int32_t kSub = KC / 32;
+        auto find = [&](int32_t c, int64_t (&row)[kSub]) {
+#pragma unroll
+            for (int32_t u = 0; u < kSub; ++u)
+                row[u] = c < sg.kb1 ? tree_row(a, sg, c * KC + u * 32 + lane, warp == 0) : -1;
         };
-        issue(sg.kb0);
-        cp_async_commit();               // q and the first chunk
+        auto issue = [&](int32_t c, const int64_t (&row)[kSub]) {
+            const uint32_t kb = kv_u + (c & 1) * 2 * KC * stride;
+#pragma unroll
+            for (int32_t u = 0; u < kSub; ++u)
+                tree_copy<32>(a, row[u], ppr, kb + u * 32 * stride, stride,
+                              kb + (KC + u * 32) * stride, stride);
+            cp_async_commit();
+        };
+        int64_t row1[kSub];
+        find(sg.kb0, row1);
+        issue(sg.kb0, row1);             // q and the first chunk
+        find(sg.kb0 + 1, row1);
         tree_visible(a, sg, up, bits);
 
         // this lane's two rows: warp * 16 + grp (half 0) and + 8 (half 1)
@@ -137,8 +132,8 @@ tree_mma_kernel(const TreeArgs a, const TreeWork w) {
 
         for (int32_t c = sg.kb0; c < sg.kb1; ++c) {
             if (c + 1 < sg.kb1) {          // next chunk in flight while this one is used
-                issue(c + 1);
-                cp_async_commit();
+                issue(c + 1, row1);
+                find(c + 2, row1);
                 cp_async_wait<1>();
             } else {
                 cp_async_wait<0>();

@@ -17,6 +17,7 @@
 // The cells' number depends on the grid alone, not on the batch.
 #pragma once
 
+#include "cp_async.cuh"
 #include "tree_args.cuh"
 
 namespace pa {
@@ -185,6 +186,49 @@ __device__ __forceinline__ TreeIter tree_begin(const TreeArgs& a, const TreeWork
     it.i = (int32_t)scratch[0];
     it.seq0 = scratch[1];
     return it;
+}
+
+// Copies of a chunk of keys by the four warps of a block.  A lane finds the
+// cache row of one key (tree_row, a chunk ahead of use: one table entry and one
+// division a lane, not one a piece), the warps then take the rows in turn, 16
+// bytes a lane.
+__device__ __forceinline__ int64_t tree_row(const TreeArgs& a, const TreeSeg& s, int32_t key,
+                                            bool report) {
+    if (key >= s.T) return -1;
+    const int32_t b = key / a.block_size;
+    const int32_t id = a.block_tables[(int64_t)s.i * a.max_blocks + b];
+    if (id < 0 || id >= a.num_blocks) {
+        if (report) raise_error(PA_DEVERR_TABLE_ENTRY);
+        return -1;
+    }
+    return ((int64_t)id * a.num_kv_heads + s.g) * a.block_size + (key - b * a.block_size);
+}
+
+// row: this lane's (lane < KC) cache row of its key, -1: zeros.  pieces: 16-byte
+// pieces of a row; kst, vst: row strides in shared memory, bytes.
+template <int KC>
+__device__ __forceinline__ void tree_copy(const TreeArgs& a, int64_t row, int32_t pieces, uint32_t kb,
+                                          int32_t kst, uint32_t vb, int32_t vst) {
+    static_assert(KC <= 32, "a key a lane");
+    const int32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint8_t* kc = static_cast<const uint8_t*>(a.k_cache);
+    const uint8_t* vc = static_cast<const uint8_t*>(a.v_cache);
+    // lanes per row: a power of two up to 32, so short rows go several at a time
+    int32_t shift = 5;
+    while (shift > 0 && (1 << (shift - 1)) >= pieces) --shift;
+    const int32_t p0 = lane & ((1 << shift) - 1), sub = lane >> shift, rows = 32 >> shift;
+#pragma unroll 4
+    for (int32_t k0 = warp * rows; k0 < KC; k0 += 4 * rows) {
+        const int32_t k = k0 + sub;
+        const int64_t r = __shfl_sync(0xffffffffu, row, k & 31);
+        if (k >= KC) continue;
+        const int64_t off = r < 0 ? 0 : r * pieces * 16;
+        const uint32_t bytes = r < 0 ? 0u : 16u;
+        for (int32_t p = p0; p < pieces; p += 32) {
+            cp_async16(kb + k * kst + p * 16, kc + off + p * 16, bytes);
+            cp_async16(vb + k * vst + p * 16, vc + off + p * 16, bytes);
+        }
+    }
 }
 
 // The cell of this CTA's part.

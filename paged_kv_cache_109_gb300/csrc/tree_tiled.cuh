@@ -1,7 +1,6 @@
 // tree_tiled.cuh -- attention of a tree of drafted tokens over the paged cache on
-// CUDA cores, in 32-bit arithmetic: fp32 caches, and bf16 shapes that no
-// tensor-core kernel takes, with head dims up to 256 whose rows are whole
-// 16-byte pieces.
+// CUDA cores, in 32-bit arithmetic, for the bf16 shapes that no tensor-core
+// kernel takes: head dims up to 256 that are multiples of 8 but not of 16.
 //
 // A unit is one tile of R = 16 RPT rows ((node, query head) pairs, head
 // fastest); a persistent CTA of 128 threads takes the parts of its range
@@ -69,7 +68,7 @@ tree_tiled_kernel(const TreeArgs a, const TreeWork w) {
     extern __shared__ __align__(16) uint8_t sm_tt[];
     griddep_wait();                 // inputs may come from the previous kernel
     const int32_t tid = threadIdx.x, rg = tid >> 3, kg = tid & 7;
-    const int32_t D = a.head_dim, G = a.group, BS = a.block_size;
+    const int32_t D = a.head_dim, G = a.group;
     const int32_t HT = w.s.heads;
     const int32_t rowb = D * kE, stride = rowb + 16, ppr = rowb / 16;
     const int32_t qst = D + 4, pst = KC + 4;
@@ -79,8 +78,6 @@ tree_tiled_kernel(const TreeArgs a, const TreeWork w) {
     uint32_t* bits = reinterpret_cast<uint32_t*>(ps + R * pst);           // [tokens][8]
     int32_t* up = reinterpret_cast<int32_t*>(bits + R * kWords);
     const E* q = static_cast<const E*>(a.q);
-    const E* kc = static_cast<const E*>(a.k_cache);
-    const E* vc = static_cast<const E*>(a.v_cache);
 
     TreeIter it = tree_begin(a, w, reinterpret_cast<int64_t*>(sm_tt));
     TreeSeg sg;
@@ -91,42 +88,26 @@ tree_tiled_kernel(const TreeArgs a, const TreeWork w) {
             cut = TreeCut{sg.q0 + sg.tok0, sg.ntok, sg.g, sg.sg, sg.parts, {0, 0, 0}};
         const int32_t hs = min(HT, G - sg.sg * HT);
         const int64_t head_base = (int64_t)sg.g * G + sg.sg * HT;
-        const int32_t* table = a.block_tables + (int64_t)sg.i * a.max_blocks;
         // Copies of chunk c (keys c KC ..) into buffer c & 1; keys past the last
         // and keys behind a bad table entry are filled with zeros.
-        auto issue = [&](int32_t c) {
-            uint8_t* kb = kvs + (c & 1) * 2 * KC * stride;
-            uint8_t* vb = kb + KC * stride;
-            for (int32_t x = tid; x < KC * ppr; x += kTreeTiledThreads) {
-                const int32_t k = x / ppr, piece = x - k * ppr;
-                const int32_t t = c * KC + k;
-                int32_t id = -1;
-                if (t < sg.T) {
-                    id = table[t / BS];
-                    if (id < 0 || id >= a.num_blocks) {
-                        raise_error(PA_DEVERR_TABLE_ENTRY);
-                        id = -1;
-                    }
-                }
-                const int64_t off =
-                    id >= 0 ? (((int64_t)id * a.num_kv_heads + sg.g) * BS + t % BS) * D : 0;
-                const uint32_t bytes = id >= 0 ? 16u : 0u;
-                cp_async16(smem_u32(kb + k * stride + piece * 16),
-                           reinterpret_cast<const uint8_t*>(kc + off) + piece * 16, bytes);
-                cp_async16(smem_u32(vb + k * stride + piece * 16),
-                           reinterpret_cast<const uint8_t*>(vc + off) + piece * 16, bytes);
-            }
+        auto find = [&](int32_t c) {
+            return (tid & 31) < KC && c < sg.kb1 ? tree_row(a, sg, c * KC + (tid & 31), tid < 32) : -1;
         };
-        issue(sg.kb0);
-        cp_async_commit();
-        for (int32_t x = tid; x < R * D; x += kTreeTiledThreads) {
-            const int32_t rho = x / D, d = x - rho * D;
+        auto issue = [&](int32_t c, int64_t row) {
+            const uint32_t kb = smem_u32(kvs + (c & 1) * 2 * KC * stride);
+            tree_copy<KC>(a, row, ppr, kb, stride, kb + KC * stride, stride);
+            cp_async_commit();
+        };
+        issue(sg.kb0, find(sg.kb0));
+        int64_t row1 = find(sg.kb0 + 1);
+        // Q rows, a warp a row (zeros in idle ones)
+#pragma unroll 4
+        for (int32_t rho = tid >> 5; rho < R; rho += kTreeTiledThreads / 32) {
             const int32_t tk = rho / HT, hh = rho - tk * HT;
-            float v = 0.f;
-            if (tk < sg.ntok && hh < hs)
-                v = Elem<E>::to_float(q[((int64_t)(sg.q0 + sg.tok0 + tk) * a.num_q_heads + head_base + hh) * D + d]) *
-                    a.scale_log2;
-            qs[rho * qst + d] = v;
+            const bool live = tk < sg.ntok && hh < hs;
+            const E* src = q + (live ? ((int64_t)(sg.q0 + sg.tok0 + tk) * a.num_q_heads + head_base + hh) * D : 0);
+            for (int32_t d = tid & 31; d < D; d += 32)
+                qs[rho * qst + d] = live ? Elem<E>::to_float(src[d]) * a.scale_log2 : 0.f;
         }
         tree_visible(a, sg, up, bits);
 
@@ -148,8 +129,8 @@ tree_tiled_kernel(const TreeArgs a, const TreeWork w) {
 
         for (int32_t c = sg.kb0; c < sg.kb1; ++c) {
             if (c + 1 < sg.kb1) {      // next chunk in flight while this one is used
-                issue(c + 1);
-                cp_async_commit();
+                issue(c + 1, row1);
+                row1 = find(c + 2);
                 cp_async_wait<1>();
             } else {
                 cp_async_wait<0>();
