@@ -618,16 +618,18 @@ def decode_tree(q, query_start_loc, parents, k_cache, v_cache, block_tables, seq
     [total_q, Hq, D] in the cache dtype; rows behind the last sequence are
     left as they were (a missing ``out`` is allocated, not cleared)."""
     device = _current(k_cache)
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    shape, q_shape, dtype = k_cache.shape, q.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache are [num_blocks, num_kv_heads, block_size, "
                          "head_dim], of one shape")
-    desc = cache_desc(k_cache)
-    d = desc.head_dim
-    if q.dim() != 3 or q.shape[2] != d:
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported cache dtype {dtype}")
+    blocks, heads, block, d = shape
+    desc = CacheDesc(blocks, block, heads, d, _DTYPES[dtype])
+    if len(q_shape) != 3 or q_shape[2] != d:
         raise ValueError(f"q must be [total_q, num_q_heads, {d}]")
-    total, hq, _ = q.shape
+    total, hq, _ = q_shape
     n = seq_lens.numel()
-    dtype = k_cache.dtype
     if q.dtype is not dtype or v_cache.dtype is not dtype:
         raise ValueError("q and caches must share one dtype")
     i32 = torch.int32
@@ -641,15 +643,15 @@ def decode_tree(q, query_start_loc, parents, k_cache, v_cache, block_tables, seq
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q, device=k_cache.device)
-    elif out.shape != q.shape or out.dtype is not dtype:
+        out = torch.empty_like(q) if q.is_cuda else torch.empty_like(q, device=k_cache.device)
+    elif out.shape != q_shape or out.dtype is not dtype:
         raise ValueError("out must have q's shape and dtype")
     lib = load_library()
     ref = ctypes.byref(desc)
     if workspace is None:
         ws_bytes = lib.pa_decode_tree_workspace_bytes(n, total, hq, max_q_len, max_seq_len, ref)
         if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=k_cache.device)
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
     else:
         _dev(workspace)
         ws_bytes = workspace.numel() * workspace.element_size()
@@ -665,29 +667,32 @@ def decode_tree(q, query_start_loc, parents, k_cache, v_cache, block_tables, seq
 
 
 def _layer_caches(caches):
-    """(first layer's cache, addresses of all layers) of one cache, a stack
-    of them, or a sequence."""
+    """(one layer's shape, dtype, device, addresses of all layers) of one
+    cache, a stack of them, or a sequence."""
     if isinstance(caches, torch.Tensor):
-        if not caches.is_contiguous():
-            raise ValueError("tensors must be contiguous")
+        shape = caches.shape
+        if not (caches.is_cuda and caches.is_contiguous()):
+            raise ValueError("caches must be contiguous CUDA tensors")
         base = caches.data_ptr()
-        if caches.dim() == 4:
-            return caches, [base]
-        if caches.dim() != 5 or caches.shape[0] < 1:
+        if len(shape) == 4:
+            return shape, caches.dtype, caches.get_device(), (base,)
+        if len(shape) != 5 or shape[0] < 1:
             raise ValueError("caches are [num_blocks, num_kv_heads, block_size, head_dim], with "
                              "a leading dimension of layers or in a sequence")
         step = caches.stride(0) * caches.element_size()
-        return caches[0], list(range(base, base + step * caches.shape[0], step))
+        return shape[1:], caches.dtype, caches.get_device(), range(base, base + step * shape[0],
+                                                                   step)
     caches = list(caches)
-    if not caches:
-        raise ValueError("no caches")
+    if not caches or caches[0].dim() != 4:
+        raise ValueError("caches are [num_blocks, num_kv_heads, block_size, head_dim], with "
+                         "a leading dimension of layers or in a sequence")
     first = caches[0]
     for c in caches:
         if c.shape != first.shape or c.dtype is not first.dtype or c.device != first.device \
-                or not c.is_contiguous():
-            raise ValueError("the caches must share one shape, dtype and device, and be "
+                or not (c.is_cuda and c.is_contiguous()):
+            raise ValueError("the caches must share one shape, dtype and CUDA device, and be "
                              "contiguous")
-    return first, [c.data_ptr() for c in caches]
+    return first.shape, first.dtype, first.get_device(), [c.data_ptr() for c in caches]
 
 
 def accept_tree(leaf, parents, query_start_loc, seq_lens, k_caches, v_caches, block_tables,
@@ -700,21 +705,24 @@ def accept_tree(leaf, parents, query_start_loc, seq_lens, k_caches, v_caches, bl
     [total_q]): the lengths with the path, and per sequence the packed rows
     of its path from its first row on, then -1 (rows behind the last sequence
     are left as they were)."""
-    first, keys = _layer_caches(k_caches)
-    other, values = _layer_caches(v_caches)
-    device = _current(first)
-    if len(keys) != len(values) or other.shape != first.shape or other.dtype is not first.dtype \
-            or other.get_device() != device:
+    shape, dtype, device, keys = _layer_caches(k_caches)
+    v_shape, v_dtype, v_device, values = _layer_caches(v_caches)
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors live on device {device}, which is not the current one")
+    if len(keys) != len(values) or v_shape != shape or v_dtype is not dtype \
+            or v_device != device:
         raise ValueError("k_caches and v_caches must have the same layers, shape and dtype")
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported cache dtype {dtype}")
     n, total = seq_lens.numel(), parents.numel()
     if leaf.numel() != n or query_start_loc.numel() != n + 1 or block_tables.dim() != 2 \
             or block_tables.shape[0] != n:
         raise ValueError("leaf, query_start_loc, block_tables and seq_lens disagree on the "
                          "sequence count")
     if new_lens is None:
-        new_lens = torch.empty(n, dtype=torch.int32, device=first.device)
+        new_lens = torch.empty(n, dtype=torch.int32, device=device)
     if accepted_rows is None:
-        accepted_rows = torch.empty(total, dtype=torch.int32, device=first.device)
+        accepted_rows = torch.empty(total, dtype=torch.int32, device=device)
     if new_lens.numel() != n or accepted_rows.numel() != total:
         raise ValueError("new_lens must have N and accepted_rows total_q entries")
     ints = (leaf, parents, query_start_loc, seq_lens, block_tables, new_lens, accepted_rows)
@@ -724,11 +732,12 @@ def accept_tree(leaf, parents, query_start_loc, seq_lens, k_caches, v_caches, bl
             raise ValueError("all arguments but the caches must be int32")
     _step_args(device, *ints)
     ptrs = ctypes.c_void_p * len(keys)
+    desc = CacheDesc(shape[0], shape[2], shape[1], shape[3], _DTYPES[dtype])
     st = load_library().pa_accept_tree(
         leaf.data_ptr(), parents.data_ptr(), query_start_loc.data_ptr(), seq_lens.data_ptr(), n,
         total, max_q_len, block_tables.data_ptr(), block_tables.shape[1], ptrs(*keys),
         ptrs(*values), len(keys), new_lens.data_ptr(), accepted_rows.data_ptr(),
-        ctypes.byref(cache_desc(first)), _raw_stream(stream, device))
+        ctypes.byref(desc), _raw_stream(stream, device))
     if st != PA_OK:
         raise PaError(st, "pa_accept_tree")
     return new_lens, accepted_rows

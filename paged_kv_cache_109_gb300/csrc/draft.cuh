@@ -15,6 +15,19 @@
 namespace pa {
 namespace {
 
+// Lets `kern` use `bytes` of shared memory on the current device: asked for once
+// per instance (its slot in `done`, a bit a device), with the most it ever uses.
+template <typename Kern>
+bool allow_smem(std::atomic<uint64_t>& done, Kern kern, size_t bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return set_smem(kern, bytes);
+    const uint64_t bit = 1ull << dev;
+    if (done.load(std::memory_order_acquire) & bit) return true;
+    if (!set_smem(kern, bytes)) return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
+}
+
 // Device memory of the current device (or managed memory).
 bool current_device_memory(const void* p) {
     if (!p) return false;
@@ -34,11 +47,14 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 }
 
 pa_status plan_impl(PlanArgs a, cudaStream_t st) {
-    cudaError_t err = launch_pdl(plan_scan_kernel, dim3(1), dim3(kPlanScanThreads), 0, st, a);
+    const bool small = a.num_seqs <= kPlanSmallSeqs && a.max_tokens <= kPlanSmallTokens;
+    cudaError_t err = launch_pdl(small ? plan_scan_kernel<true> : plan_scan_kernel<false>, dim3(1),
+                                 dim3(kPlanScanThreads), 0, st, a);
     if (err != cudaSuccess) return PA_ERR_CUDA;
-    // at most a token, and at most a fresh block a token, per thread and round
+    if (small) return PA_OK;
+    // a thread per four tokens (and at most that many fresh blocks), 8 CTAs a SM
     const int64_t sms = std::max(1, device_sm_count());
-    const int64_t want = ((int64_t)a.max_tokens + kPlanFillThreads - 1) / kPlanFillThreads;
+    const int64_t want = ((int64_t)a.max_tokens + 4 * kPlanFillThreads - 1) / (4 * kPlanFillThreads);
     const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, sms * 8));
     err = launch_pdl(plan_fill_kernel, dim3(grid), dim3(kPlanFillThreads), 0, st, a);
     return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
@@ -113,23 +129,34 @@ TreeShape tree_ws_tiling(int32_t group) {
     return s;
 }
 
-// The mma.sync kernel: 64 rows, 64-key chunks up to 128 columns, 32-key ones
-// up to 256.
+// Warps of a CTA of the mma.sync and tf32 kernels, 16 rows each.  Up to 128
+// columns the fewest of one, two and four that cover a sequence's rows, since
+// more CTAs then share an SM (16 rows, D = 128, block size 4, 38 sequences x 4000
+// tokens: 204 us with one warp, 350 with four of which one works); above, four:
+// shared memory leaves room for few CTAs, and the other warps help to copy (D =
+// 256: 508 us with four, 725 with one).
+int32_t tree_row_warps(int32_t head_dim, int32_t group, int32_t max_q_len) {
+    const int64_t rows = head_dim > 128 ? 64 : (int64_t)group * max_q_len;
+    return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+}
+
+// The mma.sync kernel: 64-key chunks up to 128 columns (32-key ones for fewer
+// than four warps), 32-key ones up to 256.
 bool tree_mma_shape(const pa_cache_desc* c) {
     return c->dtype == PA_BF16 && c->head_dim % 16 == 0 && c->head_dim <= 256;
 }
-TreeShape tree_mma_tiling(int32_t head_dim, int32_t group) {
-    TreeShape s = tree_shape(kTreeMmaRows, 1, head_dim <= 128 ? 64 : 32, group);
+TreeShape tree_mma_tiling(int32_t head_dim, int32_t group, int32_t warps) {
+    TreeShape s = tree_shape(16 * warps, 1, head_dim <= 128 && warps == 4 ? 64 : 32, group);
     s.overhead = 2;
     s.min_range = 8;
     return s;
 }
 
-// The tf32 kernel of fp32 caches: 64 rows, 32-key chunks up to 128 columns,
-// 16-key ones up to 256.
+// The tf32 kernel of fp32 caches: 32-key chunks for four warps and up to 128
+// columns, else 16-key ones.
 bool tree_tf_shape(const pa_cache_desc* c) { return c->dtype == PA_F32 && tiled_shape(c); }
-TreeShape tree_tf_tiling(int32_t head_dim, int32_t group) {
-    TreeShape s = tree_shape(kTreeTfRows, 1, head_dim <= 128 ? 32 : 16, group);
+TreeShape tree_tf_tiling(int32_t head_dim, int32_t group, int32_t warps) {
+    TreeShape s = tree_shape(16 * warps, 1, head_dim <= 128 && warps == 4 ? 32 : 16, group);
     s.overhead = 2;
     s.min_range = 8;
     return s;
@@ -149,11 +176,11 @@ TreeShape tree_tiled_tiling(int32_t head_dim, int32_t group, int32_t max_q_len) 
     return s;
 }
 
-// CTAs of `kern` one SM holds, per instance (0-4) and head dim (which sets its
+// CTAs of `kern` one SM holds, per instance (0-14) and head dim (which sets its
 // shared memory).
 template <typename Kern>
 int32_t tree_per_sm(int instance, Kern kern, int threads, size_t smem, int32_t head_dim) {
-    static std::atomic<int> table[5][257];
+    static std::atomic<int> table[15][257];
     std::atomic<int>* cached = table[instance];
     int n = cached[head_dim].load(std::memory_order_relaxed);
     if (n > 0) return n;
@@ -166,22 +193,32 @@ int32_t tree_per_sm(int instance, Kern kern, int threads, size_t smem, int32_t h
     return 1;
 }
 
-// Calls f(kernel, threads, shared bytes) with the mma.sync instance of a head dim.
-template <typename F>
-auto with_tree_mma(int32_t head_dim, F f) {
-    if (head_dim <= 128)
-        return f(tree_mma_kernel<128, 64>, kTreeMmaThreads, TreeMmaCfg<128, 64>::smem_bytes(head_dim));
-    return f(tree_mma_kernel<256, 32>, kTreeMmaThreads, TreeMmaCfg<256, 32>::smem_bytes(head_dim));
+// Calls f(kernel, threads, shared bytes) with the instance of a head dim and
+// warps: of the mma.sync, the tf32 and the CUDA-core kernel.
+template <int DMAX, int KC, int WARPS, typename F>
+auto call_tree_mma(int32_t head_dim, F f) {
+    using C = TreeMmaCfg<DMAX, KC, WARPS>;
+    return f(tree_mma_kernel<DMAX, KC, WARPS>, C::kThreads, C::smem_bytes(head_dim));
 }
-
-// The same with the tf32 instance, and with the CUDA-core one.
 template <typename F>
-auto with_tree_tf(int32_t head_dim, F f) {
-    if (head_dim <= 128)
-        return f(tree_tf32_kernel<128, 32>, kTreeTfThreads, TreeTfCfg<128, 32>::smem_bytes(head_dim));
-    return f(tree_tf32_kernel<256, 16>, kTreeTfThreads, TreeTfCfg<256, 16>::smem_bytes(head_dim));
+auto with_tree_mma(int32_t head_dim, int32_t warps, F f) {
+    if (head_dim > 128) return call_tree_mma<256, 32, 4>(head_dim, f);
+    return warps == 1   ? call_tree_mma<128, 32, 1>(head_dim, f)
+           : warps == 2 ? call_tree_mma<128, 32, 2>(head_dim, f)
+                        : call_tree_mma<128, 64, 4>(head_dim, f);
 }
-
+template <int DMAX, int KC, int WARPS, typename F>
+auto call_tree_tf(int32_t head_dim, F f) {
+    using C = TreeTfCfg<DMAX, KC, WARPS>;
+    return f(tree_tf32_kernel<DMAX, KC, WARPS>, C::kThreads, C::smem_bytes(head_dim));
+}
+template <typename F>
+auto with_tree_tf(int32_t head_dim, int32_t warps, F f) {
+    if (head_dim > 128) return call_tree_tf<256, 16, 4>(head_dim, f);
+    return warps == 1   ? call_tree_tf<128, 16, 1>(head_dim, f)
+           : warps == 2 ? call_tree_tf<128, 16, 2>(head_dim, f)
+                        : call_tree_tf<128, 32, 4>(head_dim, f);
+}
 template <typename F>
 auto with_tree_tiled(int32_t head_dim, int32_t rpt, F f) {
     using E = __nv_bfloat16;
@@ -204,11 +241,12 @@ auto with_tree_tiled(int32_t head_dim, int32_t rpt, F f) {
 enum TreeKernel { kTreeWs, kTreeMma, kTreeTf, kTreeTiled };
 struct TreeLaunch {
     TreeShape s;
-    int32_t ctas;
+    int32_t ctas, warps;
 };
 TreeLaunch tree_launch(TreeKernel k, const pa_cache_desc* c, int32_t group, int32_t num_seqs,
                        int32_t max_q_len, int32_t max_seq_len) {
     TreeLaunch t{};
+    t.warps = tree_row_warps(c->head_dim, group, max_q_len);
     int32_t per_sm = 1, instance = 0;
     auto resident = [&](auto kern, int threads, size_t smem) {
         return tree_per_sm(instance, kern, threads, smem, c->head_dim);
@@ -216,16 +254,17 @@ TreeLaunch tree_launch(TreeKernel k, const pa_cache_desc* c, int32_t group, int3
     if (k == kTreeWs) {
         t.s = tree_ws_tiling(group);
     } else if (k == kTreeMma) {
-        t.s = tree_mma_tiling(c->head_dim, group);
-        per_sm = with_tree_mma(c->head_dim, resident);
+        t.s = tree_mma_tiling(c->head_dim, group, t.warps);
+        instance = t.warps;
+        per_sm = with_tree_mma(c->head_dim, t.warps, resident);
     } else if (k == kTreeTf) {
-        t.s = tree_tf_tiling(c->head_dim, group);
-        instance = 1;
-        per_sm = with_tree_tf(c->head_dim, resident);
+        t.s = tree_tf_tiling(c->head_dim, group, t.warps);
+        instance = 5 + t.warps;
+        per_sm = with_tree_tf(c->head_dim, t.warps, resident);
     } else {
         t.s = tree_tiled_tiling(c->head_dim, group, max_q_len);
         const int32_t rpt = tree_tiled_rpt(c->head_dim, group, max_q_len);
-        instance = 2 + rpt / 2;
+        instance = 10 + rpt;
         per_sm = with_tree_tiled(c->head_dim, rpt, resident);
     }
     t.ctas = tree_ctas(t.s, num_seqs, max_q_len, max_seq_len, c->num_kv_heads, per_sm);
@@ -279,7 +318,8 @@ cudaError_t launch_tree_ws(const TreeArgs& a, const TreeWork& w, const pa_cache_
     if (!encode_tree_q(&mq, a, w.s) || !encode_tree_map(&mk, a.k_cache, c, rows) || !encode_tree_map(&mv, a.v_cache, c, rows))
         return cudaErrorUnknown;
     auto kern = tree_ws_kernel<D, SPLIT>;
-    if (!set_smem(kern, Cfg::smem_bytes())) return cudaErrorUnknown;
+    static std::atomic<uint64_t> allowed;
+    if (!allow_smem(allowed, kern, Cfg::smem_bytes())) return cudaErrorUnknown;
     return launch_pdl(kern, dim3(ctas), dim3(Cfg::kThreads), Cfg::smem_bytes(), st, mq, mk, mv,
                       a, w, rows);
 }
@@ -288,8 +328,11 @@ template <typename E>
 cudaError_t launch_tree_merge(const TreeArgs& a, const TreeWork& w, int32_t ctas, cudaStream_t st) {
     if (w.cuts == nullptr || ctas == 1) return cudaSuccess;
     // (the last CTA's range ends with the work)
-    return launch_pdl(tree_merge_kernel<E>, dim3(ctas - 1, kTreeMergeSplit),
-                      dim3(kTreeMergeThreads), 0, st, a, w);
+    const int32_t rows = std::min(a.max_q_len, w.s.tokens * w.s.tiles) * w.s.heads;
+    const int32_t items = std::min(rows, w.s.rows * w.s.tiles) * ((a.head_dim + 7) / 8);
+    const int32_t split = std::min(kTreeMergeSplit, (items + kTreeMergeThreads - 1) / kTreeMergeThreads);
+    return launch_pdl(tree_merge_kernel<E>, dim3(ctas - 1, split), dim3(kTreeMergeThreads), 0, st, a,
+                      w);
 }
 
 }  // namespace
@@ -476,9 +519,9 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
         };
         cudaError_t err;
         if (mma)
-            err = with_tree_mma(a.head_dim, go);
+            err = with_tree_mma(a.head_dim, t.warps, go);
         else if (tf)
-            err = with_tree_tf(a.head_dim, go);
+            err = with_tree_tf(a.head_dim, t.warps, go);
         else if (tiled)
             err = with_tree_tiled(a.head_dim, tree_tiled_rpt(a.head_dim, a.group, max_q_len), go);
         else

@@ -6,12 +6,17 @@
 //   g_i = max(0, ceil((C_i + n_i) / B) - h_i)
 //   Q = exclusive sum of n, S = exclusive sum of g
 //   table[i][h_i + k] = free[F + S_i + k],  slot(Q_i + j) through position C_i + j.
-// Two launches.  plan_scan_kernel, one CTA: the totals decide whether the step
-// fits (all or nothing), then the running sums and the per-sequence outputs
-// are written.  plan_fill_kernel, a CTA per tile of tokens and of fresh table
-// entries: each finds its sequence by binary search in Q (or S).  A token's
-// block is taken from the table below h_i and straight from the queue above
-// it, so no thread reads an entry that another one writes.
+// plan_scan_kernel, one CTA: the totals decide whether the step fits (all or
+// nothing), then the running sums and the per-sequence outputs are written.  A
+// token's block is taken from the table below h_i and straight from the queue
+// above it, so no thread reads an entry that another one writes.  A small step
+// (up to kPlanSmallSeqs sequences and kPlanSmallTokens tokens) ends in the same
+// CTA: one launch, whose latency is what such a step costs (a second launch
+// adds 2.5 us on the host).  Otherwise plan_fill_kernel writes tokens and fresh
+// entries from the whole GPU: bound by its 16 bytes a token.  A thread takes four
+// consecutive tokens, one binary search in Q and one table entry for them as
+// long as they share a block, and 16-byte stores (a search a token: 22 us for
+// 2.1 million tokens, bound by its loads; this way 9).
 #pragma once
 
 #include "common.cuh"
@@ -62,20 +67,159 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, int32_t i, unsign
 }
 
 constexpr int kPlanScanThreads = 1024;
+constexpr int kPlanHeld = 4;            // sequences a thread keeps in registers
+constexpr int kPlanSmallSeqs = 1024, kPlanSmallTokens = 8192;
 
+// Last i in [0, n) with start[i] <= x (start[0] <= x).
+__device__ __forceinline__ int32_t plan_find(const int32_t* start, int32_t n, int32_t x) {
+    int32_t lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) / 2;
+        if (start[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Block of the queue, -1 and a report for an id outside the pool.
+__device__ __forceinline__ int32_t plan_free(const PlanArgs& a, int32_t at) {
+    const int32_t id = a.free_blocks[at];
+    if (id < 0 || id >= a.num_blocks) {
+        raise_error(PA_DEVERR_TABLE_ENTRY);
+        return -1;
+    }
+    return id;
+}
+
+// What the fill reads: the sums and the per-sequence results, in global memory
+// or (small steps) in shared memory.
+struct PlanSums {
+    const int32_t *query_start, *block_start, *lens, *held;   // [N + 1], [N + 1], [N], [N]
+    int32_t tokens, blocks, head;
+};
+
+// One sequence of the fill.
+struct PlanSpan {
+    int32_t i, q0, q1, pos0, held, taken, take0;   // tokens [q0, q1) from position pos0
+};
+__device__ __forceinline__ PlanSpan plan_span(const PlanSums& s, int32_t i) {
+    PlanSpan p;
+    p.i = i;
+    p.q0 = s.query_start[i];
+    p.q1 = s.query_start[i + 1];
+    p.take0 = s.block_start[i];
+    p.taken = s.block_start[i + 1] - p.take0;
+    p.held = s.held[i] - p.taken;
+    p.pos0 = s.lens[i] - (p.q1 - p.q0);
+    return p;
+}
+
+// Fresh table entries and tokens: thread `first` of `stride`.
+__device__ __forceinline__ void plan_fill(const PlanArgs& a, const PlanSums& s, int32_t first,
+                                          int32_t stride) {
+    const int32_t N = a.num_seqs, B = a.block_size;
+    for (int32_t e = first; e < s.blocks; e += stride) {
+        const int32_t i = plan_find(s.block_start, N, e);
+        const int32_t b0 = s.block_start[i];
+        const int32_t held = s.held[i] - (s.block_start[i + 1] - b0);
+        const int32_t id = plan_free(a, s.head + e);
+        a.block_tables[(int64_t)i * a.max_blocks + held + (e - b0)] = id;
+        if (a.ref_cnt != nullptr && id >= 0) a.ref_cnt[id] = 1;
+    }
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.slot_mapping) |
+                        reinterpret_cast<uintptr_t>(a.positions) |
+                        reinterpret_cast<uintptr_t>(a.seq_ids)) & 15) == 0;
+    const int32_t groups = a.max_tokens / 4 + (a.max_tokens % 4 != 0);
+    for (int32_t g = first; g < groups; g += stride) {
+        const int32_t t0 = 4 * g;
+        int64_t slot[4];
+        int32_t pos[4], seq[4];
+        PlanSpan p{-1, 0, 0, 0, 0, 0, 0};
+        int32_t block = -1, id = -1;                  // table column of `id`
+        if (t0 < s.tokens) p = plan_span(s, plan_find(s.query_start, N, t0));
+#pragma unroll
+        for (int32_t u = 0; u < 4; ++u) {
+            const int32_t t = t0 + u;
+            slot[u] = -1;
+            pos[u] = seq[u] = -1;
+            if (t >= s.tokens) continue;
+            while (t >= p.q1) {                       // (sequences without tokens are passed)
+                p = plan_span(s, p.i + 1);
+                block = -1;
+            }
+            pos[u] = p.pos0 + (t - p.q0);
+            seq[u] = p.i;
+            const int32_t b = pos[u] / B;
+            if (b != block) {
+                block = b;
+                if (b < p.held) {
+                    id = a.block_tables[(int64_t)p.i * a.max_blocks + b];
+                    if (id < 0 || id >= a.num_blocks) {
+                        raise_error(PA_DEVERR_TABLE_ENTRY);
+                        id = -1;
+                    }
+                } else {
+                    id = plan_free(a, s.head + p.take0 + (b - p.held));
+                }
+            }
+            if (id >= 0) slot[u] = (int64_t)id * B + (pos[u] - b * B);
+        }
+        if (wide && t0 + 4 <= a.max_tokens) {
+            longlong2* out = reinterpret_cast<longlong2*>(a.slot_mapping + t0);
+            out[0] = make_longlong2(slot[0], slot[1]);
+            out[1] = make_longlong2(slot[2], slot[3]);
+            if (a.positions != nullptr)
+                *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            if (a.seq_ids != nullptr)
+                *reinterpret_cast<int4*>(a.seq_ids + t0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+        } else {
+#pragma unroll
+            for (int32_t u = 0; u < 4; ++u) {
+                if (t0 + u >= a.max_tokens) continue;
+                a.slot_mapping[t0 + u] = slot[u];
+                if (a.positions != nullptr) a.positions[t0 + u] = pos[u];
+                if (a.seq_ids != nullptr) a.seq_ids[t0 + u] = seq[u];
+            }
+        }
+    }
+}
+
+// SMALL: the whole step in this CTA (num_seqs <= kPlanSmallSeqs).
+template <bool SMALL>
 __global__ void __launch_bounds__(kPlanScanThreads) plan_scan_kernel(const PlanArgs a) {
     __shared__ int64_t s_new[32], s_grow[32];
     __shared__ unsigned int s_bad[32];
+    __shared__ int32_t s_sums[SMALL ? 4 * (kPlanSmallSeqs + 1) : 1];
+    int32_t* s_query = s_sums;
+    int32_t* s_block = s_query + (SMALL ? kPlanSmallSeqs + 1 : 0);
+    int32_t* s_lens = s_block + (SMALL ? kPlanSmallSeqs + 1 : 0);
+    int32_t* s_held = s_lens + (SMALL ? kPlanSmallSeqs + 1 : 0);
     griddep_wait();
+    griddep_launch_dependents();
     const int32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t head = *a.free_head;
-    // totals: does the step fit?
+    // A round takes the next 4096 sequences (1024 in a small step), a thread
+    // consecutive ones.  The first pass adds them all up: does the step fit?  A
+    // batch of one round stays in registers for the second.
+    constexpr int32_t kPer = SMALL ? 1 : kPlanHeld;
+    const int32_t rounds = (a.num_seqs + kPer * kPlanScanThreads - 1) / (kPer * kPlanScanThreads);
+    PlanSeq s[kPer];
     int64_t add = 0, grow = 0;
     unsigned int bad = 0;
-    for (int32_t i = tid; i < a.num_seqs; i += kPlanScanThreads) {
-        const PlanSeq s = plan_seq(a, i, bad);
-        add += s.add;
-        grow += s.grow;
+    auto read = [&](int32_t round, unsigned int& why) {
+#pragma unroll
+        for (int32_t u = 0; u < kPer; ++u) {
+            const int32_t i = (round * kPlanScanThreads + tid) * kPer + u;
+            s[u] = PlanSeq{0, 0, 0, 0};
+            if (i < a.num_seqs) s[u] = plan_seq(a, i, why);
+        }
+    };
+    for (int32_t r = 0; r < rounds; ++r) {
+        read(r, bad);
+#pragma unroll
+        for (int32_t u = 0; u < kPer; ++u) {
+            add += s[u].add;
+            grow += s[u].grow;
+        }
     }
     for (int off = 16; off > 0; off >>= 1) {
         add += __shfl_xor_sync(0xffffffffu, add, off);
@@ -101,17 +245,19 @@ __global__ void __launch_bounds__(kPlanScanThreads) plan_scan_kernel(const PlanA
     const bool fits = bad == 0;
     if (tid == 0 && !fits) raise_error(bad);
     __syncthreads();
-    // running sums over tiles of 1024 sequences (fits: they stay in 32 bits)
+    // running sums (fits: they stay in 32 bits)
     int32_t q0 = 0, b0 = 0;
-    for (int32_t i0 = 0; i0 < a.num_seqs; i0 += kPlanScanThreads) {
-        const int32_t i = i0 + tid;
-        PlanSeq s{0, 0, 0, 0};
-        if (i < a.num_seqs) {
-            unsigned int ignored = 0;
-            s = plan_seq(a, i, ignored);
+    for (int32_t r = 0; r < rounds; ++r) {
+        unsigned int ignored = 0;
+        if (rounds > 1) read(r, ignored);
+        int32_t mq = 0, mb = 0;
+#pragma unroll
+        for (int32_t u = 0; u < kPer; ++u) {
+            if (!fits) s[u].add = s[u].grow = 0;
+            mq += s[u].add;
+            mb += s[u].grow;
         }
-        if (!fits) s.add = s.grow = 0;
-        int32_t qi = s.add, bi = s.grow;
+        int32_t qi = mq, bi = mb;
         for (int off = 1; off < 32; off <<= 1) {
             const int32_t x = __shfl_up_sync(0xffffffffu, qi, off);
             const int32_t y = __shfl_up_sync(0xffffffffu, bi, off);
@@ -136,41 +282,42 @@ __global__ void __launch_bounds__(kPlanScanThreads) plan_scan_kernel(const PlanA
         }
         const int32_t before_q = warp ? __shfl_sync(0xffffffffu, wq, max(warp - 1, 0)) : 0;
         const int32_t before_b = warp ? __shfl_sync(0xffffffffu, wb, max(warp - 1, 0)) : 0;
-        if (i < a.num_seqs) {
-            a.query_start[i] = q0 + before_q + qi - s.add;
-            a.block_start[i] = b0 + before_b + bi - s.grow;
-            a.seq_lens_out[i] = s.len + s.add;
-            a.blocks_held_out[i] = s.held + s.grow;
+        int32_t q = q0 + before_q + qi - mq, b = b0 + before_b + bi - mb;
+#pragma unroll
+        for (int32_t u = 0; u < kPer; ++u) {
+            const int32_t i = (r * kPlanScanThreads + tid) * kPer + u;
+            if (i < a.num_seqs) {
+                a.query_start[i] = q;
+                a.block_start[i] = b;
+                a.seq_lens_out[i] = s[u].len + s[u].add;
+                a.blocks_held_out[i] = s[u].held + s[u].grow;
+                if constexpr (SMALL) {
+                    s_query[i] = q;
+                    s_block[i] = b;
+                    s_lens[i] = s[u].len + s[u].add;
+                    s_held[i] = s[u].held + s[u].grow;
+                }
+                q += s[u].add;
+                b += s[u].grow;
+            }
         }
         q0 += __shfl_sync(0xffffffffu, wq, 31);
         b0 += __shfl_sync(0xffffffffu, wb, 31);
-        __syncthreads();                          // s_new, s_grow free for the next tile
+        __syncthreads();                          // s_new, s_grow free for the next round
     }
     if (tid == 0) {
         a.query_start[a.num_seqs] = q0;
         a.block_start[a.num_seqs] = b0;
         *a.free_head_out = head + b0;
+        if constexpr (SMALL) {
+            s_query[a.num_seqs] = q0;
+            s_block[a.num_seqs] = b0;
+        }
     }
-}
-
-// Last i in [0, n) with start[i] <= x (start[0] <= x).
-__device__ __forceinline__ int32_t plan_find(const int32_t* start, int32_t n, int32_t x) {
-    int32_t lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int32_t mid = (lo + hi + 1) / 2;
-        if (start[mid] <= x) lo = mid; else hi = mid - 1;
+    if constexpr (SMALL) {
+        __syncthreads();
+        plan_fill(a, PlanSums{s_query, s_block, s_lens, s_held, q0, b0, head}, tid, kPlanScanThreads);
     }
-    return lo;
-}
-
-// Block of the queue, -1 and a report for an id outside the pool.
-__device__ __forceinline__ int32_t plan_free(const PlanArgs& a, int32_t at) {
-    const int32_t id = a.free_blocks[at];
-    if (id < 0 || id >= a.num_blocks) {
-        raise_error(PA_DEVERR_TABLE_ENTRY);
-        return -1;
-    }
-    return id;
 }
 
 constexpr int kPlanFillThreads = 256;
@@ -178,44 +325,10 @@ constexpr int kPlanFillThreads = 256;
 __global__ void __launch_bounds__(kPlanFillThreads) plan_fill_kernel(const PlanArgs a) {
     griddep_wait();
     griddep_launch_dependents();
-    const int32_t N = a.num_seqs, B = a.block_size;
-    const int32_t tokens = a.query_start[N], blocks = a.block_start[N];
-    const int32_t head = *a.free_head_out - blocks;
-    const int32_t stride = gridDim.x * kPlanFillThreads;
-    const int32_t first = blockIdx.x * kPlanFillThreads + threadIdx.x;
-    for (int32_t e = first; e < blocks; e += stride) {
-        const int32_t i = plan_find(a.block_start, N, e);
-        const int32_t held = a.blocks_held_out[i] - (a.block_start[i + 1] - a.block_start[i]);
-        const int32_t id = plan_free(a, head + e);
-        a.block_tables[(int64_t)i * a.max_blocks + held + (e - a.block_start[i])] = id;
-        if (a.ref_cnt != nullptr && id >= 0) a.ref_cnt[id] = 1;
-    }
-    for (int32_t t = first; t < a.max_tokens; t += stride) {
-        int32_t i = -1, p = -1;
-        int64_t slot = -1;
-        if (t < tokens) {
-            i = plan_find(a.query_start, N, t);
-            const int32_t q0 = a.query_start[i], add = a.query_start[i + 1] - q0;
-            const int32_t took = a.block_start[i + 1] - a.block_start[i];
-            const int32_t held = a.blocks_held_out[i] - took;
-            p = a.seq_lens_out[i] - add + (t - q0);
-            const int32_t b = p / B;
-            int32_t id;
-            if (b < held) {
-                id = a.block_tables[(int64_t)i * a.max_blocks + b];
-                if (id < 0 || id >= a.num_blocks) {
-                    raise_error(PA_DEVERR_TABLE_ENTRY);
-                    id = -1;
-                }
-            } else {
-                id = plan_free(a, head + a.block_start[i] + (b - held));
-            }
-            if (id >= 0) slot = (int64_t)id * B + p % B;
-        }
-        a.slot_mapping[t] = slot;
-        if (a.positions != nullptr) a.positions[t] = p;
-        if (a.seq_ids != nullptr) a.seq_ids[t] = i;
-    }
+    const int32_t tokens = a.query_start[a.num_seqs], blocks = a.block_start[a.num_seqs];
+    plan_fill(a, PlanSums{a.query_start, a.block_start, a.seq_lens_out, a.blocks_held_out, tokens,
+                          blocks, *a.free_head_out - blocks},
+              blockIdx.x * kPlanFillThreads + threadIdx.x, gridDim.x * kPlanFillThreads);
 }
 
 }  // namespace pa

@@ -4,9 +4,9 @@
 // block sizes that are not multiples of 8, queries in host memory, unaligned
 // outputs, scale <= 0).
 //
-// A unit is one tile of 64 rows ((node, query head) pairs, head fastest), 16 a
-// warp; a persistent CTA of four warps takes the parts of its range
-// (tree_sched.cuh) one after another.  Keys come in chunks of KC through a
+// A unit is one tile of 16 rows a warp ((node, query head) pairs, head fastest);
+// a persistent CTA of one, two or four warps, the fewest that cover a sequence's
+// rows, takes the parts of its range (tree_sched.cuh) one after another.  Keys come in chunks of KC through a
 // double buffer of 16-byte cp.async copies, rows padded by 16 bytes so that an
 // ldmatrix reads eight bank groups:
 //   S = Q K^T, online softmax in base 2, O += P V with P as bf16 hi + lo (about
@@ -27,24 +27,27 @@
 
 namespace pa {
 
-constexpr int kTreeMmaThreads = 128;
-constexpr int kTreeMmaRows = 64;      // 16 rows a warp
-
-template <int DMAX, int KC>
+template <int DMAX, int KC, int WARPS>
 struct TreeMmaCfg {
     static_assert(DMAX % 16 == 0 && KC % 32 == 0, "tile shape");
-    // dynamic shared bytes: q [64][row + 16] | K, V double buffer [KC][row + 16]
-    // | visible nodes [64][8] words | parents | odd rows of the chunk
+    static constexpr int kThreads = 32 * WARPS;
+    static constexpr int kRows = 16 * WARPS;
+    // CTAs an SM holds at DMAX columns (the registers' limit for the compiler)
+    static constexpr int kPerSm = WARPS == 4 ? 2 : 4;
+
+    // dynamic shared bytes: q [rows][row + 16] | K, V double buffer [KC][row + 16]
+    // | visible nodes [rows][8] words | parents | odd rows of the chunk
     static size_t smem_bytes(int32_t head_dim) {
         const size_t stride = (size_t)head_dim * 2 + 16;
-        return kTreeMmaRows * stride + 4 * (size_t)KC * stride +
-               kTreeMmaRows * (PA_MAX_TREE_NODES / 8) + PA_MAX_TREE_NODES * 4 + KC * 4;
+        return kRows * stride + 4 * (size_t)KC * stride +
+               kRows * (PA_MAX_TREE_NODES / 8) + PA_MAX_TREE_NODES * 4 + KC * 4;
     }
 };
 
-template <int DMAX, int KC>
-__global__ void __launch_bounds__(kTreeMmaThreads)
+template <int DMAX, int KC, int WARPS>
+__global__ void __launch_bounds__(TreeMmaCfg<DMAX, KC, WARPS>::kThreads, TreeMmaCfg<DMAX, KC, WARPS>::kPerSm)
 tree_mma_kernel(const TreeArgs a, const TreeWork w) {
+    using C = TreeMmaCfg<DMAX, KC, WARPS>;
     constexpr int NT = KC / 8;           // key n-tiles of S
     constexpr int DT = DMAX / 8;         // column n-tiles of O
     constexpr int kWords = PA_MAX_TREE_NODES / 32;
@@ -57,9 +60,9 @@ tree_mma_kernel(const TreeArgs a, const TreeWork w) {
     const int32_t HT = w.s.heads;
     const int32_t rowb = D * 2, stride = rowb + 16, ppr = rowb / 16;
     uint8_t* qsm = sm_tm;                                       // [64][stride]
-    uint8_t* kvs = sm_tm + kTreeMmaRows * stride;               // [2][K, V][KC][stride]
+    uint8_t* kvs = sm_tm + C::kRows * stride;               // [2][K, V][KC][stride]
     uint32_t* bits = reinterpret_cast<uint32_t*>(kvs + 4 * KC * stride);   // [tokens][8]
-    int32_t* up = reinterpret_cast<int32_t*>(bits + kTreeMmaRows * kWords);
+    int32_t* up = reinterpret_cast<int32_t*>(bits + C::kRows * kWords);
     int32_t* odd = up + PA_MAX_TREE_NODES;                      // [KC] key's V had values taken out
     const uint32_t q_u = smem_u32(qsm), kv_u = smem_u32(kvs);
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
@@ -78,7 +81,7 @@ tree_mma_kernel(const TreeArgs a, const TreeWork w) {
         // Q rows of the tile (zeros for idle rows; plain loads where q is not
         // 16-byte aligned)
         const bool q16 = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0;
-        for (int32_t x = tid; x < kTreeMmaRows * ppr; x += kTreeMmaThreads) {
+        for (int32_t x = tid; x < C::kRows * ppr; x += C::kThreads) {
             const int32_t rho = x / ppr, piece = x - rho * ppr;
             const int32_t tk = rho / HT, hh = rho - tk * HT;
             const bool ok = tk < sg.ntok && hh < hs;
@@ -96,23 +99,23 @@ tree_mma_kernel(const TreeArgs a, const TreeWork w) {
         // keys past the last and keys behind a bad table entry are filled with
         // zeros.
         constexpr int32_t kSub = KC / 32;
-        auto find = [&](int32_t c, int64_t (&row)[kSub]) {
+        auto find = [&](int32_t c, TreeEntry (&e)[kSub]) {
 #pragma unroll
             for (int32_t u = 0; u < kSub; ++u)
-                row[u] = c < sg.kb1 ? tree_row(a, sg, c * KC + u * 32 + lane, warp == 0) : -1;
+                e[u] = tree_entry(a, sg, c < sg.kb1 ? c * KC + u * 32 + lane : sg.T);
         };
-        auto issue = [&](int32_t c, const int64_t (&row)[kSub]) {
+        auto issue = [&](int32_t c, const TreeEntry (&e)[kSub]) {
             const uint32_t kb = kv_u + (c & 1) * 2 * KC * stride;
 #pragma unroll
             for (int32_t u = 0; u < kSub; ++u)
-                tree_copy<32>(a, row[u], ppr, kb + u * 32 * stride, stride,
+                tree_copy<32, WARPS>(a, tree_row(a, sg, e[u], warp == 0), ppr, kb + u * 32 * stride, stride,
                               kb + (KC + u * 32) * stride, stride);
             cp_async_commit();
         };
-        int64_t row1[kSub];
-        find(sg.kb0, row1);
-        issue(sg.kb0, row1);             // q and the first chunk
-        find(sg.kb0 + 1, row1);
+        TreeEntry next[kSub];
+        find(sg.kb0, next);
+        issue(sg.kb0, next);             // q and the first chunk
+        find(sg.kb0 + 1, next);
         tree_visible(a, sg, up, bits);
 
         // this lane's two rows: warp * 16 + grp (half 0) and + 8 (half 1)
@@ -132,19 +135,19 @@ tree_mma_kernel(const TreeArgs a, const TreeWork w) {
 
         for (int32_t c = sg.kb0; c < sg.kb1; ++c) {
             if (c + 1 < sg.kb1) {          // next chunk in flight while this one is used
-                issue(c + 1, row1);
-                find(c + 2, row1);
+                issue(c + 1, next);
+                find(c + 2, next);
                 cp_async_wait<1>();
             } else {
                 cp_async_wait<0>();
             }
             const int32_t t0 = c * KC;
             const bool masked = t0 + KC > sg.C;
-            for (int32_t k = tid; masked && k < KC; k += kTreeMmaThreads) odd[k] = 0;
+            for (int32_t k = tid; masked && k < KC; k += C::kThreads) odd[k] = 0;
             __syncthreads();               // chunk c (and q) visible to every warp
             uint8_t* vsm = kvs + ((c & 1) * 2 + 1) * KC * stride;
             if (masked) {
-                for (int32_t x = tid; x < KC * ppr; x += kTreeMmaThreads) {
+                for (int32_t x = tid; x < KC * ppr; x += C::kThreads) {
                     const int32_t k = x / ppr, piece = x - k * ppr;
                     uint4* p = reinterpret_cast<uint4*>(vsm + k * stride + piece * 16);
                     const uint4 v = *p;
@@ -301,12 +304,12 @@ tree_mma_kernel(const TreeArgs a, const TreeWork w) {
                     out[row * D + col] = __float2bfloat16_rn(x * inv);
                     out[row * D + col + 1] = __float2bfloat16_rn(y * inv);
                 } else {
-                    *reinterpret_cast<float2*>(cell + ((size_t)(col >> 2) * kTreeMmaRows + rho) * 4 +
+                    *reinterpret_cast<float2*>(cell + ((size_t)(col >> 2) * C::kRows + rho) * 4 +
                                                (col & 3)) = make_float2(x, y);
                 }
             }
             if (!whole && tig == 0)
-                *reinterpret_cast<float2*>(cell + (size_t)D * kTreeMmaRows + 2 * rho) =
+                *reinterpret_cast<float2*>(cell + (size_t)D * C::kRows + 2 * rho) =
                     make_float2(m[h], l[h]);
         }
         __syncthreads();                   // q and the node masks are free

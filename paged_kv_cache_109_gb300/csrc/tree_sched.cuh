@@ -188,25 +188,36 @@ __device__ __forceinline__ TreeIter tree_begin(const TreeArgs& a, const TreeWork
     return it;
 }
 
-// Copies of a chunk of keys by the four warps of a block.  A lane finds the
-// cache row of one key (tree_row, a chunk ahead of use: one table entry and one
-// division a lane, not one a piece), the warps then take the rows in turn, 16
-// bytes a lane.
-__device__ __forceinline__ int64_t tree_row(const TreeArgs& a, const TreeSeg& s, int32_t key,
+// Copies of a chunk of keys by the WARPS warps of a block.  A lane finds the
+// cache row of one key: one table entry and one division a lane, not one a
+// piece.  The entry is read a chunk ahead of use (tree_entry) and looked at when
+// the copies are issued (tree_row), so its latency passes beside the chunk's
+// work.  The warps then take the rows in turn, 16 bytes a lane.
+struct TreeEntry {
+    int32_t id, off;        // table entry; the key's place in its block, < 0: no key
+};
+__device__ __forceinline__ TreeEntry tree_entry(const TreeArgs& a, const TreeSeg& s, int32_t key) {
+    TreeEntry e{0, -1};
+    if (key < s.T) {
+        const int32_t b = key / a.block_size;
+        e.id = a.block_tables[(int64_t)s.i * a.max_blocks + b];
+        e.off = key - b * a.block_size;
+    }
+    return e;
+}
+__device__ __forceinline__ int64_t tree_row(const TreeArgs& a, const TreeSeg& s, TreeEntry e,
                                             bool report) {
-    if (key >= s.T) return -1;
-    const int32_t b = key / a.block_size;
-    const int32_t id = a.block_tables[(int64_t)s.i * a.max_blocks + b];
-    if (id < 0 || id >= a.num_blocks) {
+    if (e.off < 0) return -1;
+    if (e.id < 0 || e.id >= a.num_blocks) {
         if (report) raise_error(PA_DEVERR_TABLE_ENTRY);
         return -1;
     }
-    return ((int64_t)id * a.num_kv_heads + s.g) * a.block_size + (key - b * a.block_size);
+    return ((int64_t)e.id * a.num_kv_heads + s.g) * a.block_size + e.off;
 }
 
 // row: this lane's (lane < KC) cache row of its key, -1: zeros.  pieces: 16-byte
 // pieces of a row; kst, vst: row strides in shared memory, bytes.
-template <int KC>
+template <int KC, int WARPS>
 __device__ __forceinline__ void tree_copy(const TreeArgs& a, int64_t row, int32_t pieces, uint32_t kb,
                                           int32_t kst, uint32_t vb, int32_t vst) {
     static_assert(KC <= 32, "a key a lane");
@@ -218,7 +229,7 @@ __device__ __forceinline__ void tree_copy(const TreeArgs& a, int64_t row, int32_
     while (shift > 0 && (1 << (shift - 1)) >= pieces) --shift;
     const int32_t p0 = lane & ((1 << shift) - 1), sub = lane >> shift, rows = 32 >> shift;
 #pragma unroll 4
-    for (int32_t k0 = warp * rows; k0 < KC; k0 += 4 * rows) {
+    for (int32_t k0 = warp * rows; k0 < KC; k0 += WARPS * rows) {
         const int32_t k = k0 + sub;
         const int64_t r = __shfl_sync(0xffffffffu, row, k & 31);
         if (k >= KC) continue;

@@ -6,9 +6,9 @@
 // a 32-bit sum over a head dim of terms loses.  Head dims up to 256 whose rows
 // are whole 16-byte pieces.
 //
-// A unit is one tile of 64 rows ((node, query head) pairs, head fastest), 16 a
-// warp; a persistent CTA of four warps takes the parts of its range
-// (tree_sched.cuh) one after another.  Keys come in chunks of KC through a
+// A unit is one tile of 16 rows a warp ((node, query head) pairs, head fastest);
+// a persistent CTA of one, two or four warps, the fewest that cover a sequence's
+// rows, takes the parts of its range (tree_sched.cuh) one after another.  Keys come in chunks of KC through a
 // double buffer of 16-byte cp.async copies:
 //   S = Q K^T   (q scaled by scale log2 e), online softmax in base 2, O += P V.
 // A contraction's index may be taken in any order that both operands share, so
@@ -35,23 +35,24 @@
 
 namespace pa {
 
-constexpr int kTreeTfThreads = 128;
-constexpr int kTreeTfRows = 64;       // 16 rows a warp
-
-template <int DMAX, int KC>
+template <int DMAX, int KC, int WARPS>
 struct TreeTfCfg {
     static_assert(DMAX % 32 == 0 && KC % 8 == 0, "tile shape");
+    static constexpr int kThreads = 32 * WARPS;
+    static constexpr int kRows = 16 * WARPS;
+    // CTAs an SM holds at DMAX columns (the registers' limit for the compiler)
+    static constexpr int kPerSm = DMAX > 128 ? (WARPS == 1 ? 2 : 1) : WARPS == 4 ? 2 : 4;
     // row strides in floats
     static __host__ __device__ int32_t k_stride(int32_t D) {
         const int32_t p = (D + 15) / 16 * 16;
         return p % 32 == 16 ? p : p + 16;
     }
     static __host__ __device__ int32_t v_stride(int32_t D) { return (D + 15) / 16 * 16 + 4; }
-    // dynamic shared bytes: q [64], K [2][KC], V [2][KC] rows | visible nodes
-    // [64][8] words | parents | odd keys of the chunk
+    // dynamic shared bytes: q [rows], K [2][KC], V [2][KC] rows | visible nodes
+    // [rows][8] words | parents | odd keys of the chunk
     static size_t smem_bytes(int32_t D) {
-        return 4 * ((size_t)(kTreeTfRows + 2 * KC) * k_stride(D) + 2 * (size_t)KC * v_stride(D) +
-                    kTreeTfRows * (PA_MAX_TREE_NODES / 32) + PA_MAX_TREE_NODES + KC);
+        return 4 * ((size_t)(kRows + 2 * KC) * k_stride(D) + 2 * (size_t)KC * v_stride(D) +
+                    kRows * (PA_MAX_TREE_NODES / 32) + PA_MAX_TREE_NODES + KC);
     }
 };
 
@@ -72,10 +73,10 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
 
 __device__ __forceinline__ bool f32_odd(float x) { return !(fabsf(x) <= 3.4028235e38f); }
 
-template <int DMAX, int KC>
-__global__ void __launch_bounds__(kTreeTfThreads, DMAX <= 128 ? 2 : 1)
+template <int DMAX, int KC, int WARPS>
+__global__ void __launch_bounds__(TreeTfCfg<DMAX, KC, WARPS>::kThreads, TreeTfCfg<DMAX, KC, WARPS>::kPerSm)
 tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
-    using C = TreeTfCfg<DMAX, KC>;
+    using C = TreeTfCfg<DMAX, KC, WARPS>;
     constexpr int NT = KC / 8;           // key tiles
     constexpr int CG = DMAX / 32;        // 32-column groups of O
     constexpr int kWords = PA_MAX_TREE_NODES / 32;
@@ -87,16 +88,16 @@ tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
     const int32_t HT = w.s.heads;
     const int32_t kst = C::k_stride(D), vst = C::v_stride(D), ppr = D / 4;
     float* qs = sm_tf;                                          // [64][kst]
-    float* ks = qs + kTreeTfRows * kst;                         // [2][KC][kst]
+    float* ks = qs + C::kRows * kst;                         // [2][KC][kst]
     float* vs = ks + 2 * KC * kst;                              // [2][KC][vst]
     uint32_t* bits = reinterpret_cast<uint32_t*>(vs + 2 * KC * vst);   // [tokens][8]
-    int32_t* up = reinterpret_cast<int32_t*>(bits + kTreeTfRows * kWords);
+    int32_t* up = reinterpret_cast<int32_t*>(bits + C::kRows * kWords);
     int32_t* odd = up + PA_MAX_TREE_NODES;                      // [KC] key's V had values taken out
     const float* q = static_cast<const float*>(a.q);
     const float* vc = static_cast<const float*>(a.v_cache);
 
     // columns of Q and K past the head dim stay zero
-    for (int32_t x = tid; x < (kTreeTfRows + 2 * KC) * kst; x += kTreeTfThreads) qs[x] = 0.f;
+    for (int32_t x = tid; x < (C::kRows + 2 * KC) * kst; x += C::kThreads) qs[x] = 0.f;
     TreeIter it = tree_begin(a, w, reinterpret_cast<int64_t*>(bits));
     TreeSeg sg;
     TreeCut cut{};
@@ -110,32 +111,42 @@ tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
         // Copies of chunk c (keys c KC ..) into buffer c & 1; keys past the last
         // and keys behind a bad table entry are filled with zeros.
         auto find = [&](int32_t c) {
-            return lane < KC && c < sg.kb1 ? tree_row(a, sg, c * KC + lane, warp == 0) : -1;
+            return tree_entry(a, sg, lane < KC && c < sg.kb1 ? c * KC + lane : sg.T);
         };
-        auto issue = [&](int32_t c, int64_t row) {
-            tree_copy<KC>(a, row, ppr, smem_u32(ks + (c & 1) * KC * kst), kst * 4,
+        auto issue = [&](int32_t c, TreeEntry e) {
+            tree_copy<KC, WARPS>(a, tree_row(a, sg, e, warp == 0), ppr, smem_u32(ks + (c & 1) * KC * kst), kst * 4,
                           smem_u32(vs + (c & 1) * KC * vst), vst * 4);
             cp_async_commit();
         };
         issue(sg.kb0, find(sg.kb0));
-        int64_t row1 = find(sg.kb0 + 1);
-        // rows in use of Q (idle rows' scores reach no other row), a warp a row
+        TreeEntry next = find(sg.kb0 + 1);
+        // rows in use of Q (idle rows' scores reach no other row): a warp takes a
+        // row at a time, eight rows' loads before their stores
         const bool q16 = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0;
-#pragma unroll 4
-        for (int32_t rho = warp; rho < sg.ntok * HT; rho += 4) {
-            const int32_t tk = rho / HT, hh = rho - tk * HT;
-            if (hh >= hs) continue;
-            const float* src = q + ((int64_t)(sg.q0 + sg.tok0 + tk) * a.num_q_heads + head_base + hh) * D;
+        const int32_t rows = sg.ntok * HT;
+        for (int32_t r0 = warp; r0 < rows; r0 += 8 * WARPS) {
             for (int32_t d = 4 * lane; d < D; d += 128) {
-                float4 v;
-                if (q16) {
-                    v = *reinterpret_cast<const float4*>(src + d);
-                } else {
-                    v = make_float4(src[d], src[d + 1], src[d + 2], src[d + 3]);
+                float4 v[8];
+#pragma unroll
+                for (int32_t u = 0; u < 8; ++u) {
+                    const int32_t rho = r0 + u * WARPS, tk = rho / HT, hh = rho - tk * HT;
+                    v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (rho >= rows || hh >= hs) continue;
+                    const float* src =
+                        q + ((int64_t)(sg.q0 + sg.tok0 + tk) * a.num_q_heads + head_base + hh) * D + d;
+                    if (q16)
+                        v[u] = *reinterpret_cast<const float4*>(src);
+                    else
+                        v[u] = make_float4(src[0], src[1], src[2], src[3]);
                 }
                 const float c = a.scale_log2;
-                *reinterpret_cast<float4*>(qs + rho * kst + d) =
-                    make_float4(v.x * c, v.y * c, v.z * c, v.w * c);
+#pragma unroll
+                for (int32_t u = 0; u < 8; ++u) {
+                    const int32_t rho = r0 + u * WARPS;
+                    if (rho < rows)
+                        *reinterpret_cast<float4*>(qs + rho * kst + d) =
+                            make_float4(v[u].x * c, v[u].y * c, v[u].z * c, v[u].w * c);
+                }
             }
         }
         tree_visible(a, sg, up, bits);
@@ -159,20 +170,20 @@ tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
 
         for (int32_t c = sg.kb0; c < sg.kb1; ++c) {
             if (c + 1 < sg.kb1) {          // next chunk in flight while this one is used
-                issue(c + 1, row1);
-                row1 = find(c + 2);
+                issue(c + 1, next);
+                next = find(c + 2);
                 cp_async_wait<1>();
             } else {
                 cp_async_wait<0>();
             }
             const int32_t t0 = c * KC;
             const bool masked = t0 + KC > sg.C;
-            for (int32_t k = tid; masked && k < KC; k += kTreeTfThreads) odd[k] = 0;
+            for (int32_t k = tid; masked && k < KC; k += C::kThreads) odd[k] = 0;
             __syncthreads();               // chunk c (and q) visible to every warp
             const float* kb = ks + (c & 1) * KC * kst;
             float* vb = vs + (c & 1) * KC * vst;
             if (masked) {
-                for (int32_t x = tid; x < KC * D; x += kTreeTfThreads) {
+                for (int32_t x = tid; x < KC * D; x += C::kThreads) {
                     const int32_t k = x / D;
                     float* p = vb + k * vst + (x - k * D);
                     if (f32_odd(*p)) {
@@ -185,11 +196,11 @@ tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
             if (busy) {
                 // (the corrections are summed apart: a tensor-core sum cuts off
                 // what it cannot hold, so long chains drift)
-                float s[NT][4], sc[NT][4];
+                float s[NT][4], sc[NT][4], sd[NT][4];
 #pragma unroll
                 for (int32_t n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int32_t e = 0; e < 4; ++e) s[n][e] = sc[n][e] = 0.f;
+                    for (int32_t e = 0; e < 4; ++e) s[n][e] = sc[n][e] = sd[n][e] = 0.f;
                 const float* qa = qs + (warp * 16 + grp) * kst + 4 * tig;
                 const float* ka = kb + grp * kst + 4 * tig;
 #pragma unroll 2
@@ -217,14 +228,14 @@ tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
                         for (int32_t e = 0; e < 2; ++e) {
                             mma_tf32_1688(s[n], ah[e], bh[2 * e], bh[2 * e + 1]);
                             mma_tf32_1688(sc[n], al[e], bh[2 * e], bh[2 * e + 1]);
-                            mma_tf32_1688(sc[n], ah[e], bl[2 * e], bl[2 * e + 1]);
+                            mma_tf32_1688(sd[n], ah[e], bl[2 * e], bl[2 * e + 1]);
                         }
                     }
                 }
 #pragma unroll
                 for (int32_t n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int32_t e = 0; e < 4; ++e) s[n][e] += sc[n][e];
+                    for (int32_t e = 0; e < 4; ++e) s[n][e] += sc[n][e] + sd[n][e];
 
                 // mask, online softmax of rows grp (h = 0) and grp + 8 (h = 1);
                 // a row's columns are spread over its 4 lanes
@@ -353,12 +364,12 @@ tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
                 for (int32_t e = 0; e < 2; ++e) {
                     const int32_t col = cg * 32 + 8 * tig + 4 * e;
                     if (col < D)
-                        *reinterpret_cast<float4*>(dst + (whole ? col : (size_t)col * kTreeTfRows)) =
+                        *reinterpret_cast<float4*>(dst + (whole ? col : (size_t)col * C::kRows)) =
                             make_float4(acc[cg][0][2 * h + e] * inv, acc[cg][1][2 * h + e] * inv,
                                         acc[cg][2][2 * h + e] * inv, acc[cg][3][2 * h + e] * inv);
                 }
             if (!whole && tig == 0)
-                *reinterpret_cast<float2*>(cell + (size_t)D * kTreeTfRows + 2 * rho) =
+                *reinterpret_cast<float2*>(cell + (size_t)D * C::kRows + 2 * rho) =
                     make_float2(m[h], l[h]);
         }
         __syncthreads();                   // q and the node masks are free

@@ -91,23 +91,33 @@ tree_tiled_kernel(const TreeArgs a, const TreeWork w) {
         // Copies of chunk c (keys c KC ..) into buffer c & 1; keys past the last
         // and keys behind a bad table entry are filled with zeros.
         auto find = [&](int32_t c) {
-            return (tid & 31) < KC && c < sg.kb1 ? tree_row(a, sg, c * KC + (tid & 31), tid < 32) : -1;
+            return tree_entry(a, sg, (tid & 31) < KC && c < sg.kb1 ? c * KC + (tid & 31) : sg.T);
         };
-        auto issue = [&](int32_t c, int64_t row) {
+        auto issue = [&](int32_t c, TreeEntry e) {
             const uint32_t kb = smem_u32(kvs + (c & 1) * 2 * KC * stride);
-            tree_copy<KC>(a, row, ppr, kb, stride, kb + KC * stride, stride);
+            tree_copy<KC, kTreeTiledThreads / 32>(a, tree_row(a, sg, e, tid < 32), ppr, kb, stride, kb + KC * stride, stride);
             cp_async_commit();
         };
         issue(sg.kb0, find(sg.kb0));
-        int64_t row1 = find(sg.kb0 + 1);
-        // Q rows, a warp a row (zeros in idle ones)
-#pragma unroll 4
-        for (int32_t rho = tid >> 5; rho < R; rho += kTreeTiledThreads / 32) {
-            const int32_t tk = rho / HT, hh = rho - tk * HT;
-            const bool live = tk < sg.ntok && hh < hs;
-            const E* src = q + (live ? ((int64_t)(sg.q0 + sg.tok0 + tk) * a.num_q_heads + head_base + hh) * D : 0);
-            for (int32_t d = tid & 31; d < D; d += 32)
-                qs[rho * qst + d] = live ? Elem<E>::to_float(src[d]) * a.scale_log2 : 0.f;
+        TreeEntry next = find(sg.kb0 + 1);
+        // Q rows, eight rows' loads of a warp at a time (zeros in idle rows)
+        for (int32_t r0 = tid >> 5; r0 < R; r0 += 8 * (kTreeTiledThreads / 32)) {
+            for (int32_t d = tid & 31; d < D; d += 32) {
+                float v[8];
+#pragma unroll
+                for (int32_t u = 0; u < 8; ++u) {
+                    const int32_t rho = r0 + u * (kTreeTiledThreads / 32), tk = rho / HT, hh = rho - tk * HT;
+                    v[u] = 0.f;
+                    if (tk < sg.ntok && hh < hs)
+                        v[u] = Elem<E>::to_float(
+                            q[((int64_t)(sg.q0 + sg.tok0 + tk) * a.num_q_heads + head_base + hh) * D + d]);
+                }
+#pragma unroll
+                for (int32_t u = 0; u < 8; ++u) {
+                    const int32_t rho = r0 + u * (kTreeTiledThreads / 32);
+                    if (rho < R) qs[rho * qst + d] = v[u] * a.scale_log2;
+                }
+            }
         }
         tree_visible(a, sg, up, bits);
 
@@ -129,8 +139,8 @@ tree_tiled_kernel(const TreeArgs a, const TreeWork w) {
 
         for (int32_t c = sg.kb0; c < sg.kb1; ++c) {
             if (c + 1 < sg.kb1) {      // next chunk in flight while this one is used
-                issue(c + 1, row1);
-                row1 = find(c + 2);
+                issue(c + 1, next);
+                next = find(c + 2);
                 cp_async_wait<1>();
             } else {
                 cp_async_wait<0>();
