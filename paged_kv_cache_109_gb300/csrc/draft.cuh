@@ -114,6 +114,7 @@ int32_t tree_ctas(const TreeShape& s, int32_t num_seqs, int32_t max_q_len, int32
 }
 
 size_t tree_workspace(const TreeShape& s, int32_t ctas, int32_t head_dim) {
+    if (s.fixed_cost > 0) return 0;
     return align256((size_t)ctas * sizeof(TreeCut)) +
            align256(2 * (size_t)ctas * tree_cell_floats(s, head_dim) * 4);
 }
@@ -266,6 +267,13 @@ TreeLaunch tree_launch(TreeKernel k, const pa_cache_desc* c, int32_t group, int3
         const int32_t rpt = tree_tiled_rpt(c->head_dim, group, max_q_len);
         instance = 10 + rpt;
         per_sm = with_tree_tiled(c->head_dim, rpt, resident);
+    }
+    // Short sequences go whole: no range ends inside a unit, so no merge follows
+    // (a launch and 3 us, more than a cut of so little work gives).  A unit's
+    // parts then cost the same whatever its length.
+    if (max_seq_len <= (k == kTreeWs ? 512 : 128)) {
+        t.s.fixed_cost = (int32_t)tree_most(t.s, max_q_len, max_seq_len);
+        t.s.min_range = t.s.fixed_cost;
     }
     t.ctas = tree_ctas(t.s, num_seqs, max_q_len, max_seq_len, c->num_kv_heads, per_sm);
     return t;
@@ -511,8 +519,10 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
         TreeWork w{};
         w.s = t.s;
         uint8_t* base = static_cast<uint8_t*>(workspace);
-        w.cuts = reinterpret_cast<TreeCut*>(base);
-        w.cells = reinterpret_cast<float*>(base + align256((size_t)t.ctas * sizeof(TreeCut)));
+        if (t.s.fixed_cost == 0) {
+            w.cuts = reinterpret_cast<TreeCut*>(base);
+            w.cells = reinterpret_cast<float*>(base + align256((size_t)t.ctas * sizeof(TreeCut)));
+        }
         auto go = [&](auto kern, int threads, size_t smem) {
             if (!set_smem(kern, smem)) return cudaErrorUnknown;
             return launch_pdl(kern, dim3(t.ctas), dim3(threads), smem, st, a, w);

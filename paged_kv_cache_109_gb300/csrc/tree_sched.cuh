@@ -33,7 +33,7 @@ struct TreeShape {
     int32_t block_one, block_more;   // cost of a key block, with one tile in use or more
     int32_t overhead;       // cost of a unit beside its key blocks
     int32_t min_range;      // least cost of a CTA's range
-    int32_t fixed_cost;     // > 0: every unit counts as this much, one unit a CTA
+    int32_t fixed_cost;     // > 0: every unit counts as this much, and no range ends inside one
 };
 
 // A unit cut by the end of a CTA's range, for the merge: written by the CTA
@@ -128,6 +128,17 @@ __device__ __forceinline__ bool tree_next(const TreeArgs& a, const TreeShape& sh
     return false;
 }
 
+// This CTA's range of a line of `total` cost.
+__device__ __forceinline__ void tree_range(const TreeShape& s, int64_t total, TreeIter& it) {
+    const uint32_t ctas = gridDim.x;
+    it.range = total <= 0x7fffffff ? (int64_t)(((uint32_t)total + ctas - 1) / ctas)
+                                   : (total + ctas - 1) / ctas;
+    it.range = s.fixed_cost > 0 ? (it.range + s.fixed_cost - 1) / s.fixed_cost * s.fixed_cost
+                                : max(it.range, (int64_t)s.min_range);
+    it.pos = min(total, it.range * blockIdx.x);
+    it.end = min(total, it.pos + it.range);
+}
+
 // This CTA's range: all threads of the block, `scratch` holding 2 + threads /
 // 32 values.  Every CTA sums the batch's costs; CTA 0 reports refused
 // sequences.
@@ -161,13 +172,8 @@ __device__ __forceinline__ TreeIter tree_begin(const TreeArgs& a, const TreeWork
         total += v;
     }
     int64_t at = before + incl - sum;           // cost before sequence i0
-    const uint32_t ctas = gridDim.x;
     TreeIter it;
-    it.range = total <= 0x7fffffff ? (int64_t)(((uint32_t)total + ctas - 1) / ctas)
-                                   : (total + ctas - 1) / ctas;
-    it.range = w.s.fixed_cost > 0 ? (int64_t)w.s.fixed_cost : max(it.range, (int64_t)w.s.min_range);
-    it.pos = min(total, it.range * blockIdx.x);
-    it.end = min(total, it.pos + it.range);
+    tree_range(w.s, total, it);
     // the thread whose sequences hold the range's start names the sequence
     if (at <= it.pos && it.pos < at + sum) {
         int32_t i = i0;
@@ -185,6 +191,47 @@ __device__ __forceinline__ TreeIter tree_begin(const TreeArgs& a, const TreeWork
     __syncthreads();
     it.i = (int32_t)scratch[0];
     it.seq0 = scratch[1];
+    return it;
+}
+
+// The same by one warp, for up to 128 sequences (four a lane): no barrier, so
+// the block's other warps set up meanwhile.
+constexpr int32_t kTreeWarpSeqs = 128;
+__device__ __forceinline__ TreeIter tree_begin_warp(const TreeArgs& a, const TreeWork& w) {
+    const int32_t lane = threadIdx.x & 31;
+    int64_t c[4];
+#pragma unroll
+    for (int32_t u = 0; u < 4; ++u) {
+        const int32_t i = 4 * lane + u;
+        c[u] = 0;
+        if (i < a.num_seqs) {
+            const TreeSeq s = tree_seq(a, i, blockIdx.x == 0);
+            c[u] = (int64_t)tree_units(a, w.s, s.n) * tree_cost(w.s, s.n, s.T);
+        }
+    }
+    int64_t incl = c[0] + c[1] + c[2] + c[3];
+    const int64_t sum = incl;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += x;
+    }
+    TreeIter it;
+    tree_range(w.s, __shfl_sync(0xffffffffu, incl, 31), it);
+    int64_t at = incl - sum;
+    int32_t i = 4 * lane;
+    const bool mine = at <= it.pos && it.pos < incl;
+#pragma unroll
+    for (int32_t u = 0; u < 3; ++u) {
+        if (it.pos >= at + c[u] && i == 4 * lane + u) {
+            at += c[u];
+            ++i;
+        }
+    }
+    const uint32_t who = __ballot_sync(0xffffffffu, mine);
+    const int32_t src = who ? __ffs(who) - 1 : 0;         // (none: an empty range)
+    it.i = who ? __shfl_sync(0xffffffffu, i, src) : 0;
+    it.seq0 = who ? __shfl_sync(0xffffffffu, at, src) : 0;
     return it;
 }
 

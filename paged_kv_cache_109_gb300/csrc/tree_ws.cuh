@@ -22,9 +22,9 @@
 //   warps 0-3, 4-7  softmax of accumulator 0, 1: thread t owns tensor-memory
 //                   lane t (one row); output or workspace cells at the end
 //   warps 8, 10     producers of K and of V: block-table lookups, TMA copies.
-//                   The K warp walks the range and hands its parts to the
-//                   other warps through a short queue, with Q (TMA) and the
-//                   nodes' parents.  The V warp checks the blocks that not
+//                   The K warp walks the range, hands its parts to the other
+//                   warps through a short queue and loads Q (TMA), the V warp
+//                   the nodes' parents.  The V warp checks the blocks that not
 //                   every row may see (tree nodes, rows behind the last key)
 //                   before their use: rows behind are cleared, and values that
 //                   are not finite are taken out (0 times NaN would reach rows
@@ -172,9 +172,15 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if (warp == C::kMmaWarp && lane == 0) prefetch_tmap(&tmap_q);
     if (warp == C::kMmaWarp) tmem_alloc(smem_u32(tslot), C::kTmemCols);
     griddep_wait();
-    // (the ring is not in use yet: its start serves the range's search)
-    TreeIter it = tree_begin(a, w, reinterpret_cast<int64_t*>(sm + C::kSlotOff));
-    fence_proxy_async_smem();
+    // the range: by the K warp alone where it can (the ring is not in use yet:
+    // its start serves the search of larger batches)
+    TreeIter it{};
+    if (a.num_seqs > kTreeWarpSeqs) {
+        it = tree_begin(a, w, reinterpret_cast<int64_t*>(sm + C::kSlotOff));
+        fence_proxy_async_smem();
+    } else if (warp == C::kKWarp) {
+        it = tree_begin_warp(a, w);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -222,6 +228,7 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
         int32_t checked = 0;                              // V blocks checked so far
         TreeCut cut{};
         bool was_one = false;                             // the part before used one tile
+        int32_t q_parts = 0;                              // parts whose Q is asked for
         // K's warp finds the parts and announces them (n = 0: there are no more)
         auto announce = [&]() {
             if (!tree_next(a, w.s, it, sg)) sg.n = 0;
@@ -237,7 +244,7 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
         };
         // Q: a copy per tile and half of `tokens` x `heads` rows in place (rows
         // behind the part's last node or head hold whatever comes there: a
-        // row's scores reach no other row), and the nodes' parents.
+        // row's scores reach no other row).
         auto load_q = [&]() {
             const int32_t tiles = sg.ntok > tpt ? 2 : 1;
             if (seg > 0) ok = warp_wait(q_free, (seg - 1) & 1);
@@ -246,6 +253,7 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
             if (ok && tiles == 2 && was_one) ok = warp_wait(o_free, (seg - 1) & 1);
             if (!ok) return;
             was_one = tiles == 1;
+            ++q_parts;
             if (lane == 0) {
                 mbar_arrive_expect_tx(q_full, (uint32_t)(tpt * HT) * 128u * C::kHalves * tiles);
                 for (int32_t t = 0; t < tiles; ++t)
@@ -253,17 +261,23 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         tma_load_3d(sm_u + t * C::kQTile + h * (C::kRows * 128), &tmap_q, h * 64,
                                     sg.g * G + sg.sg * HT, sg.q0 + sg.tok0 + t * tpt, q_full);
             }
-            for (int32_t j = lane; j < sg.n; j += 32) {
-                const int32_t p = tree_parent(a.parents[sg.q0 + j], j, true);
-                parents[(seg % C::kBufs) * PA_MAX_TREE_NODES + j] = (uint8_t)(p + 1);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);           // the parents are there
         };
         while (ok && (is_v ? next_part() : announce())) {
             const int32_t n = sg.kb1 - sg.kb0, lag = sg.ntok > tpt ? 1 : 2;
             uint32_t* noted = flags + (seg % C::kBufs) * (PA_MAX_TREE_NODES / 32);
-            if (is_v && lane < PA_MAX_TREE_NODES / 32) noted[lane] = 0;
+            if (is_v) {
+                // the nodes' parents (the K warp is at most one part further, after
+                // the output of the part three before this one)
+                if (lane < PA_MAX_TREE_NODES / 32) noted[lane] = 0;
+                for (int32_t j = lane; j < sg.n; j += 32) {
+                    const int32_t p = tree_parent(a.parents[sg.q0 + j], j, true);
+                    parents[(seg % C::kBufs) * PA_MAX_TREE_NODES + j] = (uint8_t)(p + 1);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
+            } else if (seg == 0) {
+                load_q();
+            }
             // V's block y, if it reaches past the cached tokens: rows of tree
             // nodes, and rows behind the last key up to the end of its 16-key
             // step (the later steps are left out)
@@ -368,7 +382,7 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 // that this block's use frees)
                 if (is_v)
                     check(x - 1);
-                else if (x == min(n - 1, 1))              // with the part's first keys under way
+                else if (seg > 0 && x == min(n - 1, 1))   // with the part's first keys under way
                     load_q();
             }
             if (is_v) check(n - 1);
@@ -381,7 +395,8 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (!ok) {
             if (mine >= 0)
                 mbar_wait_bounded(kv_full(lane), (mine / C::kSlots) & 1, kWaitLimitCycles);
-            if (!is_v && seg > 0) mbar_wait_bounded(q_full, (seg - 1) & 1, kWaitLimitCycles);
+            if (!is_v && q_parts > 0)
+                mbar_wait_bounded(q_full, (q_parts - 1) & 1, kWaitLimitCycles);
             if (lane == 0) raise_error(PA_DEVERR_TIMEOUT);
         }
     } else if (warp == C::kMmaWarp) {
