@@ -437,6 +437,9 @@ pa_status pa_check_wait_timeout(int32_t expected, int32_t arrivals, int64_t limi
 
 /* ---- drafted (speculative) steps ------------------------------------------
  *
+ * The calls below take memory of the current device, managed or page-locked
+ * memory; memory of another device is refused with PA_ERR_INVALID_ARG.
+ *
  * A verify step runs several drafted tokens of each sequence through the
  * model at once and keeps those that hold.  How many hold is known on the
  * device only, so the three calls below keep the step there: pa_plan_step
@@ -491,7 +494,9 @@ pa_status pa_check_wait_timeout(int32_t expected, int32_t arrivals, int64_t limi
  * outputs        device or pinned; seq_lens_out, blocks_held_out and
  *                free_head_out may be the input arrays themselves (no other
  *                overlap).  positions and seq_ids may be NULL.
- * num_seqs <= 65535, max_tokens < 2^31 - 2^20.
+ * num_seqs <= 65535, max_tokens and num_free < 2^31 - 2^20.  A step without
+ * sequences writes query_start_loc[0] = block_start[0] = 0, the front and the
+ * tokens' -1.
  */
 pa_status pa_plan_step(const int32_t* seq_lens, const int32_t* new_tokens,
                        const int32_t* blocks_held, int32_t num_seqs,
@@ -520,7 +525,7 @@ pa_status pa_plan_step(const int32_t* seq_lens, const int32_t* new_tokens,
  * query_start_loc  device or pinned int32 [num_seqs + 1], non-decreasing.  Rows
  *                  from its last entry up to total_q are left as they were.
  * parents          device or pinned int32 [total_q].
- * max_q_len        host upper bound of n_i, at most PA_MAX_TREE_NODES.
+ * max_q_len        host upper bound of n_i, at most PA_MAX_TREE_NODES; 0: no rows.
  * max_seq_len      host upper bound of T_i.
  * workspace        device, >= pa_decode_tree_workspace_bytes(...) bytes, 256-byte
  *                  aligned; may be NULL when that size is 0.  Two calls that may

@@ -505,6 +505,17 @@ def _raw_stream(stream, device: int) -> int:
     return _stream(stream)
 
 
+def _empty(shape, dtype, device: int, stream):
+    """A tensor for a call on ``stream``, from that stream's memory: what the
+    call leaves behind is only reused by work ordered after it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class StepPlan:
     """What ``plan_step`` writes, all int32 but slot_mapping (int64):
     ``seq_lens`` and ``blocks_held`` [N] after the step, ``free_head`` [1],
@@ -528,6 +539,7 @@ class StepPlan:
 
     @classmethod
     def empty(cls, num_seqs: int, max_tokens: int, device="cuda") -> "StepPlan":
+        """Buffers for up to num_seqs sequences' step of max_tokens tokens."""
         def i32(n):
             return torch.empty(n, dtype=torch.int32, device=device)
 
@@ -560,7 +572,11 @@ def plan_step(seq_lens, new_tokens, block_tables, blocks_held, free_blocks, free
     if plan is None:
         if max_tokens is None:
             raise ValueError("pass a plan or max_tokens")
-        plan = StepPlan.empty(n, max_tokens, block_tables.device)
+        i32 = torch.int32
+        plan = StepPlan(*(_empty(k, i32, device, stream) for k in (n, n, 1, n + 1, n + 1)),
+                        _empty(max_tokens, torch.int64, device, stream),
+                        _empty(max_tokens, i32, device, stream),
+                        _empty(max_tokens, i32, device, stream))
     lens_out, held_out, head_out = plan.seq_lens, plan.blocks_held, plan.free_head
     start, taken, slots = plan.query_start_loc, plan.block_start, plan.slot_mapping
     positions, seq_ids = plan.positions, plan.seq_ids
@@ -643,7 +659,7 @@ def decode_tree(q, query_start_loc, parents, k_cache, v_cache, block_tables, seq
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q) if q.is_cuda else torch.empty_like(q, device=k_cache.device)
+        out = _empty(q_shape, dtype, device, stream)
     elif out.shape != q_shape or out.dtype is not dtype:
         raise ValueError("out must have q's shape and dtype")
     lib = load_library()
@@ -651,7 +667,7 @@ def decode_tree(q, query_start_loc, parents, k_cache, v_cache, block_tables, seq
     if workspace is None:
         ws_bytes = lib.pa_decode_tree_workspace_bytes(n, total, hq, max_q_len, max_seq_len, ref)
         if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+            workspace = _empty(ws_bytes, torch.uint8, device, stream)
     else:
         _dev(workspace)
         ws_bytes = workspace.numel() * workspace.element_size()
@@ -720,9 +736,9 @@ def accept_tree(leaf, parents, query_start_loc, seq_lens, k_caches, v_caches, bl
         raise ValueError("leaf, query_start_loc, block_tables and seq_lens disagree on the "
                          "sequence count")
     if new_lens is None:
-        new_lens = torch.empty(n, dtype=torch.int32, device=device)
+        new_lens = _empty(n, torch.int32, device, stream)
     if accepted_rows is None:
-        accepted_rows = torch.empty(total, dtype=torch.int32, device=device)
+        accepted_rows = _empty(total, torch.int32, device, stream)
     if new_lens.numel() != n or accepted_rows.numel() != total:
         raise ValueError("new_lens must have N and accepted_rows total_q entries")
     ints = (leaf, parents, query_start_loc, seq_lens, block_tables, new_lens, accepted_rows)

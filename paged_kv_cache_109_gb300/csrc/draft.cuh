@@ -40,6 +40,35 @@ bool current_device_memory(const void* p) {
     return at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == dev);
 }
 
+// map_step_arg for memory that a kernel of the current device may touch: its
+// own, managed or page-locked (nullptr passes).
+template <typename T>
+bool map_current_arg(T*& p) {
+    if (!p) return true;
+    cudaPointerAttributes at;
+    int dev = -1;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    if (at.type == cudaMemoryTypeDevice) return at.device == dev;
+    if (at.type == cudaMemoryTypeHost && at.devicePointer) {
+        p = static_cast<T*>(at.devicePointer);
+        return true;
+    }
+    return at.type == cudaMemoryTypeManaged;
+}
+
+// A debug pass, whose host copies may throw: no exception leaves the library.
+template <typename F>
+pa_status debug_pass(F f) {
+    try {
+        return f();
+    } catch (...) {
+        return PA_ERR_CUDA;
+    }
+}
+
 // Arrays of na and nb bytes share a byte.
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -362,9 +391,9 @@ pa_status pa_plan_step(const int32_t* seq_lens, const int32_t* new_tokens,
         max_blocks_per_seq < 0 || max_tokens < 0)
         return PA_ERR_INVALID_ARG;
     if (num_seqs > 65535 || max_tokens >= kMost || num_free >= kMost) return PA_ERR_UNSUPPORTED;
-    if (num_seqs == 0) return PA_OK;
-    if (!seq_lens || !new_tokens || !blocks_held || !free_head || !block_tables ||
-        !seq_lens_out || !blocks_held_out || !free_head_out || !query_start_loc || !block_start ||
+    if ((num_seqs > 0 && (!seq_lens || !new_tokens || !blocks_held || !block_tables ||
+                          !seq_lens_out || !blocks_held_out)) ||
+        !free_head || !free_head_out || !query_start_loc || !block_start ||
         (max_tokens > 0 && !slot_mapping) || (num_free > 0 && !free_blocks))
         return PA_ERR_INVALID_ARG;
     PlanArgs a{seq_lens, new_tokens, blocks_held, free_blocks, free_head, ref_cnt, block_tables,
@@ -398,17 +427,18 @@ pa_status pa_plan_step(const int32_t* seq_lens, const int32_t* new_tokens,
             if (!same && overlap(out[x].p, out[x].bytes, y.p, y.bytes)) return PA_ERR_INVALID_ARG;
         }
     }
-    if (!map_step_arg(a.seq_lens) || !map_step_arg(a.new_tokens) || !map_step_arg(a.blocks_held) ||
-        !map_step_arg(a.free_blocks) || !map_step_arg(a.free_head) ||
-        !map_step_arg(a.seq_lens_out) || !map_step_arg(a.blocks_held_out) ||
-        !map_step_arg(a.free_head_out) || !map_step_arg(a.query_start) ||
-        !map_step_arg(a.block_start) || !map_step_arg(a.slot_mapping) ||
-        !map_step_arg(a.positions) || !map_step_arg(a.seq_ids) ||
-        !current_device_memory(block_tables) || (ref_cnt && !current_device_memory(ref_cnt)))
+    if (!map_current_arg(a.seq_lens) || !map_current_arg(a.new_tokens) || !map_current_arg(a.blocks_held) ||
+        !map_current_arg(a.free_blocks) || !map_current_arg(a.free_head) ||
+        !map_current_arg(a.seq_lens_out) || !map_current_arg(a.blocks_held_out) ||
+        !map_current_arg(a.free_head_out) || !map_current_arg(a.query_start) ||
+        !map_current_arg(a.block_start) || !map_current_arg(a.slot_mapping) ||
+        !map_current_arg(a.positions) || !map_current_arg(a.seq_ids) ||
+        (block_tables && !current_device_memory(block_tables)) || (ref_cnt && !current_device_memory(ref_cnt)))
         return PA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (debug::enabled()) {
-        const pa_status r = debug::check_free(a.free_blocks, num_free, a.free_head, num_blocks, st);
+        const pa_status r = debug_pass(
+            [&] { return debug::check_free(a.free_blocks, num_free, a.free_head, num_blocks, st); });
         if (r != PA_OK) return r;
     }
     return plan_impl(a, st);
@@ -448,21 +478,22 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
     if (pa_decode_path(num_q_heads, cache) < 0 || num_seqs < 0 || total_q < 0 || max_q_len < 0 ||
         max_seq_len < 0 || max_blocks_per_seq < 0 || max_q_len > max_seq_len)
         return PA_ERR_INVALID_ARG;
-    if (num_seqs == 0 || total_q == 0) return PA_OK;
+    if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return PA_OK;
     if (!q || !query_start_loc || !parents || !k_cache || !v_cache || !block_tables ||
         !seq_lens || !out)
         return PA_ERR_INVALID_ARG;
     if ((int64_t)max_blocks_per_seq * cache->block_size < max_seq_len) return PA_ERR_INVALID_ARG;
+    // (key positions of a block behind the last stay in 32 bits)
     if (max_q_len > PA_MAX_TREE_NODES || num_seqs > 65535 || cache->num_kv_heads > 65535 ||
-        cache->head_dim > 32 * kTreeDimPerLane)
+        cache->head_dim > 32 * kTreeDimPerLane || max_seq_len > INT32_MAX - 4096)
         return PA_ERR_UNSUPPORTED;
     const int eb = elem_bytes(cache);
     if (!aligned(q, eb) || !aligned(out, eb) || !aligned(k_cache, eb) || !aligned(v_cache, eb) ||
         !aligned(query_start_loc, 4) || !aligned(parents, 4) || !aligned(block_tables, 4) ||
         !aligned(seq_lens, 4))
         return PA_ERR_INVALID_ARG;
-    if (!map_step_arg(q) || !map_step_arg(query_start_loc) || !map_step_arg(parents) ||
-        !map_step_arg(block_tables) || !map_step_arg(seq_lens) || !map_step_arg(out) ||
+    if (!map_current_arg(q) || !map_current_arg(query_start_loc) || !map_current_arg(parents) ||
+        !map_current_arg(block_tables) || !map_current_arg(seq_lens) || !map_current_arg(out) ||
         !current_device_memory(k_cache) || !current_device_memory(v_cache))
         return PA_ERR_INVALID_ARG;
     const size_t need = pa_decode_tree_workspace_bytes(num_seqs, total_q, num_q_heads, max_q_len,
@@ -472,10 +503,14 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
         return PA_ERR_WORKSPACE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (debug::enabled()) {
-        pa_status r = debug::check_tables(block_tables, max_blocks_per_seq, seq_lens, num_seqs,
-                                          max_seq_len, query_start_loc, total_q, cache, st);
-        if (r == PA_OK)
-            r = debug::check_tree(query_start_loc, num_seqs, parents, total_q, max_q_len, nullptr, st);
+        const pa_status r = debug_pass([&] {
+            const pa_status x = debug::check_tables(block_tables, max_blocks_per_seq, seq_lens,
+                                                    num_seqs, max_seq_len, query_start_loc, total_q,
+                                                    cache, st);
+            return x != PA_OK ? x
+                              : debug::check_tree(query_start_loc, num_seqs, parents, total_q,
+                                                  max_q_len, nullptr, st);
+        });
         if (r != PA_OK) return r;
     }
     TreeArgs a{};
@@ -585,9 +620,9 @@ pa_status pa_accept_tree(const int32_t* leaf, const int32_t* parents,
     AcceptArgs a{leaf, parents, query_start_loc, seq_lens, block_tables, new_lens, accepted_rows,
                  total_q, max_q_len, max_blocks_per_seq, cache->num_blocks, cache->block_size,
                  cache->num_kv_heads, cache->head_dim * elem_bytes(cache)};
-    if (!map_step_arg(a.leaf) || !map_step_arg(a.parents) || !map_step_arg(a.query_start) ||
-        !map_step_arg(a.seq_lens) || !map_step_arg(a.block_tables) ||
-        !map_step_arg(a.new_lens) || !map_step_arg(a.accepted_rows))
+    if (!map_current_arg(a.leaf) || !map_current_arg(a.parents) || !map_current_arg(a.query_start) ||
+        !map_current_arg(a.seq_lens) || !map_current_arg(a.block_tables) ||
+        !map_current_arg(a.new_lens) || !map_current_arg(a.accepted_rows))
         return PA_ERR_INVALID_ARG;
     int vec = 16;
     while (vec > 2 && a.row_bytes % vec) vec >>= 1;
@@ -610,8 +645,9 @@ pa_status pa_accept_tree(const int32_t* leaf, const int32_t* parents,
         if (bases[x] - bases[x - 1] < cache_bytes) return PA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (debug::enabled()) {
-        const pa_status r = debug::check_tree(a.query_start, num_seqs, a.parents, total_q,
-                                              max_q_len, a.leaf, st);
+        const pa_status r = debug_pass([&] {
+            return debug::check_tree(a.query_start, num_seqs, a.parents, total_q, max_q_len, a.leaf, st);
+        });
         if (r != PA_OK) return r;
     }
     for (int32_t l0 = 0; l0 < num_layers; l0 += kAcceptLayers) {

@@ -147,6 +147,70 @@ def test_plan_bad_ids_lose_their_tokens_only(cuda_device):
     assert got["tables"][0][1] == -1
 
 
+def test_plan_without_sequences(cuda_device):
+    st = PlanState([], [], 4, 6, 2, seed=1)
+    st.tables = torch.zeros(0, 2, dtype=torch.int32)
+    got = _plan(cuda_device, st, [], 3, max_tokens=5)
+    assert pa.last_device_error() == 0
+    assert got["free_head"] == [3] and got["query_start_loc"] == [0] == got["block_start"]
+    assert got["slot_mapping"] == got["positions"] == got["seq_ids"] == [-1] * 5
+
+
+@pytest.mark.parametrize("offset", [0, 1, 3])
+@pytest.mark.parametrize("n,most", [(5, 40), (3000, 30000)])
+def test_plan_into_unaligned_buffers_of_odd_sizes(cuda_device, offset, n, most):
+    """Token buffers that start off a 16-byte boundary, positions and ids left
+    out, and neighbours of the buffers untouched."""
+    rng = np.random.default_rng(n + offset)
+    lens, new = rng.integers(0, 50, n).tolist(), rng.integers(0, 9, n).tolist()
+    st = PlanState(lens, [0] * n, 8, 10 * n, 9, seed=n)
+    tokens = most + offset
+    plan = pa.StepPlan.empty(n, tokens, cuda_device)
+    slots = torch.full((tokens + 8,), 77, dtype=torch.int64, device=cuda_device)
+    plan.slot_mapping, plan.positions, plan.seq_ids = slots[offset:offset + tokens], None, None
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    tables = st.tables.to(cuda_device)
+    pa.plan_step(dev(lens), dev(new), tables, dev(st.held), dev(st.free), dev([0]), st.num_blocks, 8,
+                 plan)
+    torch.cuda.synchronize()
+    assert pa.last_device_error() == 0
+    ref = plan_reference(st, new, 0, tokens)
+    assert plan.slot_mapping.tolist() == ref["slot_mapping"] and tables.tolist() == ref["tables"]
+    assert (slots[:offset] == 77).all() and (slots[offset + tokens:] == 77).all()
+
+
+@pytest.mark.parametrize("n", [4096, 4097, 20000, 65535])
+def test_plan_of_many_sequences(cuda_device, n):
+    """Past one round of the scan: sums against torch's."""
+    g = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 60, (n,), generator=g, dtype=torch.int32)
+    new = torch.randint(0, 4, (n,), generator=g, dtype=torch.int32)
+    held = (lens + 7) // 8
+    need = torch.maximum(held, (lens + new + 7) // 8)
+    blocks = int(need.sum())
+    tables = torch.full((n, 9), -1, dtype=torch.int32)
+    perm = torch.randperm(blocks, generator=g).int()
+    used = torch.arange(9) < held[:, None]
+    tables[used] = perm[:int(held.sum())]
+    free = perm[int(held.sum()):].contiguous()
+    dev = [x.to(cuda_device) for x in (lens, new, tables, held, free)]
+    plan = pa.plan_step(*dev, torch.zeros(1, dtype=torch.int32, device=cuda_device), blocks, 8,
+                        max_tokens=int(new.sum()))
+    torch.cuda.synchronize()
+    assert pa.last_device_error() == 0
+    start = torch.cat([torch.zeros(1, dtype=torch.int64), new.cumsum(0)])
+    assert torch.equal(plan.query_start_loc.cpu().long(), start)
+    assert int(plan.free_head) == free.numel()
+    fresh = (torch.arange(9) >= held[:, None]) & (torch.arange(9) < need[:, None])
+    tables[fresh] = free
+    assert torch.equal(dev[2].cpu(), tables)
+    seq = torch.repeat_interleave(torch.arange(n), new.long())
+    pos = lens[seq] + torch.arange(seq.numel()) - start[seq]
+    slot = tables[seq, pos // 8].long() * 8 + pos % 8
+    assert torch.equal(plan.slot_mapping.cpu(), slot)
+    assert torch.equal(plan.positions.cpu().long(), pos) and torch.equal(plan.seq_ids.cpu().long(), seq)
+
+
 # ---- pa_decode_tree ----------------------------------------------------------------------
 
 # kv heads, group, head dim, block size, dtype
@@ -154,10 +218,13 @@ SHAPES = [
     (2, 4, 128, 16, BF), (1, 8, 128, 32, BF), (4, 1, 64, 16, BF), (2, 5, 96, 24, BF),
     (2, 2, 80, 8, BF), (1, 16, 64, 64, BF), (2, 3, 112, 40, BF), (1, 4, 16, 16, BF),
     (1, 7, 48, 8, BF), (1, 33, 128, 16, BF), (1, 128, 64, 16, BF), (1, 200, 64, 16, BF),
-    (2, 2, 256, 16, BF), (1, 1, 144, 16, BF), (2, 2, 64, 4, BF), (1, 3, 32, 5, BF),
+    (1, 4, 128, 48, BF), (1, 2, 64, 96, BF), (1, 3, 128, 256, BF), (1, 2, 64, 512, BF),
+    (2, 2, 256, 16, BF), (1, 1, 144, 16, BF), (1, 20, 256, 16, BF), (1, 9, 128, 4, BF),
+    (1, 2, 8, 16, BF), (1, 40, 72, 16, BF), (2, 2, 64, 4, BF), (1, 3, 32, 5, BF),
     (1, 3, 20, 5, BF), (1, 2, 72, 16, BF),
     (2, 4, 128, 16, F32), (1, 3, 64, 24, F32), (1, 1, 256, 16, F32), (2, 2, 20, 5, F32),
-    (1, 2, 7, 3, F32), (1, 70, 36, 16, F32),
+    (1, 2, 7, 3, F32), (1, 70, 36, 16, F32), (1, 20, 16, 8, F32), (1, 9, 200, 16, F32),
+    (1, 12, 128, 1, F32),
 ]
 
 
@@ -374,6 +441,90 @@ def test_pinned_arguments_and_unaligned_queries(cuda_device):
     args = b.to(cuda_device)
     args[3] = k
     assert_tree_close(pa.decode_tree(*args, b.max_q, b.max_len, b.scale), ref, bound, BF)
+
+
+@pytest.mark.parametrize("n,d,dtype", [(129, 64, BF), (20000, 64, BF), (20000, 20, F32),
+                                       (65535, 16, BF)])
+def test_batches_of_many_sequences(cuda_device, n, d, dtype):
+    """Every sequence one node on one cached token: a mean of two value rows
+    weighted by two scores."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k = torch.randn(n, 1, 8, d, generator=g, device=cuda_device).to(dtype)
+    v = torch.randn(n, 1, 8, d, generator=g, device=cuda_device).to(dtype)
+    q = torch.randn(n, 1, d, generator=g, device=cuda_device).to(dtype)
+    i32 = lambda *a: torch.arange(*a, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    lens = torch.full((n,), 2, dtype=torch.int32, device=cuda_device)
+    got = pa.decode_tree(q, i32(n + 1), torch.full_like(lens, -1), k, v, i32(n)[:, None].contiguous(),
+                         lens, 1, 8)
+    torch.cuda.synchronize()
+    assert pa.last_device_error() == 0
+    kk, vv, qq = k[:, 0, :2].double(), v[:, 0, :2].double(), q.double()
+    s = (qq @ kk.transpose(1, 2)) / math.sqrt(d)
+    p = torch.softmax(s, 2)
+    ref = p @ vv
+    # as tree_reference's bound, with one ds for all rows
+    ds = (d + 4) * 2.0 ** -24 / math.sqrt(d) * float((qq.abs() @ kk.abs().transpose(1, 2)).max())
+    bound = (p @ vv.abs()) * (2 * ds + 4 * 2.0 ** -24 + 2.0 ** -19 + (2.0 ** -15 if dtype == BF else 0))
+    assert_tree_close(got, ref.cpu(), bound.cpu(), dtype)
+
+
+def test_positions_of_one_block_shared_by_a_long_table(cuda_device):
+    """A table whose rows all name one block: 400,000 positions over 16 rows of
+    keys give the softmax over those 16, whatever the split."""
+    d, bs, blocks = 64, 16, 25000
+    g = torch.Generator().manual_seed(5)
+    k = torch.randn(2, 1, bs, d, generator=g).to(BF)
+    v = torch.randn(2, 1, bs, d, generator=g).to(BF)
+    q = torch.randn(1, 2, d, generator=g).to(BF)
+    tables = torch.zeros(1, blocks + 1, dtype=torch.int32)
+    tables[0, -1] = 1
+    lens = torch.tensor([blocks * bs + 1], dtype=torch.int32)
+    dev = [x.to(cuda_device) for x in (q, torch.tensor([0, 1], dtype=torch.int32),
+                                       torch.tensor([-1], dtype=torch.int32), k, v, tables, lens)]
+    got = pa.decode_tree(*dev, 1, int(lens[0])).double().cpu()
+    s = torch.cat([k[0, 0].double(), k[1, 0, :1].double()]) @ q[0].double().T / math.sqrt(d)
+    w = torch.exp(s) * torch.tensor([float(blocks)] * bs + [1.0], dtype=torch.float64)[:, None]
+    vv = torch.cat([v[0, 0].double(), v[1, 0, :1].double()])
+    p = w / w.sum(0)
+    ds = (d + 4) * 2.0 ** -24 / 8 * float((k[0, 0].double().abs() @ q[0].double().abs().T).max())
+    # 400,001 keys: sums of 128 a block, the rest as that many rounded additions
+    n = int(lens[0]) / 128 + 128
+    bound = (p.T @ vv.abs()) * (2 * ds + 2 * n * 2.0 ** -24 + 2.0 ** -19 + 2.0 ** -15)
+    assert_tree_close(got[0], p.T @ vv, bound, BF)
+
+
+def test_unaligned_outputs_of_cut_units(cuda_device):
+    b = Batch([5000, 40], [5, 2], 1, 2, 64, 16, BF, seed=12)
+    ref, bound = tree_reference(b)
+    store = torch.full((b.q.numel() + 2,), 7.0, dtype=BF, device=cuda_device)
+    out = store[1:-1].view(b.q.shape)                           # 2-byte aligned
+    pa.decode_tree(*b.to(cuda_device), b.max_q, b.max_len, b.scale, out=out)
+    torch.cuda.synchronize()
+    assert_tree_close(out, ref, bound, BF)
+    assert float(store[0]) == 7.0 == float(store[-1])
+
+
+def test_side_streams_own_what_a_call_allocates(cuda_device):
+    """Calls on a stream that is not the current one, their workspaces dropped
+    at once while the current stream allocates."""
+    b = Batch([6000, 900], [6, 9], 2, 4, 128, 16, BF, seed=4)
+    ref, bound = tree_reference(b)
+    args = b.to(cuda_device)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for s in (side, side.cuda_stream, side):
+        outs.append(pa.decode_tree(*args, b.max_q, b.max_len, b.scale, stream=s))
+        torch.full((64 << 20,), float("nan"), device=cuda_device)
+    leaf = torch.tensor([5, 8], dtype=torch.int32, device=cuda_device)
+    side.wait_stream(torch.cuda.current_stream())
+    lens, rows = pa.accept_tree(leaf, args[2], args[1], args[6], args[3], args[4], args[5], b.max_q,
+                                stream=side)
+    torch.cuda.synchronize()
+    for out in outs:
+        assert_tree_close(out, ref, bound, BF)
+    want = accept_reference(b, [5, 8], b.k, b.v)
+    assert torch.equal(lens.cpu(), want[0]) and torch.equal(rows.cpu(), want[1])
 
 
 def test_two_calls_at_once_with_their_own_workspaces(cuda_device):

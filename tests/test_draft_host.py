@@ -23,9 +23,12 @@ def _desc(**kw):
 
 
 def test_empty_batches_are_no_ops(lib):
+    # (a plan without sequences still has outputs to write)
     assert lib.pa_plan_step(None, None, None, 0, None, 0, None, None, 8, 16, None, 4, None, None,
-                            None, None, None, None, None, None, 0, None) == pa.PA_OK
+                            None, None, None, None, None, None, 0, None) == pa.PA_ERR_INVALID_ARG
     assert lib.pa_decode_tree(None, None, None, 0, 0, None, None, None, 4, None, 0, 0, 32, 1.0,
+                              None, None, 0, _desc(), None) == pa.PA_OK
+    assert lib.pa_decode_tree(None, None, None, 7, 0, None, None, None, 4, None, 3, 9, 32, 1.0,
                               None, None, 0, _desc(), None) == pa.PA_OK
     assert lib.pa_accept_tree(None, None, None, None, 0, 0, 0, None, 4, None, None, 1, None, None,
                               _desc(), None) == pa.PA_OK
@@ -37,6 +40,7 @@ def test_empty_batches_are_no_ops(lib):
     (32, 70, 60, 4, 128, 1),        # more nodes than tokens
     (32, -1, 60, 4, 128, 1), (32, 4, -1, 4, 128, 1),
     (32, 257, 300, 40, 128, 2),     # past PA_MAX_TREE_NODES
+    (32, 4, 2 ** 31 - 1, 2 ** 28, 128, 2),   # positions past 32 bits
     (32, 4, 60, 4, 264, 2),         # past the largest head dim
 ])
 def test_tree_argument_errors(lib, hq, max_q, max_len, width, dim, status):
