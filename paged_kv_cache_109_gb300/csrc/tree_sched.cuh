@@ -267,25 +267,44 @@ __device__ __forceinline__ int64_t tree_row(const TreeArgs& a, const TreeSeg& s,
 template <int KC, int WARPS>
 __device__ __forceinline__ void tree_copy(const TreeArgs& a, int64_t row, int32_t pieces, uint32_t kb,
                                           int32_t kst, uint32_t vb, int32_t vst) {
-    static_assert(KC <= 32, "a key a lane");
+    static_assert(KC <= 32 && KC % WARPS == 0, "a key a lane");
     const int32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint8_t* kc = static_cast<const uint8_t*>(a.k_cache);
     const uint8_t* vc = static_cast<const uint8_t*>(a.v_cache);
-    // lanes per row: a power of two up to 32, so short rows go several at a time
-    int32_t shift = 5;
+    const int64_t off = row < 0 ? -1 : row * pieces * 16;
+    if (pieces > 16) {
+        // a row a warp at a time
+#pragma unroll
+        for (int32_t u = 0; u < KC / WARPS; ++u) {
+            const int32_t k = warp + u * WARPS;
+            const int64_t r = __shfl_sync(0xffffffffu, off, k);
+            const uint32_t bytes = r < 0 ? 0u : 16u;
+            const int64_t src = r < 0 ? 0 : r + lane * 16;
+            if (lane < pieces) {
+                cp_async16(kb + k * kst + lane * 16, kc + src, bytes);
+                cp_async16(vb + k * vst + lane * 16, vc + src, bytes);
+            }
+            for (int32_t p = lane + 32; p < pieces; p += 32) {
+                const int64_t more = r < 0 ? 0 : r + p * 16;
+                cp_async16(kb + k * kst + p * 16, kc + more, bytes);
+                cp_async16(vb + k * vst + p * 16, vc + more, bytes);
+            }
+        }
+        return;
+    }
+    // short rows: several at a time, lanes per row a power of two
+    int32_t shift = 4;
     while (shift > 0 && (1 << (shift - 1)) >= pieces) --shift;
-    const int32_t p0 = lane & ((1 << shift) - 1), sub = lane >> shift, rows = 32 >> shift;
+    const int32_t p = lane & ((1 << shift) - 1), sub = lane >> shift, rows = 32 >> shift;
 #pragma unroll 4
     for (int32_t k0 = warp * rows; k0 < KC; k0 += WARPS * rows) {
         const int32_t k = k0 + sub;
-        const int64_t r = __shfl_sync(0xffffffffu, row, k & 31);
-        if (k >= KC) continue;
-        const int64_t off = r < 0 ? 0 : r * pieces * 16;
+        const int64_t r = __shfl_sync(0xffffffffu, off, k & 31);
+        if (k >= KC || p >= pieces) continue;
+        const int64_t src = r < 0 ? 0 : r + p * 16;
         const uint32_t bytes = r < 0 ? 0u : 16u;
-        for (int32_t p = p0; p < pieces; p += 32) {
-            cp_async16(kb + k * kst + p * 16, kc + off + p * 16, bytes);
-            cp_async16(vb + k * vst + p * 16, vc + off + p * 16, bytes);
-        }
+        cp_async16(kb + k * kst + p * 16, kc + src, bytes);
+        cp_async16(vb + k * vst + p * 16, vc + src, bytes);
     }
 }
 

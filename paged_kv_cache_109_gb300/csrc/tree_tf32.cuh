@@ -10,7 +10,7 @@
 // a persistent CTA of one, two or four warps, the fewest that cover a sequence's
 // rows, takes the parts of its range (tree_sched.cuh) one after another.  Keys come in chunks of KC through a
 // double buffer of 16-byte cp.async copies:
-//   S = Q K^T   (q scaled by scale log2 e), online softmax in base 2, O += P V.
+//   S = Q K^T, online softmax in base 2 (S times scale log2 e), O += P V.
 // A contraction's index may be taken in any order that both operands share, so
 // the fragments are read 16 bytes at a time:
 //   S: lane (g, t) holds columns 4 t .. 4 t + 3 of each 16 of Q's row g and K's
@@ -118,37 +118,24 @@ tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
                           smem_u32(vs + (c & 1) * KC * vst), vst * 4);
             cp_async_commit();
         };
-        issue(sg.kb0, find(sg.kb0));
-        TreeEntry next = find(sg.kb0 + 1);
-        // rows in use of Q (idle rows' scores reach no other row): a warp takes a
-        // row at a time, eight rows' loads before their stores
+        // rows in use of Q (idle rows' scores reach no other row), a warp a row at a
+        // time; plain loads where q is not 16-byte aligned
         const bool q16 = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0;
-        const int32_t rows = sg.ntok * HT;
-        for (int32_t r0 = warp; r0 < rows; r0 += 8 * WARPS) {
+        for (int32_t rho = warp; rho < sg.ntok * HT; rho += WARPS) {
+            const int32_t tk = rho / HT, hh = rho - tk * HT;
+            if (hh >= hs) continue;
+            const float* src = q + ((int64_t)(sg.q0 + sg.tok0 + tk) * a.num_q_heads + head_base + hh) * D;
             for (int32_t d = 4 * lane; d < D; d += 128) {
-                float4 v[8];
-#pragma unroll
-                for (int32_t u = 0; u < 8; ++u) {
-                    const int32_t rho = r0 + u * WARPS, tk = rho / HT, hh = rho - tk * HT;
-                    v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (rho >= rows || hh >= hs) continue;
-                    const float* src =
-                        q + ((int64_t)(sg.q0 + sg.tok0 + tk) * a.num_q_heads + head_base + hh) * D + d;
-                    if (q16)
-                        v[u] = *reinterpret_cast<const float4*>(src);
-                    else
-                        v[u] = make_float4(src[0], src[1], src[2], src[3]);
-                }
-                const float c = a.scale_log2;
-#pragma unroll
-                for (int32_t u = 0; u < 8; ++u) {
-                    const int32_t rho = r0 + u * WARPS;
-                    if (rho < rows)
-                        *reinterpret_cast<float4*>(qs + rho * kst + d) =
-                            make_float4(v[u].x * c, v[u].y * c, v[u].z * c, v[u].w * c);
-                }
+                float* dst = qs + rho * kst + d;
+                if (q16)
+                    cp_async16(smem_u32(dst), src + d, 16u);
+                else
+                    *reinterpret_cast<float4*>(dst) =
+                        make_float4(src[d], src[d + 1], src[d + 2], src[d + 3]);
             }
         }
+        issue(sg.kb0, find(sg.kb0));       // q and the first chunk
+        TreeEntry next = find(sg.kb0 + 1);
         tree_visible(a, sg, up, bits);
 
         // this lane's two rows: warp * 16 + grp (half 0) and + 8 (half 1)
@@ -235,7 +222,8 @@ tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
 #pragma unroll
                 for (int32_t n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int32_t e = 0; e < 4; ++e) s[n][e] += sc[n][e] + sd[n][e];
+                    for (int32_t e = 0; e < 4; ++e)
+                        s[n][e] = (s[n][e] + (sc[n][e] + sd[n][e])) * a.scale_log2;
 
                 // mask, online softmax of rows grp (h = 0) and grp + 8 (h = 1);
                 // a row's columns are spread over its 4 lanes
