@@ -4,11 +4,17 @@
 //   out[r] = sum_t softmax_t(scale q_r.k_t) v_t over the cached tokens, the
 //   node's ancestors and itself.
 //
-// What bounds it: K and V are read once per unit and serve all its rows, 4 D
-// operations per row and key against 4 D bytes per key, so up to about 250
-// rows a kv head the cache's bytes decide.  The kernel is therefore one
-// persistent CTA per SM that keeps a ring of K/V blocks full through the whole
-// of its range (tree_sched.cuh), across the ends of units.
+// What bounds it: K and V are read once per unit and serve all its rows, 6 D
+// operations per row and key (P in two parts) against 4 D bytes per key, so with
+// one tile in use the cache's bytes decide and with two the products: measured
+// on one GB300 (D = 128, 38 sequences x 8 kv heads x 64 key blocks) 203 us = 6270
+// GB/s of K and V, 93% of the copy rate, with 64 rows, and 312 us = 4090 GB/s with
+// 256 rows, where the GPU then runs into its power limit (1.7 of 2.07 GHz).  P as
+// one bf16 part would take 237 us there, at 1.4 times the error: the second part
+// stays, so that a verified row is as near to the decode's as the formula allows.
+//
+// The kernel is one persistent CTA per SM that keeps a ring of K/V blocks full
+// through the whole of its range (tree_sched.cuh), across the ends of units.
 //
 // A unit has two tiles of 128 rows = (node, query head of the group) pairs,
 // head fastest; keys come in blocks of 128.
@@ -101,6 +107,14 @@ struct TreeWsCfg {
 // its high word (SBO, version, swizzle).
 __device__ __forceinline__ uint64_t umma_desc(uint32_t lo, uint32_t hi) {
     return (uint64_t)hi << 32 | lo;
+}
+
+// split_bf16x2 with one packed subtraction.
+__device__ __forceinline__ void split_bf16x2_packed(float2 x, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16x2(x.x, x.y);
+    const float2 h = make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+    const float2 d = __ffma2_rn(h, make_float2(-1.f, -1.f), x);
+    lo = pack_bf16x2(d.x, d.y);
 }
 
 // Any of the two bf16 values not finite (exponent all ones).
@@ -545,11 +559,11 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 // 64 keys of S at a time: mask them and take their maximum; move
                 // this row's reference m if the block's exceeds it by more than 8
                 // (so O is rescaled rarely; p <= 2^8); then again 64 at a time p =
-                // 2^(s c - m), as hi + lo over the same columns of S.  (The loops are
-                // not unrolled: a call's first pass is bound by instruction
-                // fetches.  Publishing P by halves, so that its products begin
-                // beside the second half's softmax, cost the MMA warp more in waits
-                // than it gave.)
+                // 2^(s c - m), as hi + lo over the same columns of S.  (Publishing P
+                // by halves, so that its products begin beside the other half's
+                // softmax, cost the MMA warp more in waits than it gave: 126 us
+                // became 138 on 32 multi-head sequences, and two tiles in use run at
+                // the power limit either way.)
                 uint32_t sr[2][32];
                 float mx = -INFINITY;
                 auto load = [&](int32_t hh) {
@@ -584,7 +598,7 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const float ref = m_ref == -INFINITY ? 0.f : m_ref;
                 const float2 c2 = make_float2(c, c), nm2 = make_float2(-ref, -ref);
                 float2 rs[2] = {make_float2(l * al, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
+#pragma unroll
                 for (int32_t hh = 1; hh >= 0; --hh) {     // (the second half's are in registers)
                     if (hh == 0) load(0);
                     uint32_t pk[32], plo[32];             // hi and lo parts of P
@@ -596,7 +610,7 @@ tree_ws_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                                      c2, nm2);
                         const float2 pp = make_float2(ex2_approx(xx.x), ex2_approx(xx.y));
                         rs[jj & 1] = __fadd2_rn(rs[jj & 1], pp);
-                        split_bf16x2(pp.x, pp.y, pk[jj], plo[jj]);
+                        split_bf16x2_packed(pp, pk[jj], plo[jj]);
                     }
                     tmem_st32_async(s_tm + hh * 64, pk);
                     tmem_st32_async(s_tm + hh * 64 + 32, plo);
