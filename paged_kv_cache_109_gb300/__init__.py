@@ -475,18 +475,21 @@ def prefill(q, query_start_loc, k_cache, v_cache, block_tables, seq_lens, max_q_
 # ---- drafted (speculative) steps ------------------------------------------------
 #
 # These calls run once a layer or a step with little work on the GPU, so their
-# checks stay few and plain: one pass over the tensors, no copies.
+# checks here are few: what would be read wrongly (dtype, strides, sizes).  Where
+# the memory is, the library checks (PaError for another device's or pageable
+# memory).
 
-def _step_args(device: int, *ts) -> None:
-    """Contiguous tensors on CUDA device ``device`` or in page-locked memory."""
+def _contiguous(*ts) -> None:
     for t in ts:
-        if t.is_cuda:
-            if t.get_device() != device:
-                raise ValueError("tensors live on different devices")
-        elif not t.is_pinned():
-            raise ValueError("tensors must be on a CUDA device or in page-locked host memory")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
+
+
+def _int32(*ts) -> None:
+    i32 = torch.int32
+    for t in ts:
+        if t.dtype is not i32:
+            raise ValueError("lengths, tables, rows and indices must be int32")
 
 
 def _current(t) -> int:
@@ -595,15 +598,12 @@ def plan_step(seq_lens, new_tokens, block_tables, blocks_held, free_blocks, free
         ints += (seq_ids,)
     if ref_cnt is not None:
         ints += (ref_cnt,)
-        if not ref_cnt.is_cuda or ref_cnt.numel() != num_blocks:
-            raise ValueError("ref_cnt must be a device tensor of num_blocks entries")
-    i32 = torch.int32
-    for t in ints:
-        if t.dtype is not i32:
-            raise ValueError("all but slot_mapping must be int32")
+        if ref_cnt.numel() != num_blocks:
+            raise ValueError("ref_cnt must have num_blocks entries")
     if slots.dtype is not torch.int64:
         raise ValueError("slot_mapping must be int64")
-    _step_args(device, slots, *ints)
+    _int32(*ints)
+    _contiguous(slots, *ints)
     st = load_library().pa_plan_step(
         seq_lens.data_ptr(), new_tokens.data_ptr(), blocks_held.data_ptr(), n,
         free_blocks.data_ptr(), free_blocks.numel(), free_head.data_ptr(), _ptr(ref_cnt),
@@ -648,10 +648,7 @@ def decode_tree(q, query_start_loc, parents, k_cache, v_cache, block_tables, seq
     n = seq_lens.numel()
     if q.dtype is not dtype or v_cache.dtype is not dtype:
         raise ValueError("q and caches must share one dtype")
-    i32 = torch.int32
-    if query_start_loc.dtype is not i32 or parents.dtype is not i32 \
-            or block_tables.dtype is not i32 or seq_lens.dtype is not i32:
-        raise ValueError("query_start_loc, parents, block_tables and seq_lens must be int32")
+    _int32(query_start_loc, parents, block_tables, seq_lens)
     if query_start_loc.numel() != n + 1 or parents.numel() != total \
             or block_tables.dim() != 2 or block_tables.shape[0] != n:
         raise ValueError("query_start_loc, parents, block_tables and seq_lens disagree on the "
@@ -669,9 +666,9 @@ def decode_tree(q, query_start_loc, parents, k_cache, v_cache, block_tables, seq
         if ws_bytes:
             workspace = _empty(ws_bytes, torch.uint8, device, stream)
     else:
-        _dev(workspace)
+        _contiguous(workspace)
         ws_bytes = workspace.numel() * workspace.element_size()
-    _step_args(device, k_cache, v_cache, q, query_start_loc, parents, block_tables, seq_lens, out)
+    _contiguous(k_cache, v_cache, q, query_start_loc, parents, block_tables, seq_lens, out)
     st = lib.pa_decode_tree(
         q.data_ptr(), query_start_loc.data_ptr(), parents.data_ptr(), total, max_q_len,
         k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
@@ -742,11 +739,8 @@ def accept_tree(leaf, parents, query_start_loc, seq_lens, k_caches, v_caches, bl
     if new_lens.numel() != n or accepted_rows.numel() != total:
         raise ValueError("new_lens must have N and accepted_rows total_q entries")
     ints = (leaf, parents, query_start_loc, seq_lens, block_tables, new_lens, accepted_rows)
-    i32 = torch.int32
-    for t in ints:
-        if t.dtype is not i32:
-            raise ValueError("all arguments but the caches must be int32")
-    _step_args(device, *ints)
+    _int32(*ints)
+    _contiguous(*ints)
     ptrs = ctypes.c_void_p * len(keys)
     desc = CacheDesc(shape[0], shape[2], shape[1], shape[3], _DTYPES[dtype])
     st = load_library().pa_accept_tree(

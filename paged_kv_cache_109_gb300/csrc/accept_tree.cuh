@@ -17,12 +17,15 @@ namespace pa {
 
 constexpr int kAcceptThreads = 128;
 constexpr int kAcceptUnroll = 4;
-constexpr int kAcceptLayers = 128;      // layers of one launch (2 KB of pointers)
+// Layers of one launch: 16, or 128 (2 KB of pointers, which the host copies for
+// every launch).
+constexpr int kAcceptFew = 16, kAcceptLayers = 128;
 constexpr int kAcceptMaxLayers = 1024;  // layers of one call
 
+template <int LAYERS>
 struct AcceptCaches {
-    uint8_t* k[kAcceptLayers];
-    uint8_t* v[kAcceptLayers];
+    uint8_t* k[LAYERS];
+    uint8_t* v[LAYERS];
 };
 
 struct AcceptArgs {
@@ -38,9 +41,9 @@ struct AcceptArgs {
 };
 
 // One CTA per (sequence, layer, K or V).
-template <int VEC>
+template <int VEC, int LAYERS>
 __global__ void __launch_bounds__(kAcceptThreads)
-accept_tree_kernel(const AcceptArgs a, const __grid_constant__ AcceptCaches caches) {
+accept_tree_kernel(const AcceptArgs a, const __grid_constant__ AcceptCaches<LAYERS> caches) {
     using V = typename VecType<VEC>::T;
     __shared__ int32_t s_parent[PA_MAX_TREE_NODES];
     __shared__ int32_t s_path[PA_MAX_TREE_NODES];

@@ -89,6 +89,23 @@ pa_status plan_impl(PlanArgs a, cudaStream_t st) {
     return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+template <int LAYERS>
+cudaError_t launch_accept(const AcceptArgs& a, void* const* k, void* const* v, int32_t layers,
+                          int32_t num_seqs, int vec, cudaStream_t st) {
+    AcceptCaches<LAYERS> c;
+    for (int32_t l = 0; l < layers; ++l) {
+        c.k[l] = static_cast<uint8_t*>(k[l]);
+        c.v[l] = static_cast<uint8_t*>(v[l]);
+    }
+    const dim3 grid(num_seqs, 2 * layers);
+    switch (vec) {
+        case 16: return launch_pdl(accept_tree_kernel<16, LAYERS>, grid, dim3(kAcceptThreads), 0, st, a, c);
+        case 8: return launch_pdl(accept_tree_kernel<8, LAYERS>, grid, dim3(kAcceptThreads), 0, st, a, c);
+        case 4: return launch_pdl(accept_tree_kernel<4, LAYERS>, grid, dim3(kAcceptThreads), 0, st, a, c);
+        default: return launch_pdl(accept_tree_kernel<2, LAYERS>, grid, dim3(kAcceptThreads), 0, st, a, c);
+    }
+}
+
 // ---- tree attention: kernel choice, work division, workspace ---------------------
 
 // Rows of one copy of the tcgen05 tree kernel: it lies inside one block and
@@ -652,23 +669,11 @@ pa_status pa_accept_tree(const int32_t* leaf, const int32_t* parents,
     }
     for (int32_t l0 = 0; l0 < num_layers; l0 += kAcceptLayers) {
         const int32_t nl = std::min(kAcceptLayers, num_layers - l0);
-        AcceptCaches c{};
-        for (int32_t l = 0; l < nl; ++l) {
-            c.k[l] = static_cast<uint8_t*>(k_caches[l0 + l]);
-            c.v[l] = static_cast<uint8_t*>(v_caches[l0 + l]);
-        }
         if (l0 > 0) a.new_lens = nullptr;        // written by the first launch
-        const dim3 grid(num_seqs, 2 * nl);
-        auto go = [&](auto kern) {
-            return launch_pdl(kern, grid, dim3(kAcceptThreads), 0, st, a, c);
-        };
-        cudaError_t err;
-        switch (vec) {
-            case 16: err = go(accept_tree_kernel<16>); break;
-            case 8: err = go(accept_tree_kernel<8>); break;
-            case 4: err = go(accept_tree_kernel<4>); break;
-            default: err = go(accept_tree_kernel<2>); break;
-        }
+        const cudaError_t err =
+            nl <= kAcceptFew
+                ? launch_accept<kAcceptFew>(a, k_caches + l0, v_caches + l0, nl, num_seqs, vec, st)
+                : launch_accept<kAcceptLayers>(a, k_caches + l0, v_caches + l0, nl, num_seqs, vec, st);
         if (err != cudaSuccess) return PA_ERR_CUDA;
     }
     return PA_OK;

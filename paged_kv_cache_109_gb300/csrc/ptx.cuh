@@ -76,17 +76,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int3
         : "memory");
 }
 
-// 5-D tiled bulk tensor load global -> shared, completion counted on `bar`.
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int32_t c0, int32_t c1,
-                                            int32_t c2, int32_t c3, int32_t c4, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
-        : "memory");
-}
-
-// 3-D load with an L2 cache policy (e.g. evict-first for streamed K/V).
+// Same, with an L2 cache policy (e.g. evict-first for streamed K/V).
 __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const void* tmap, int32_t x,
                                                  int32_t y, int32_t z, uint32_t bar,
                                                  uint64_t policy) {

@@ -103,6 +103,16 @@ struct TreeWsCfg {
     static_assert(sizeof(TreeSeg) % 16 == 0, "queue entries");
 };
 
+// 5-D tiled bulk tensor load global -> shared, completion counted on `bar`.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3, int32_t c4, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+}
+
 // A shared-memory matrix descriptor from its low word (start address, LBO) and
 // its high word (SBO, version, swizzle).
 __device__ __forceinline__ uint64_t umma_desc(uint32_t lo, uint32_t hi) {
