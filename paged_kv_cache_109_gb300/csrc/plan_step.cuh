@@ -13,10 +13,17 @@
 // (up to kPlanSmallSeqs sequences and kPlanSmallTokens tokens) ends in the same
 // CTA: one launch, whose latency is what such a step costs (a second launch
 // adds 2.5 us on the host).  Otherwise plan_fill_kernel writes tokens and fresh
-// entries from the whole GPU: bound by its 16 bytes a token.  A thread takes four
-// consecutive tokens, one binary search in Q and one table entry for them as
-// long as they share a block, and 16-byte stores (a search a token: 22 us for
-// 2.1 million tokens, bound by its loads; this way 9).
+// entries from the whole GPU.  A thread takes four consecutive tokens, with one
+// table entry for as long as they share a block and 16-byte stores; in global
+// memory a warp searches Q together for its 128 tokens.
+//
+// Measured (GPU time of the whole call): 2048 sequences with some 2.1 million new
+// tokens 19.7 us, where the bytes take 5.6; with a search by each thread 21.0.  It
+// is bound by latencies: the one CTA's scan (8 us) and then the fill's dependent
+// loads; filling the SMs further (32 registers a thread) changed nothing.  In the
+// small form the sums are in shared memory and each thread's own search is the
+// faster one: 6.4 us against 6.8 for a decode step, 8.8 against 9.4 for a drafted
+// one.
 #pragma once
 
 #include "common.cuh"
@@ -80,6 +87,20 @@ __device__ __forceinline__ int32_t plan_find(const int32_t* start, int32_t n, in
     return lo;
 }
 
+// The same by a whole warp, all lanes with one x: 32 probes a round.
+__device__ __forceinline__ int32_t plan_find_warp(const int32_t* start, int32_t n, int32_t x) {
+    const int32_t lane = threadIdx.x & 31;
+    int32_t lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int32_t step = (hi - lo + 32) / 32;
+        const int32_t at = lo + (lane + 1) * step;
+        const uint32_t yes = __ballot_sync(0xffffffffu, at <= hi && start[min(at, hi)] <= x);
+        lo += __popc(yes) * step;
+        hi = min(hi, lo + step - 1);
+    }
+    return lo;
+}
+
 // Block of the queue, -1 and a report for an id outside the pool.
 __device__ __forceinline__ int32_t plan_free(const PlanArgs& a, int32_t at) {
     const int32_t id = a.free_blocks[at];
@@ -113,12 +134,34 @@ __device__ __forceinline__ PlanSpan plan_span(const PlanSums& s, int32_t i) {
     return p;
 }
 
-// Fresh table entries and tokens: thread `first` of `stride`.
+// The sequence of item x of [0, total), all lanes of a warp with consecutive
+// groups of PER items from x0 on (x = x0 + PER * lane).  TOGETHER (sums in global
+// memory): the warp finds the first and the last one's, and only where they
+// differ does each lane search between them.
+template <bool TOGETHER, int32_t PER>
+__device__ __forceinline__ int32_t plan_seq_of(const int32_t* start, int32_t n, int32_t x0,
+                                               int32_t x, int32_t total) {
+    if constexpr (!TOGETHER) {
+        return x < total ? plan_find(start, n, x) : 0;
+    } else {
+        if (x0 >= total) return 0;
+        const int32_t lo = plan_find_warp(start, n, x0);
+        const int32_t end = x0 + min(total - x0, 32 * PER) - 1;
+        const int32_t hi = start[lo + 1] > end ? lo : plan_find_warp(start, n, end);
+        return lo == hi || x >= total ? lo : lo + plan_find(start + lo, hi - lo + 1, x);
+    }
+}
+
+// Fresh table entries and tokens: thread `first` of `stride` (whole warps).
+template <bool TOGETHER>
 __device__ __forceinline__ void plan_fill(const PlanArgs& a, const PlanSums& s, int32_t first,
                                           int32_t stride) {
     const int32_t N = a.num_seqs, B = a.block_size;
-    for (int32_t e = first; e < s.blocks; e += stride) {
-        const int32_t i = plan_find(s.block_start, N, e);
+    const int32_t lane = threadIdx.x & 31;
+    for (int32_t e0 = first - lane; e0 < s.blocks; e0 += stride) {
+        const int32_t e = e0 + lane;
+        const int32_t i = plan_seq_of<TOGETHER, 1>(s.block_start, N, e0, e, s.blocks);
+        if (e >= s.blocks) continue;
         const int32_t b0 = s.block_start[i];
         const int32_t held = s.held[i] - (s.block_start[i + 1] - b0);
         const int32_t id = plan_free(a, s.head + e);
@@ -129,13 +172,16 @@ __device__ __forceinline__ void plan_fill(const PlanArgs& a, const PlanSums& s, 
                         reinterpret_cast<uintptr_t>(a.positions) |
                         reinterpret_cast<uintptr_t>(a.seq_ids)) & 15) == 0;
     const int32_t groups = a.max_tokens / 4 + (a.max_tokens % 4 != 0);
-    for (int32_t g = first; g < groups; g += stride) {
-        const int32_t t0 = 4 * g;
+    for (int32_t g0 = first - lane; g0 < groups; g0 += stride) {
+        const int32_t g = g0 + lane;
+        const int32_t t0 = g < groups ? 4 * g : s.tokens;
+        const int32_t i = plan_seq_of<TOGETHER, 4>(s.query_start, N, 4 * g0, t0, s.tokens);
+        if (g >= groups) continue;
         int64_t slot[4];
         int32_t pos[4], seq[4];
         PlanSpan p{-1, 0, 0, 0, 0, 0, 0};
         int32_t block = -1, id = -1;                  // table column of `id`
-        if (t0 < s.tokens) p = plan_span(s, plan_find(s.query_start, N, t0));
+        if (t0 < s.tokens) p = plan_span(s, i);
 #pragma unroll
         for (int32_t u = 0; u < 4; ++u) {
             const int32_t t = t0 + u;
@@ -316,7 +362,8 @@ __global__ void __launch_bounds__(kPlanScanThreads) plan_scan_kernel(const PlanA
     }
     if constexpr (SMALL) {
         __syncthreads();
-        plan_fill(a, PlanSums{s_query, s_block, s_lens, s_held, q0, b0, head}, tid, kPlanScanThreads);
+        plan_fill<false>(a, PlanSums{s_query, s_block, s_lens, s_held, q0, b0, head}, tid,
+                         kPlanScanThreads);
     }
 }
 
@@ -326,9 +373,9 @@ __global__ void __launch_bounds__(kPlanFillThreads) plan_fill_kernel(const PlanA
     griddep_wait();
     griddep_launch_dependents();
     const int32_t tokens = a.query_start[a.num_seqs], blocks = a.block_start[a.num_seqs];
-    plan_fill(a, PlanSums{a.query_start, a.block_start, a.seq_lens_out, a.blocks_held_out, tokens,
-                          blocks, *a.free_head_out - blocks},
-              blockIdx.x * kPlanFillThreads + threadIdx.x, gridDim.x * kPlanFillThreads);
+    plan_fill<true>(a, PlanSums{a.query_start, a.block_start, a.seq_lens_out, a.blocks_held_out,
+                                tokens, blocks, *a.free_head_out - blocks},
+                    blockIdx.x * kPlanFillThreads + threadIdx.x, gridDim.x * kPlanFillThreads);
 }
 
 }  // namespace pa
