@@ -7,6 +7,10 @@
 // step (a_m > a_j >= j for m > j).  A thread owns the same bytes of every row
 // and takes the steps in order, a batch of loads before that batch's stores,
 // so no thread depends on another.
+//
+// Bound: each moved row's bytes, read and written once.  Measured (GPU time): 128
+// sequences x 16 layers 9.8 us, of which the bytes take 9.0 at the copy rate; one
+// sequence 2.8 us, the launch.
 #pragma once
 
 #include "common.cuh"

@@ -209,8 +209,10 @@ TreeShape tree_tf_tiling(int32_t head_dim, int32_t group, int32_t warps) {
     return s;
 }
 
-// The CUDA-core kernel of the other bf16 shapes: 16, 32 or 64 rows by what a sequence can have (up to 32
-// above 128 columns); 32-key chunks up to 128 columns, 16-key ones up to 256.
+// The CUDA-core kernel of the other bf16 shapes: 16, 32 or 64 rows by what a
+// sequence can have (up to 32 above 128 columns: D = 72, 38 sequences x 16 kv heads
+// x 4000 tokens, 16 rows 956 us, 2460 in tiles of 64; 32 rows 1420, 2460); 32-key
+// chunks up to 128 columns, 16-key ones up to 256.
 int32_t tree_tiled_rpt(int32_t head_dim, int32_t group, int32_t max_q_len) {
     const int64_t rows = (int64_t)group * max_q_len;
     return rows <= 16 ? 1 : rows <= 32 || head_dim > 128 ? 2 : 4;
@@ -314,9 +316,13 @@ TreeLaunch tree_launch(TreeKernel k, const pa_cache_desc* c, int32_t group, int3
         instance = 10 + rpt;
         per_sm = with_tree_tiled(c->head_dim, rpt, resident);
     }
-    // Short sequences go whole: no range ends inside a unit, so no merge follows
-    // (a launch and 3 us, more than a cut of so little work gives).  A unit's
-    // parts then cost the same whatever its length.
+    // Short sequences go whole: no range ends inside a unit, so no merge follows.  A
+    // unit's parts then cost the same whatever its length.  Whole against cut, 1 and
+    // 64 sequences of 8 nodes, 8 kv heads, group 4, D = 128: tcgen05, 500 cached
+    // tokens 12.0, 15.1 and 41.3, 53.6 us, 1000 tokens 17.0, 15.7 and 61.8, 69.9 us,
+    // 2000 tokens 26.9, 16.2 and 106.5, 103.0 us; mma.sync, 118 tokens 19.2, 33.7 and
+    // 24.9, 42.4 us, 500 tokens 48.9, 32.1 and 60.8, 64.5 us; tf32, 118 tokens 35.5,
+    // 38.9 and 43.3, 55.0 us, 500 tokens 105, 39.8 and 133, 131 us.
     if (max_seq_len <= (k == kTreeWs ? 512 : 128)) {
         t.s.fixed_cost = (int32_t)tree_most(t.s, max_q_len, max_seq_len);
         t.s.min_range = t.s.fixed_cost;

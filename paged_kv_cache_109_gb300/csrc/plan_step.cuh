@@ -11,8 +11,9 @@
 // token's block is taken from the table below h_i and straight from the queue
 // above it, so no thread reads an entry that another one writes.  A small step
 // (up to kPlanSmallSeqs sequences and kPlanSmallTokens tokens) ends in the same
-// CTA: one launch, whose latency is what such a step costs (a second launch
-// adds 2.5 us on the host).  Otherwise plan_fill_kernel writes tokens and fresh
+// CTA: one launch, whose latency is what such a step costs (GPU time, one launch
+// against two: 64 sequences with a token each 6.4 us, 10.9; at the limits, 256 x 32
+// tokens 9.2, 9.6 and 1024 x 8 10.6, 11.3).  Otherwise plan_fill_kernel writes tokens and fresh
 // entries from the whole GPU.  A thread takes four consecutive tokens, with one
 // table entry for as long as they share a block and 16-byte stores; in global
 // memory a warp searches Q together for its 128 tokens.

