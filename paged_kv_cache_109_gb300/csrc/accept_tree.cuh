@@ -9,7 +9,8 @@
 // so no thread depends on another.
 //
 // Bound: each moved row's bytes, read and written once.  Measured (GPU time): 128
-// sequences x 16 layers 9.8 us, of which the bytes take 9.0 at the copy rate; one
+// sequences x 16 layers, 61 MB moved, 9.8 us in back-to-back calls, whose rows stay
+// in L2, and 15 us alone with cold caches, where the copy rate allows 9.0; one
 // sequence 2.8 us, the launch.
 #pragma once
 

@@ -19,7 +19,7 @@
 // memory a warp searches Q together for its 128 tokens.
 //
 // Measured (GPU time of the whole call): 2048 sequences with some 2.1 million new
-// tokens 19.7 us, where the bytes take 5.6; with a search by each thread 21.0.  It
+// tokens 19.7 us, where the bytes take 5.0; with a search by each thread 21.0.  It
 // is bound by latencies: the one CTA's scan (8 us) and then the fill's dependent
 // loads; filling the SMs further (32 registers a thread) changed nothing.  In the
 // small form the sums are in shared memory and each thread's own search is the

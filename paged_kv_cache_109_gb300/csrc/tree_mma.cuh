@@ -7,8 +7,8 @@
 // A unit is one tile of 16 rows a warp ((node, query head) pairs, head fastest);
 // a persistent CTA of one, two or four warps, the fewest that cover a sequence's
 // rows, takes the parts of its range (tree_sched.cuh) one after another.  Keys
-// come in chunks of KC through a double buffer of 16-byte cp.async copies, rows padded by 16 bytes so that an
-// ldmatrix reads eight bank groups:
+// come in chunks of KC through a double buffer of 16-byte cp.async copies, rows
+// padded by 16 bytes so that an ldmatrix reads eight bank groups:
 //   S = Q K^T, online softmax in base 2, O += P V with P as bf16 hi + lo (about
 //   16 significant bits, as in the other tensor-core kernels).
 // Bound: the products of mma.sync, 6 D operations per row and key with both
