@@ -82,6 +82,29 @@ def test_plan_prompts_of_many_tiles(cuda_device):
     assert rng is not None
 
 
+@pytest.mark.parametrize("n,new", [
+    (1, {0: 9001}), (2, {1: 8999}), (33, {0: 5000, 32: 4003}),
+    # runs of sequences without tokens at the front, inside and at the end
+    (1025, {1024: 3}), (1057, {0: 1, 512: 2, 513: 300}), (2500, {700: 1, 1500: 140, 1501: 1}),
+    (1500, {i: 1 for i in range(0, 1500, 7)}), (1030, {}),
+])
+def test_plan_of_few_sequences_with_tokens(cuda_device, n, new):
+    """Plans past the one-launch form: a warp's tokens of one sequence, of many,
+    and of sequences that others without tokens lie between."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, 60, n).tolist()
+    counts = [new.get(i, 0) for i in range(n)]
+    width = max(-(-(a + c) // 16) for a, c in zip(lens, counts)) + 2
+    blocks = sum(-(-(a + c) // 16) for a, c in zip(lens, counts)) + n + 3
+    st = PlanState(lens, rng.integers(0, 2, n).tolist(), 16, blocks, width, seed=n)
+    max_tokens = max(sum(counts) + 7, 1)
+    got = _plan(cuda_device, st, counts, 0, max_tokens)
+    assert pa.last_device_error() == 0
+    ref = plan_reference(st, counts, 0, max_tokens)
+    for k in ref:
+        assert got[k] == [list(r) if isinstance(r, tuple) else r for r in ref[k]], k
+
+
 def _unplanned(st, got, head, max_tokens):
     n = len(st.lens)
     assert got["tables"] == st.tables.tolist()
