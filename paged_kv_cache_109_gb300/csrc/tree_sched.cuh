@@ -317,9 +317,12 @@ __device__ __forceinline__ float* tree_cell(const TreeArgs& a, const TreeWork& w
 // starts and does not end.  A thread takes one row and eight columns at a
 // time, lanes along the rows.  Measured alone with cold caches: 13.5 us for the 19 MB
 // of parts that 128 sequences of up to 64 nodes leave (1.4 TB/s, 42% of the warps
-// active, so neither bytes nor instructions bound it), 7.4 us for 1.8 MB.
+// active, so neither bytes nor instructions bound it), 7.4 us for 1.8 MB, with up to
+// 8 CTAs a cut.  16 give a thread one item of the largest tile: a whole call on 24
+// sequences of up to 48 nodes, group 5, D = 96 took 53.5 us with 8, 52.8 with 16,
+// larger batches the same either way.
 constexpr int kTreeMergeThreads = 256;
-constexpr int kTreeMergeSplit = 8;      // CTAs per cut
+constexpr int kTreeMergeSplit = 16;     // CTAs per cut
 
 template <typename E>
 __global__ void __launch_bounds__(kTreeMergeThreads)
