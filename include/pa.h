@@ -519,7 +519,11 @@ pa_status pa_plan_step(const int32_t* seq_lens, const int32_t* new_tokens,
  *   out[r][h] = sum_{t visible} softmax_t(scale * q[r][h].k_t) v_t
  * with kv heads, tables and lengths as in pa_prefill.  A chain (parents[j] =
  * j - 1) is pa_prefill's causal chunk; n_i = 1 is pa_decode's row.  Keys a node
- * does not see leave no trace in its row, whatever their K and V hold.
+ * does not see leave no trace in its row, whatever their K and V hold.  In fp32,
+ * visible values up to the largest, infinities and NaN have the effect that the
+ * formula gives them, computed in 32 bits.  In bf16 that holds for the nodes' V;
+ * an infinity in a cached token's V makes its column infinite or NaN, as in
+ * pa_prefill.
  *
  * q, out           device or pinned [total_q][num_q_heads][head_dim], cache dtype.
  * query_start_loc  device or pinned int32 [num_seqs + 1], non-decreasing.  Rows

@@ -24,11 +24,22 @@
 // Bound: the products, 12 D operations per row and key (three for one) at the
 // mma.sync tf32 rate (measured 300 TFLOP/s, so 100 of the operator's, against 73
 // for FMAs); with one warp's rows in use, the copies.  Measured (D = 128, 38
-// sequences x 8 kv heads x 4000 tokens): 64 rows 771 us = 52 TFLOP/s, 16 rows 438 us
+// sequences x 8 kv heads x 4000 tokens): 64 rows 776 us = 51 TFLOP/s, 16 rows 438 us
 // = 2840 GB/s; 16-key chunks with three CTAs an SM reached 47 TFLOP/s.
 //
 // In chunks that reach past the cached tokens, values of V that are not finite
 // are taken out before the product, and added for the rows that see them.
+//
+// Two parts cannot hold an infinity, nor a value that 11 bits round up to 2^128
+// (|x| >= 0x7f7ff000 as bits): hi - lo is then inf - inf, and what they meet, even
+// with weight 0, becomes NaN.  No later step takes a NaN out of l or O (a NaN score
+// is in l), so rows that end finite are right as they are; a CTA with one that does
+// not goes through its range again and does such rows by FMAs (tree_plain_part),
+// where a hidden key is not read and a visible infinity gives what the formula
+// gives.  Without that look at the rows and with it, which finds nothing: 16 sequences
+// of up to 24 nodes 140.6, 142.2 us; D = 256, 64 rows, 38 sequences x 2000 tokens 1060,
+// 1078.  (Clamping each hi part instead took 152 and 1157, and would leave infinite
+// operands to be told apart.)
 #pragma once
 
 #include "cp_async.cuh"
@@ -54,7 +65,7 @@ struct TreeTfCfg {
     // [rows][8] words | parents | odd keys of the chunk
     static size_t smem_bytes(int32_t D) {
         return 4 * ((size_t)(kRows + 2 * KC) * k_stride(D) + 2 * (size_t)KC * v_stride(D) +
-                    kRows * (PA_MAX_TREE_NODES / 32) + PA_MAX_TREE_NODES + KC);
+                    kRows * (PA_MAX_TREE_NODES / 32) + PA_MAX_TREE_NODES + KC + 1);
     }
 };
 
@@ -74,6 +85,104 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
 }
 
 __device__ __forceinline__ bool f32_odd(float x) { return !(fabsf(x) <= 3.4028235e38f); }
+
+// Those rows of a part that did not end finite again, in 32-bit FMAs: a warp takes
+// a row and 32 keys at a time, a lane a key's score and then every 32nd column of O.
+// Keys that the row does not see are not read.  An infinite value or sum stays one
+// under weights that underflow.
+template <int DMAX, int WARPS>
+__device__ __forceinline__ void tree_plain_part(const TreeArgs& a, const TreeWork& w, const TreeSeg& sg,
+                                                int32_t keys, const uint32_t* bits) {
+    constexpr int32_t kWords = PA_MAX_TREE_NODES / 32;
+    const int32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t D = a.head_dim, HT = w.s.heads, hs = min(HT, a.group - sg.sg * HT);
+    const int32_t* table = a.block_tables + (int64_t)sg.i * a.max_blocks;
+    const float* kc = static_cast<const float*>(a.k_cache);
+    const float* vc = static_cast<const float*>(a.v_cache);
+    const int32_t key0 = sg.kb0 * keys, key1 = min((int64_t)sg.kb1 * keys, (int64_t)sg.T);
+    const bool whole = sg.kb0 == 0 && sg.kb1 == sg.nb;
+    float* cell = whole ? nullptr : tree_cell(a, w, sg);
+#pragma unroll 1
+    for (int32_t rho = warp; rho < sg.ntok * HT; rho += WARPS) {
+        const int32_t tk = rho / HT, hh = rho - tk * HT;
+        if (hh >= hs) continue;
+        const int64_t row = ((int64_t)(sg.q0 + sg.tok0 + tk) * a.num_q_heads + (int64_t)sg.g * a.group +
+                             sg.sg * HT + hh) * D;
+        const float* q = static_cast<const float*>(a.q) + row;
+        float* out = static_cast<float*>(a.out) + row;
+        float* ml = whole ? nullptr : cell + (size_t)D * 16 * WARPS + 2 * rho;
+        auto sum_at = [&](int32_t d) { return cell + ((size_t)(d >> 2) * 16 * WARPS + rho) * 4 + (d & 3); };
+        bool odd = !whole && f32_odd(ml[1]);
+        for (int32_t d = lane; d < D; d += 32) odd |= f32_odd(whole ? out[d] : *sum_at(d));
+        if (!__any_sync(0xffffffffu, odd)) continue;
+        float m = -INFINITY, l = 0.f, acc[DMAX / 32];
+#pragma unroll
+        for (int32_t c = 0; c < DMAX / 32; ++c) acc[c] = 0.f;
+#pragma unroll 1
+        for (int32_t t0 = key0; t0 < key1; t0 += 32) {
+            const int32_t t = t0 + lane, node = t - sg.C;
+            bool sees = t < key1 && (node < 0 || (bits[tk * kWords + (node >> 5)] >> (node & 31) & 1u));
+            int64_t at = 0;
+            if (sees) {
+                const int32_t id = table[t / a.block_size];
+                sees = id >= 0 && id < a.num_blocks;
+                at = (((int64_t)id * a.num_kv_heads + sg.g) * a.block_size + t % a.block_size) * D;
+            }
+            float s = sees ? 0.f : -INFINITY;
+            for (int32_t d = 0; sees && d < D; d += 4) {
+                const float4 y = *reinterpret_cast<const float4*>(kc + at + d);
+                s = fmaf(q[d] * a.scale_log2, y.x, s);
+                s = fmaf(q[d + 1] * a.scale_log2, y.y, s);
+                s = fmaf(q[d + 2] * a.scale_log2, y.z, s);
+                s = fmaf(q[d + 3] * a.scale_log2, y.w, s);
+            }
+            float mx = s;
+            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
+            const float al = exp2f(m - ref), p = exp2f(s - ref);
+            float sum = p;
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            l = fmaf(l, al, sum);
+            m = mn;
+#pragma unroll
+            for (int32_t c = 0; c < DMAX / 32; ++c)
+                if (!f32_odd(acc[c])) acc[c] *= al;
+            for (uint32_t left = __ballot_sync(0xffffffffu, sees); left != 0; left &= left - 1) {
+                const int32_t k = __ffs(left) - 1;
+                const float pk = __shfl_sync(0xffffffffu, p, k);
+                const float* v = vc + __shfl_sync(0xffffffffu, at, k);
+#pragma unroll
+                for (int32_t c = 0; c < DMAX / 32; ++c) {
+                    const int32_t d = lane + 32 * c;
+                    if (d >= D) continue;
+                    const float y = v[d];
+                    acc[c] = f32_odd(y) ? acc[c] + y : fmaf(pk, y, acc[c]);
+                }
+            }
+        }
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int32_t c = 0; c < DMAX / 32; ++c) {
+            const int32_t d = lane + 32 * c;
+            if (d < D) *(whole ? out + d : sum_at(d)) = whole ? acc[c] * inv : acc[c];
+        }
+        if (!whole && lane == 0) *reinterpret_cast<float2*>(ml) = make_float2(m, l);
+    }
+}
+
+// This CTA's range by tree_plain_part.
+template <int DMAX, int WARPS>
+__device__ __forceinline__ void tree_plain_range(const TreeArgs& a, const TreeWork& w, int32_t keys,
+                                                 uint32_t* bits, int32_t* up) {
+    TreeIter it = tree_begin(a, w, reinterpret_cast<int64_t*>(bits));
+    TreeSeg sg;
+    __syncthreads();                     // the search's scratch is free
+    while (tree_next(a, w.s, it, sg)) {
+        tree_visible(a, sg, up, bits);
+        tree_plain_part<DMAX, WARPS>(a, w, sg, keys, bits);
+        __syncthreads();                 // the node masks are free
+    }
+}
 
 template <int DMAX, int KC, int WARPS>
 __global__ void __launch_bounds__(TreeTfCfg<DMAX, KC, WARPS>::kThreads, TreeTfCfg<DMAX, KC, WARPS>::kPerSm)
@@ -95,6 +204,7 @@ tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
     uint32_t* bits = reinterpret_cast<uint32_t*>(vs + 2 * KC * vst);   // [tokens][8]
     int32_t* up = reinterpret_cast<int32_t*>(bits + C::kRows * kWords);
     int32_t* odd = up + PA_MAX_TREE_NODES;                      // [KC] key's V had values taken out
+    int32_t* redo = odd + KC;                                   // a row did not end finite
     const float* q = static_cast<const float*>(a.q);
     const float* vc = static_cast<const float*>(a.v_cache);
 
@@ -103,6 +213,7 @@ tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
     TreeIter it = tree_begin(a, w, reinterpret_cast<int64_t*>(bits));
     TreeSeg sg;
     TreeCut cut{};
+    if (tid == 0) *redo = 0;
     __syncthreads();                     // the search's scratch is free
     while (tree_next(a, w.s, it, sg)) {
         if (sg.kb0 == 0 && sg.parts > 0)
@@ -353,11 +464,14 @@ tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
 #pragma unroll
                 for (int32_t e = 0; e < 2; ++e) {
                     const int32_t col = cg * 32 + 8 * tig + 4 * e;
-                    if (col < D)
-                        *reinterpret_cast<float4*>(dst + (whole ? col : (size_t)col * C::kRows)) =
-                            make_float4(acc[cg][0][2 * h + e] * inv, acc[cg][1][2 * h + e] * inv,
-                                        acc[cg][2][2 * h + e] * inv, acc[cg][3][2 * h + e] * inv);
+                    if (col < D) {
+                        const float4 o = make_float4(acc[cg][0][2 * h + e] * inv, acc[cg][1][2 * h + e] * inv,
+                                                     acc[cg][2][2 * h + e] * inv, acc[cg][3][2 * h + e] * inv);
+                        *reinterpret_cast<float4*>(dst + (whole ? col : (size_t)col * C::kRows)) = o;
+                        if (f32_odd(o.x) || f32_odd(o.y) || f32_odd(o.z) || f32_odd(o.w)) *redo = 1;
+                    }
                 }
+            if (f32_odd(l[h])) *redo = 1;
             if (!whole && tig == 0)
                 *reinterpret_cast<float2*>(cell + (size_t)D * C::kRows + 2 * rho) =
                     make_float2(m[h], l[h]);
@@ -365,6 +479,8 @@ tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
         __syncthreads();                   // q and the node masks are free
     }
     if (w.cuts != nullptr && tid == 0) w.cuts[blockIdx.x] = cut;
+    __syncthreads();
+    if (*redo) tree_plain_range<DMAX, WARPS>(a, w, KC, bits, up);
     griddep_launch_dependents();
 }
 

@@ -1,0 +1,164 @@
+"""The drafted step at its edges: values at the type's ends, infinities in the
+caches."""
+import math
+
+import pytest
+import torch
+
+import paged_kv_cache_109_gb300 as pa
+from tests._draft import Batch, assert_tree_close, path_of, tree_reference
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def clear_device_error(cuda_device):
+    pa.last_device_error()
+    yield
+
+
+def _place(b, i, p):
+    """Block and row of position ``p`` of sequence ``i``."""
+    return int(b.tables[i, p // b.bs]), p % b.bs
+
+
+# ---- values at the type's ends, infinities ---------------------------------------------
+
+# kv heads, group, head dim, block size, dtype, cached tokens, nodes
+ENDS = [
+    (1, 4, 128, 16, F32, [37, 200], [8, 40]), (1, 2, 64, 16, F32, [37, 200], [8, 40]),
+    (1, 1, 64, 8, F32, [37, 5], [8, 9]), (1, 2, 128, 16, F32, [37, 60], [8, 9]),
+    (1, 1, 256, 16, F32, [37, 200], [8, 40]), (1, 2, 36, 16, F32, [37, 200], [8, 40]),
+    (2, 1, 64, 16, F32, [5000, 3], [9, 4]), (1, 2, 7, 3, F32, [37, 20], [8, 5]),
+    (1, 4, 128, 16, BF, [37, 200], [8, 40]), (1, 1, 64, 8, BF, [37, 200], [8, 40]),
+    (1, 2, 256, 16, BF, [37, 200], [8, 40]), (1, 2, 72, 16, BF, [37, 200], [8, 40]),
+    (1, 64, 128, 16, BF, [37, 200], [8, 40]),
+]
+
+
+def _largest(dtype):
+    # the largest value, and in fp32 the least one that 11 bits round up to 2^128
+    top = torch.finfo(dtype).max
+    least = torch.tensor(0x7F7FF000, dtype=torch.int32).view(F32).item()
+    return [top, -top] + ([least, -least] if dtype == F32 else [])
+
+
+@pytest.mark.parametrize("hkv,group,d,bs,dtype,ctx,nodes", ENDS)
+@pytest.mark.parametrize("which", range(4))
+def test_a_hidden_nodes_largest_values_leave_no_trace(cuda_device, hkv, group, d, bs, dtype, ctx,
+                                                      nodes, which):
+    bads = _largest(dtype)
+    if which >= len(bads):
+        pytest.skip("two values of this type")
+    for hit in ("v", "k"):
+        b = Batch(ctx, nodes, hkv, group, d, bs, dtype, seed=11)
+        node = [3, nodes[1] // 2]
+        for i in range(2):
+            blk, off = _place(b, i, ctx[i] + node[i])
+            if hit == "v":
+                b.v[blk, :, off, 1::3] = bads[which]
+            else:
+                b.k[blk, :, off] = bads[which]
+        got = b.run(pa, cuda_device).double().cpu()
+        torch.cuda.synchronize()
+        ref, bound = tree_reference(b)
+        for i in range(2):
+            for j in range(nodes[i]):
+                r = int(b.start[i]) + j
+                sees = node[i] in path_of(b.par[i], j)
+                if not sees or (hit == "v" and dtype == F32):
+                    # (fp32: one such value under a weight of at most one is
+                    # finite, and the bound is in terms of sum p |v|)
+                    assert torch.isfinite(got[r]).all(), (hit, r)
+                    assert_tree_close(got[r], ref[r], bound[r], dtype, f"{hit} {r}")
+
+
+FP32 = [x for x in ENDS if x[4] == F32]
+
+
+@pytest.mark.parametrize("hkv,group,d,bs,dtype,ctx,nodes", FP32)
+@pytest.mark.parametrize("bad", ["max", "least", "inf", "-inf", "both"])
+def test_cached_values_at_the_ends_fp32(cuda_device, hkv, group, d, bs, dtype, ctx, nodes, bad):
+    """A cached token's V holds the type's largest value or an infinity: the
+    formula's value, in every row of the sequence."""
+    b = Batch(ctx, nodes, hkv, group, d, bs, dtype, seed=5)
+    top = _largest(F32)
+    for i, p in ((0, ctx[0] // 2), (1, 1)):
+        blk, off = _place(b, i, p)
+        b.v[blk, :, off, 2::5] = {"max": top[0], "least": -top[2], "inf": math.inf,
+                                  "-inf": -math.inf, "both": math.inf}[bad]
+        if bad == "both":
+            blk, off = _place(b, i, p + 1)
+            b.v[blk, :, off, 2::5] = -math.inf
+    got = b.run(pa, cuda_device).double().cpu()
+    assert pa.last_device_error() == 0
+    ref, bound = tree_reference(b)
+    if bad in ("max", "least"):
+        assert torch.isfinite(got).all()
+        assert_tree_close(got, ref, bound, dtype)
+        return
+    assert torch.isfinite(got).logical_not()[..., 2::5].all()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    fine = torch.isfinite(ref)
+    assert torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)])
+    assert_tree_close(got[fine], ref[fine], bound[fine], dtype)
+
+
+@pytest.mark.parametrize("hkv,group,d,bs,dtype,ctx,nodes", FP32)
+@pytest.mark.parametrize("bad", ["max", "least", "inf"])
+def test_cached_keys_at_the_ends_fp32(cuda_device, hkv, group, d, bs, dtype, ctx, nodes, bad):
+    """One element of a cached K holds the largest value or an infinity, q half
+    of one against it with either sign: weight one, weight zero, or (an
+    infinite score) NaN."""
+    b = Batch(ctx, nodes, hkv, group, d, bs, dtype, seed=6)
+    top = _largest(F32)
+    x = {"max": top[0], "least": top[2], "inf": math.inf}[bad]
+    g = torch.Generator().manual_seed(1)
+    b.q[..., 1] = torch.where(torch.rand(b.q.shape[:2], generator=g) < 0.5, 0.5, -0.5)
+    at = [(0, ctx[0] // 2), (1, 1)]
+    # rows with q < 0: the formula without that key
+    clean = Batch(ctx, nodes, hkv, group, d, bs, dtype, seed=6)
+    clean.q = b.q
+    for i, p in at:
+        blk, off = _place(clean, i, p)
+        clean.k[blk, :, off] = 0.0
+        clean.k[blk, :, off, 1] = 1e6              # a weight of exp(-0.5e6 scale) = 0
+    drop, _ = tree_reference(clean)
+    for i, p in at:
+        blk, off = _place(b, i, p)
+        b.k[blk, :, off, 1] = x
+    got = b.run(pa, cuda_device).double().cpu()
+    assert pa.last_device_error() == 0
+    # (tree_reference's bound, with products of q and k below 64 and |v| below 6)
+    ds = (d + 4) * 2.0 ** -24 * b.scale * 64 * d
+    for i, (_, p) in enumerate(at):
+        blk, off = _place(b, i, p)
+        for r in range(int(b.start[i]), int(b.start[i + 1])):
+            for h in range(hkv * group):
+                if b.q[r, h, 1] < 0:
+                    share = 2 * ds + 2 * (ctx[i] + nodes[i]) * 2.0 ** -24 + 2.0 ** -19
+                    tol = share * 6 + 2.0 ** -24 * drop[r, h].abs()
+                    assert ((got[r, h] - drop[r, h]).abs() <= tol).all(), (r, h)
+                elif bad == "inf":
+                    assert torch.isnan(got[r, h]).all(), (r, h)
+                else:
+                    want = b.v[blk, h // group, off].double()
+                    assert ((got[r, h] - want).abs() <= 2.0 ** -22 * want.abs()).all(), (r, h)
+
+
+@pytest.mark.parametrize("hkv,group,d,bs,dtype,ctx,nodes", FP32)
+def test_queries_at_the_ends_fp32(cuda_device, hkv, group, d, bs, dtype, ctx, nodes):
+    """A row's q holds the largest value where every key holds zero, another's
+    NaN: the first is the formula's, the second NaN, the others do not change."""
+    b = Batch(ctx, nodes, hkv, group, d, bs, dtype, seed=7)
+    b.k[..., 1] = torch.where(torch.isnan(b.k[..., 1]), b.k[..., 1], torch.zeros(()))
+    b.q[1, :, 1] = torch.finfo(F32).max
+    ref, bound = tree_reference(b)
+    # (q k is zero there: its share of the bound too)
+    b.q[2, :, 3] = math.nan
+    got = b.run(pa, cuda_device).double().cpu()
+    assert torch.isnan(got[2]).all()
+    keep = [r for r in range(b.total) if r != 2]
+    assert_tree_close(got[keep], ref[keep], bound[keep], dtype)
