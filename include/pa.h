@@ -574,7 +574,9 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
  * new_lens         device or pinned int32 [num_seqs]; must not be seq_lens.
  * The blocks written must be the sequence's own (a shared one is copied first).
  * A sequence with rows or a length out of range (as in pa_decode_tree) is
- * reported (PA_DEVERR_SEQ_LEN): nothing moves, new_lens[i] = seq_lens[i].  A
+ * reported (PA_DEVERR_SEQ_LEN): nothing moves, new_lens[i] = seq_lens[i], and
+ * accepted_rows is -1 in those of its rows that are below total_q (nothing is
+ * written there while query_start_loc descends anywhere).  A
  * leaf outside [-1, n_i) or a bad parent on the path is reported
  * (PA_DEVERR_TREE) and read as leaf -1.  A row behind a bad table entry is
  * skipped and reported (PA_DEVERR_TABLE_ENTRY).

@@ -716,8 +716,8 @@ def accept_tree(leaf, parents, query_start_loc, seq_lens, k_caches, v_caches, bl
     and ``v_caches`` are one cache each, a [layers, num_blocks, Hkv, B, D]
     tensor, or a sequence of caches.  Returns (new_lens [N], accepted_rows
     [total_q]): the lengths with the path, and per sequence the packed rows
-    of its path from its first row on, then -1 (rows behind the last sequence
-    are left as they were)."""
+    of its path from its first row on, then -1 (a refused sequence's are all
+    -1; rows behind the last sequence are left as they were)."""
     shape, dtype, device, keys = _layer_caches(k_caches)
     v_shape, v_dtype, v_device, values = _layer_caches(v_caches)
     if device != torch.cuda.current_device():

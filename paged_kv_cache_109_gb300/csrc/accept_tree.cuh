@@ -58,16 +58,27 @@ accept_tree_kernel(const AcceptArgs a, const __grid_constant__ AcceptCaches<LAYE
     griddep_launch_dependents();
     const int32_t tid = threadIdx.x, i = blockIdx.x;
     const bool first = blockIdx.y == 0;
-    const int32_t q0 = a.query_start[i], n = a.query_start[i + 1] - q0;
+    const int32_t q0 = a.query_start[i], q1 = a.query_start[i + 1];
     const int32_t T = a.seq_lens[i], B = a.block_size;
-    if (n < 0 || n > a.max_q_len || n > PA_MAX_TREE_NODES || q0 < 0 || q0 > a.total_q - n ||
-        T < n || T > (int64_t)a.max_blocks * B) {
-        if (first && tid == 0) {
-            raise_error(PA_DEVERR_SEQ_LEN);
-            if (a.new_lens != nullptr) a.new_lens[i] = T;
+    if (q1 < q0 || (int64_t)q1 - q0 > min(a.max_q_len, PA_MAX_TREE_NODES) || q0 < 0 ||
+        q1 > a.total_q || T < q1 - q0 || T > (int64_t)a.max_blocks * B) {
+        if (first && a.new_lens != nullptr) {
+            if (tid == 0) {
+                raise_error(PA_DEVERR_SEQ_LEN);
+                a.new_lens[i] = T;
+            }
+            // those of its rows that there are, unless starts in no order may have
+            // given them to another sequence too
+            bool ordered = a.accepted_rows != nullptr;
+            for (int32_t j = tid; j < (int32_t)gridDim.x; j += kAcceptThreads)
+                ordered = ordered && a.query_start[j] <= a.query_start[j + 1];
+            if (__syncthreads_and(ordered))
+                for (int64_t r = (int64_t)max(q0, 0) + tid; r < min(q1, a.total_q); r += kAcceptThreads)
+                    a.accepted_rows[r] = -1;
         }
         return;
     }
+    const int32_t n = q1 - q0;
     const int32_t C = T - n;
     for (int32_t j = tid; j < n; j += kAcceptThreads) s_parent[j] = a.parents[q0 + j];
     __syncthreads();

@@ -1,5 +1,5 @@
 """The drafted step at its edges: values at the type's ends, infinities in the
-caches."""
+caches, sequences that are refused."""
 import math
 
 import pytest
@@ -162,3 +162,47 @@ def test_queries_at_the_ends_fp32(cuda_device, hkv, group, d, bs, dtype, ctx, no
     assert torch.isnan(got[2]).all()
     keep = [r for r in range(b.total) if r != 2]
     assert_tree_close(got[keep], ref[keep], bound[keep], dtype)
+
+
+# ---- refused sequences -------------------------------------------------------------------
+
+def test_accept_gives_a_refused_sequences_rows_as_none(cuda_device):
+    b = Batch([10, 3, 8], [5, 6, 4], 2, 1, 64, 8, BF, seed=2, kind="chain")
+    _, start, parents, k, v, tables, lens = b.to(cuda_device)
+    k0, v0 = k.clone(), v.clone()
+
+    def run(start=start, lens=lens, max_q=6):
+        rows = torch.full((b.total,), 12345, dtype=torch.int32, device=cuda_device)
+        got = pa.accept_tree(torch.zeros(3, dtype=torch.int32, device=cuda_device), parents, start,
+                             lens, k, v, tables, max_q, accepted_rows=rows)
+        torch.cuda.synchronize()
+        assert torch.equal(k.view(torch.uint8), k0.view(torch.uint8))
+        assert torch.equal(v.view(torch.uint8), v0.view(torch.uint8))
+        return got[0].tolist(), rows.tolist(), pa.last_device_error()
+
+    kept = [0, -1, -1, -1, -1], [11, -1, -1, -1]
+    for short in (4, -1, 10 ** 6):                               # lengths out of range
+        bad = lens.clone()
+        bad[1] = short
+        new, rows, err = run(lens=bad)
+        assert (new, err) == ([11, short, 9], pa.DEVERR_SEQ_LEN)
+        assert rows == kept[0] + [-1] * 6 + kept[1]
+    new, rows, err = run(max_q=5)                               # six nodes, bound five
+    assert (new, err) == ([11, 9, 9], pa.DEVERR_SEQ_LEN)
+    assert rows == kept[0] + [-1] * 6 + kept[1]
+    late = start.clone()
+    late[3] = b.total + 1000                                    # rows past total_q
+    new, rows, err = run(start=late)
+    assert (new, err) == ([11, 4, 12], pa.DEVERR_SEQ_LEN)
+    assert rows == kept[0] + [5] + [-1] * 5 + [-1] * 4
+    early = start.clone()
+    early[0] = -2147483648                                      # rows before the first
+    new, rows, err = run(start=early)
+    assert (new, err) == ([15, 4, 9], pa.DEVERR_SEQ_LEN)
+    assert rows == [-1] * 5 + [5] + [-1] * 5 + kept[1]
+    back = start.clone()
+    back[1], back[2] = 20, 11                                   # 0..20 and 20..11 refused
+    for _ in range(20):
+        new, rows, err = run(start=back)
+        assert (new, err) == ([15, 9, 9], pa.DEVERR_SEQ_LEN)
+        assert rows == [12345] * 11 + kept[1]                   # the third's own stay
