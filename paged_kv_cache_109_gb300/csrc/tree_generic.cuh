@@ -10,30 +10,21 @@
 // group, lanes split the head dimension, keys come one at a time with an
 // online softmax.  Keys that the row does not see are not read.  Bound by the
 // latency of a key's load and reduction, one after another: 8 sequences x 8 kv
-// heads x 2000 tokens, 8 nodes, group 4, D = 42 take 1.48 ms in bf16, 1.65 in fp32.
+// heads x 2000 tokens, 8 nodes, group 4, D = 42 take 1.48 ms in bf16, 1.67 in fp32.
 #pragma once
 
 #include "tree_args.cuh"
 
 namespace pa {
 
+// This CTA's row, which is sequence i's.
 template <typename E>
-__global__ void __launch_bounds__(128) tree_generic_kernel(const TreeArgs a) {
+__device__ __forceinline__ void tree_generic_row(const TreeArgs& a, int32_t i, const TreeSeq s) {
     __shared__ uint32_t s_vis[PA_MAX_TREE_NODES / 32];
-    griddep_wait();
     const int32_t r = blockIdx.x, g = blockIdx.y;
     const int32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t D = a.head_dim, G = a.group, BS = a.block_size;
-    // sequence of row r: the last i with query_start[i] <= r
-    int32_t lo = 0, hi = a.num_seqs - 1;
-    while (lo < hi) {
-        const int32_t mid = (lo + hi + 1) / 2;
-        if (a.query_start[mid] <= r) lo = mid; else hi = mid - 1;
-    }
-    const int32_t i = lo;
-    const TreeSeq s = tree_seq(a, i, g == 0 && threadIdx.x == 0);
     const int32_t j = r - s.q0;
-    if (j < 0 || j >= s.n) return;                // behind the last sequence, or refused
     if (threadIdx.x < PA_MAX_TREE_NODES / 32) s_vis[threadIdx.x] = 0;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -94,6 +85,38 @@ __global__ void __launch_bounds__(128) tree_generic_kernel(const TreeArgs a) {
             if (d < D) out[row_q + d] = Elem<E>::from_float(acc[c] * inv);
         }
     }
+}
+
+template <typename E>
+__global__ void __launch_bounds__(128) tree_generic_kernel(const TreeArgs a) {
+    griddep_wait();
+    const int32_t r = blockIdx.x;
+    // the first CTA reports the refused sequences (some have no rows)
+    if (r == 0 && blockIdx.y == 0)
+        for (int32_t x = threadIdx.x; x < a.num_seqs; x += 128) tree_seq(a, x, true);
+    // sequence of row r: the last i with query_start[i] <= r
+    int32_t lo = 0, hi = a.num_seqs - 1;
+    while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) / 2;
+        if (a.query_start[mid] <= r) lo = mid; else hi = mid - 1;
+    }
+    const TreeSeq s = tree_seq(a, lo, false);
+    if (r >= s.q0 && r - s.q0 < s.n) {
+        tree_generic_row<E>(a, lo, s);
+        return;
+    }
+    // behind the last sequence, refused, or starts that do not ascend (a copy of the
+    // row's code: with one for both, fp32 rows took 15% longer)
+    __shared__ int32_t s_seq;
+    if (threadIdx.x == 0) s_seq = -1;
+    __syncthreads();
+    for (int32_t x = threadIdx.x; x < a.num_seqs; x += 128) {
+        const TreeSeq t = tree_seq(a, x, false);
+        if (r >= t.q0 && r - t.q0 < t.n) atomicMax(&s_seq, x);
+    }
+    __syncthreads();
+    const int32_t i = s_seq;
+    if (i >= 0) tree_generic_row<E>(a, i, tree_seq(a, i, false));
 }
 
 }  // namespace pa

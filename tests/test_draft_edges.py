@@ -206,3 +206,51 @@ def test_accept_gives_a_refused_sequences_rows_as_none(cuda_device):
         new, rows, err = run(start=back)
         assert (new, err) == ([15, 9, 9], pa.DEVERR_SEQ_LEN)
         assert rows == [12345] * 11 + kept[1]                   # the third's own stay
+
+
+TREES = [(64, 16, BF), (144, 16, BF), (72, 16, BF), (64, 16, F32), (7, 3, F32), (20, 5, BF)]
+
+
+@pytest.mark.parametrize("d,bs,dtype", TREES)
+def test_refused_sequences_without_rows_are_reported(cuda_device, d, bs, dtype):
+    b = Batch([30, 10, 20], [4, 0, 3], 1, 2, d, bs, dtype, seed=6)
+    q, start, parents, k, v, tables, lens = b.to(cuda_device)
+    ref, bound = tree_reference(b)
+
+    def run(lens):
+        out = pa.decode_tree(q, start, parents, k, v, tables, lens, b.max_q, b.max_len, b.scale)
+        torch.cuda.synchronize()
+        assert_tree_close(out, ref, bound, dtype)
+        return pa.last_device_error()
+
+    assert run(lens) == 0
+    for bad in (-1, b.max_len + 1):
+        wrong = lens.clone()
+        wrong[1] = bad
+        assert run(wrong) == pa.DEVERR_SEQ_LEN
+
+
+@pytest.mark.parametrize("d,bs,dtype", TREES)
+@pytest.mark.parametrize("head", [[4], [0, 9], [-3], [0, 0, 2, 9, 7]])
+def test_rows_of_a_sequence_behind_refused_ones(cuda_device, d, bs, dtype, head):
+    """Starts that do not ascend: the sequences that they break are refused, and
+    one whose own rows are in range has its value."""
+    b = Batch([30], [3], 1, 2, d, bs, dtype, seed=6)
+    q, _, parents, k, v, tables, lens = b.to(cuda_device)
+    ref, bound = tree_reference(b)
+    n = len(head) + 1
+    rows = torch.full((8, 2, d), 1.0, dtype=dtype, device=cuda_device)
+    rows[2:5] = q
+    par = torch.full((8,), -1, dtype=torch.int32, device=cuda_device)
+    par[2:5] = parents
+    start = torch.tensor(head + [2, 5], dtype=torch.int32, device=cuda_device)
+    out = torch.full_like(rows, 7.0)
+    every = lens.repeat(n)
+    every[:-1] = 2                              # (two keys: sequences of two rows and none fit)
+    pa.decode_tree(rows, start, par, k, v, tables.repeat(n, 1).contiguous(), every, 4, 33, b.scale,
+                   out=out)
+    torch.cuda.synchronize()
+    assert pa.last_device_error() == pa.DEVERR_SEQ_LEN
+    got = out.double().cpu()
+    assert_tree_close(got[2:5], ref, bound, dtype)
+    assert (got[5:] == 7.0).all()
