@@ -532,8 +532,9 @@ pa_status pa_plan_step(const int32_t* seq_lens, const int32_t* new_tokens,
  * max_q_len        host upper bound of n_i, at most PA_MAX_TREE_NODES; 0: no rows.
  * max_seq_len      host upper bound of T_i.
  * workspace        device, >= pa_decode_tree_workspace_bytes(...) bytes, 256-byte
- *                  aligned; may be NULL when that size is 0.  Two calls that may
- *                  run at the same time need two workspaces.
+ *                  aligned; may be NULL when that size is 0.  The size does not
+ *                  grow as num_seqs, max_q_len or max_seq_len get smaller.  Two
+ *                  calls that may run at the same time need two workspaces.
  * A sequence with n_i < 0 or above max_q_len, n_i > T_i, rows outside total_q
  * or T_i out of range is reported (PA_DEVERR_SEQ_LEN) and its rows are left
  * untouched.  A parent outside [-1, own node) is reported (PA_DEVERR_TREE)

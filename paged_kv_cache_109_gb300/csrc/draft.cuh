@@ -473,12 +473,19 @@ size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t total_q, int32_t
     if (pa_decode_path(num_q_heads, cache) < 0 || num_seqs <= 0 || total_q <= 0 ||
         max_q_len <= 0 || max_seq_len <= 0)
         return 0;
-    // the largest of the kernels that the call's pointers may select
+    // the largest of the kernels that the call's pointers may select, for any number
+    // of nodes up to max_q_len: CTAs of fewer row warps are more, so the size does
+    // not grow with the nodes by itself
     const int32_t group = num_q_heads / cache->num_kv_heads;
     size_t most = 0;
     auto take = [&](TreeKernel k) {
-        const TreeLaunch t = tree_launch(k, cache, group, num_seqs, max_q_len, max_seq_len);
-        most = std::max(most, tree_workspace(t.s, t.ctas, cache->head_dim));
+        for (int32_t rows = k == kTreeWs ? 64 : 16; rows <= 64; rows *= 2) {
+            // the most nodes that this many rows cover (64 take any number, in turn)
+            const int32_t nodes = rows < 64 ? rows / group : max_q_len;
+            if (nodes < 1 || nodes > max_q_len) continue;
+            const TreeLaunch t = tree_launch(k, cache, group, num_seqs, nodes, max_seq_len);
+            most = std::max(most, tree_workspace(t.s, t.ctas, cache->head_dim));
+        }
     };
     if (tree_ws_shape(cache)) take(kTreeWs);
     if (tree_mma_shape(cache))

@@ -1,5 +1,5 @@
 """The drafted step at its edges: values at the type's ends, infinities in the
-caches, sequences that are refused."""
+caches, sequences that are refused, workspaces kept for calls of other sizes."""
 import math
 
 import pytest
@@ -254,3 +254,34 @@ def test_rows_of_a_sequence_behind_refused_ones(cuda_device, d, bs, dtype, head)
     got = out.double().cpu()
     assert_tree_close(got[2:5], ref, bound, dtype)
     assert (got[5:] == 7.0).all()
+
+
+# ---- workspaces and plans kept for calls of other sizes ----------------------------------
+
+@pytest.mark.parametrize("hkv,group,d,bs,dtype", [
+    (8, 4, 128, 16, F32), (8, 1, 256, 16, F32), (8, 4, 128, 4, BF), (8, 2, 256, 16, BF),
+    (8, 4, 72, 16, BF), (8, 3, 200, 8, BF), (8, 4, 128, 16, BF), (8, 5, 96, 24, BF),
+    (2, 40, 64, 16, BF), (3, 7, 64, 16, F32),
+])
+def test_a_workspace_serves_every_smaller_call(cuda_device, hkv, group, d, bs, dtype):
+    desc = pa.CacheDesc(4096, bs, hkv, d, pa.PA_BF16 if dtype == BF else pa.PA_F32)
+    hq = hkv * group
+
+    def size(n, nodes, keys):
+        return pa.decode_tree_workspace_bytes(n, n * nodes, hq, nodes, keys, desc)
+
+    steps = [1, 2, 3, 4, 5, 8, 9, 16, 17, 33, 64, 65, 129, 256]
+    for keys in (300, 4000, 131072):
+        for n in (1, 7, 64):
+            sizes = [size(n, x, keys) for x in steps]
+            assert sizes == sorted(sizes), (n, keys)
+            assert size(n, 8, keys) <= size(n + 9, 8, keys + 5000)
+    # a batch that fills the GPU, its workspace made for 64 nodes
+    b = Batch([700] * 24, [3] * 24, hkv, group, d, bs, dtype, seed=3)
+    ref, bound = tree_reference(b)
+    ws = torch.empty(max(1, size(24, 64, 4000)), dtype=torch.uint8, device=cuda_device)
+    args = b.to(cuda_device)
+    args[5] = torch.cat([args[5], torch.full((24, -(-4000 // bs)), -1, dtype=torch.int32,
+                                             device=cuda_device)], 1).contiguous()
+    got = pa.decode_tree(*args, 3, 4000, b.scale, workspace=ws)
+    assert_tree_close(got, ref, bound, dtype)
