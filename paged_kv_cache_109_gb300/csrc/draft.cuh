@@ -225,16 +225,31 @@ TreeShape tree_tiled_tiling(int32_t head_dim, int32_t group, int32_t max_q_len) 
     return s;
 }
 
-// CTAs of `kern` one SM holds, per instance (0-14) and head dim (which sets its
-// shared memory).
+// An instance of the mma.sync, the tf32 or the CUDA-core kernel: its number, and its
+// shared memory at the call's head dim and at its largest.  An instance's limit is
+// set to the largest only, so that host threads with calls of two head dims do not
+// set it under one another.
+constexpr int kTreeInstances = 15;
+struct TreeInstance {
+    int number, threads;
+    size_t smem, most;
+};
+
 template <typename Kern>
-int32_t tree_per_sm(int instance, Kern kern, int threads, size_t smem, int32_t head_dim) {
-    static std::atomic<int> table[15][257];
-    std::atomic<int>* cached = table[instance];
+bool tree_allow_smem(Kern kern, const TreeInstance& t) {
+    static std::atomic<uint64_t> allowed[kTreeInstances];    // (one type for all instances)
+    return allow_smem(allowed[t.number], kern, t.most);
+}
+
+// CTAs of an instance that one SM holds, per head dim.
+template <typename Kern>
+int32_t tree_per_sm(Kern kern, const TreeInstance& t, int32_t head_dim) {
+    static std::atomic<int> table[kTreeInstances][257];
+    std::atomic<int>* cached = table[t.number];
     int n = cached[head_dim].load(std::memory_order_relaxed);
     if (n > 0) return n;
-    if (set_smem(kern, smem) && cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                                    &n, kern, threads, smem) == cudaSuccess && n > 0) {
+    if (tree_allow_smem(kern, t) && cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                                    &n, kern, t.threads, t.smem) == cudaSuccess && n > 0) {
         cached[head_dim].store(n, std::memory_order_relaxed);
         return n;
     }
@@ -242,12 +257,13 @@ int32_t tree_per_sm(int instance, Kern kern, int threads, size_t smem, int32_t h
     return 1;
 }
 
-// Calls f(kernel, threads, shared bytes) with the instance of a head dim and
-// warps: of the mma.sync, the tf32 and the CUDA-core kernel.
+// Calls f(kernel, instance) with the instance of a head dim and warps: of the
+// mma.sync, the tf32 and the CUDA-core kernel.
 template <int DMAX, int KC, int WARPS, typename F>
 auto call_tree_mma(int32_t head_dim, F f) {
     using C = TreeMmaCfg<DMAX, KC, WARPS>;
-    return f(tree_mma_kernel<DMAX, KC, WARPS>, C::kThreads, C::smem_bytes(head_dim));
+    return f(tree_mma_kernel<DMAX, KC, WARPS>,
+             TreeInstance{DMAX > 128 ? 0 : WARPS, C::kThreads, C::smem_bytes(head_dim), C::smem_bytes(DMAX)});
 }
 template <typename F>
 auto with_tree_mma(int32_t head_dim, int32_t warps, F f) {
@@ -259,7 +275,8 @@ auto with_tree_mma(int32_t head_dim, int32_t warps, F f) {
 template <int DMAX, int KC, int WARPS, typename F>
 auto call_tree_tf(int32_t head_dim, F f) {
     using C = TreeTfCfg<DMAX, KC, WARPS>;
-    return f(tree_tf32_kernel<DMAX, KC, WARPS>, C::kThreads, C::smem_bytes(head_dim));
+    return f(tree_tf32_kernel<DMAX, KC, WARPS>,
+             TreeInstance{5 + (DMAX > 128 ? 0 : WARPS), C::kThreads, C::smem_bytes(head_dim), C::smem_bytes(DMAX)});
 }
 template <typename F>
 auto with_tree_tf(int32_t head_dim, int32_t warps, F f) {
@@ -268,22 +285,20 @@ auto with_tree_tf(int32_t head_dim, int32_t warps, F f) {
            : warps == 2 ? call_tree_tf<128, 16, 2>(head_dim, f)
                         : call_tree_tf<128, 32, 4>(head_dim, f);
 }
+template <int RPT, int NF, int KC, typename F>
+auto call_tree_tiled(int32_t head_dim, F f) {
+    using C = TreeTiledCfg<RPT, NF, KC>;
+    return f(tree_tiled_kernel<__nv_bfloat16, RPT, NF, KC>,
+             TreeInstance{10 + (NF == 8 ? RPT - 1 : RPT == 4 ? 4 : RPT + 1), kTreeTiledThreads,
+                          C::smem_bytes(head_dim, 2), C::smem_bytes(32 * NF, 2)});
+}
 template <typename F>
 auto with_tree_tiled(int32_t head_dim, int32_t rpt, F f) {
-    using E = __nv_bfloat16;
     if (head_dim > 128)
-        return rpt == 1 ? f(tree_tiled_kernel<E, 1, 8, 16>, kTreeTiledThreads,
-                            TreeTiledCfg<1, 8, 16>::smem_bytes(head_dim, 2))
-                        : f(tree_tiled_kernel<E, 2, 8, 16>, kTreeTiledThreads,
-                            TreeTiledCfg<2, 8, 16>::smem_bytes(head_dim, 2));
-    if (rpt == 1)
-        return f(tree_tiled_kernel<E, 1, 4, 32>, kTreeTiledThreads,
-                 TreeTiledCfg<1, 4, 32>::smem_bytes(head_dim, 2));
-    if (rpt == 2)
-        return f(tree_tiled_kernel<E, 2, 4, 32>, kTreeTiledThreads,
-                 TreeTiledCfg<2, 4, 32>::smem_bytes(head_dim, 2));
-    return f(tree_tiled_kernel<E, 4, 4, 32>, kTreeTiledThreads,
-             TreeTiledCfg<4, 4, 32>::smem_bytes(head_dim, 2));
+        return rpt == 1 ? call_tree_tiled<1, 8, 16>(head_dim, f) : call_tree_tiled<2, 8, 16>(head_dim, f);
+    return rpt == 1   ? call_tree_tiled<1, 4, 32>(head_dim, f)
+           : rpt == 2 ? call_tree_tiled<2, 4, 32>(head_dim, f)
+                      : call_tree_tiled<4, 4, 32>(head_dim, f);
 }
 
 // A kernel's tiling and CTAs for a call.
@@ -296,24 +311,19 @@ TreeLaunch tree_launch(TreeKernel k, const pa_cache_desc* c, int32_t group, int3
                        int32_t max_q_len, int32_t max_seq_len) {
     TreeLaunch t{};
     t.warps = tree_row_warps(c->head_dim, group, max_q_len);
-    int32_t per_sm = 1, instance = 0;
-    auto resident = [&](auto kern, int threads, size_t smem) {
-        return tree_per_sm(instance, kern, threads, smem, c->head_dim);
-    };
+    int32_t per_sm = 1;
+    auto resident = [&](auto kern, const TreeInstance& x) { return tree_per_sm(kern, x, c->head_dim); };
     if (k == kTreeWs) {
         t.s = tree_ws_tiling(group);
     } else if (k == kTreeMma) {
         t.s = tree_mma_tiling(c->head_dim, group, t.warps);
-        instance = t.warps;
         per_sm = with_tree_mma(c->head_dim, t.warps, resident);
     } else if (k == kTreeTf) {
         t.s = tree_tf_tiling(c->head_dim, group, t.warps);
-        instance = 5 + t.warps;
         per_sm = with_tree_tf(c->head_dim, t.warps, resident);
     } else {
         t.s = tree_tiled_tiling(c->head_dim, group, max_q_len);
         const int32_t rpt = tree_tiled_rpt(c->head_dim, group, max_q_len);
-        instance = 10 + rpt;
         per_sm = with_tree_tiled(c->head_dim, rpt, resident);
     }
     // Short sequences go whole: no range ends inside a unit, so no merge follows.  A
@@ -588,9 +598,9 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
             w.cuts = reinterpret_cast<TreeCut*>(base);
             w.cells = reinterpret_cast<float*>(base + align256((size_t)t.ctas * sizeof(TreeCut)));
         }
-        auto go = [&](auto kern, int threads, size_t smem) {
-            if (!set_smem(kern, smem)) return cudaErrorUnknown;
-            return launch_pdl(kern, dim3(t.ctas), dim3(threads), smem, st, a, w);
+        auto go = [&](auto kern, const TreeInstance& x) {
+            if (!tree_allow_smem(kern, x)) return cudaErrorUnknown;
+            return launch_pdl(kern, dim3(t.ctas), dim3(x.threads), x.smem, st, a, w);
         };
         cudaError_t err;
         if (mma)

@@ -1,6 +1,9 @@
 """The drafted step at its edges: values at the type's ends, infinities in the
-caches, sequences that are refused, workspaces kept for calls of other sizes."""
+caches, sequences that are refused, workspaces kept for calls of other sizes, calls
+from several host threads."""
+import ctypes
 import math
+import threading
 
 import pytest
 import torch
@@ -285,3 +288,42 @@ def test_a_workspace_serves_every_smaller_call(cuda_device, hkv, group, d, bs, d
                                              device=cuda_device)], 1).contiguous()
     got = pa.decode_tree(*args, 3, 4000, b.scale, workspace=ws)
     assert_tree_close(got, ref, bound, dtype)
+
+
+# ---- two host threads -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,dims,bs", [(F32, (128, 96), 16), (BF, (256, 192), 16),
+                                           (BF, (232, 200), 16), (BF, (128, 112), 4)])
+def test_host_threads_with_two_head_dims(cuda_device, dtype, dims, bs):
+    """Calls at once that share a kernel and need different shared memory."""
+    bs_ = [Batch([60] * 2, [16] * 2, 1, 4, d, bs, dtype, seed=d) for d in dims]
+    lib, refs = pa.load_library(), [tree_reference(b) for b in bs_]
+    work = []
+    for x in range(4):
+        b = bs_[x % 2]
+        q, start, parents, k, v, tables, lens = b.to(cuda_device)
+        out, stream = torch.zeros_like(q), torch.cuda.Stream()
+        desc = pa.CacheDesc(k.shape[0], bs, 1, k.shape[3], pa.PA_F32 if dtype == F32 else pa.PA_BF16)
+        p = [ctypes.c_void_p(t.data_ptr()) for t in (q, start, parents, k, v, tables, lens, out)]
+        args = (p[0], p[1], p[2], b.total, b.max_q, p[3], p[4], p[5], tables.shape[1], p[6], 2,
+                b.max_len, 4, b.scale, p[7], None, 0, ctypes.byref(desc),
+                ctypes.c_void_p(stream.cuda_stream))
+        work.append((args, out, stream, desc, (q, start, parents, k, v, tables, lens)))
+    torch.cuda.synchronize()
+    go, failed = threading.Barrier(len(work)), []
+
+    def run(args):
+        torch.cuda.set_device(cuda_device)
+        go.wait()
+        failed.append(sum(lib.pa_decode_tree(*args) != pa.PA_OK for _ in range(4000)))
+
+    threads = [threading.Thread(target=run, args=(w[0],)) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0] * len(work)
+    assert pa.last_device_error() == 0
+    for x, w in enumerate(work):
+        assert_tree_close(w[1], *refs[x % 2], dtype)
