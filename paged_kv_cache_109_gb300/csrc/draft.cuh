@@ -147,16 +147,25 @@ int64_t tree_most(const TreeShape& s, int32_t max_q_len, int32_t max_seq_len) {
            s.overhead;
 }
 
+// The current device, asked for once a call's sizing.
+struct TreeDevice {
+    int32_t id, sms;
+};
+TreeDevice tree_device() {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) dev = -1;
+    return {dev, std::max(1, device_sm_count())};
+}
+
 // CTAs of a call: `per_sm` a SM, fewer when the host's bounds say that less
 // work can be there.
 int32_t tree_ctas(const TreeShape& s, int32_t num_seqs, int32_t max_q_len, int32_t max_seq_len,
-                  int32_t num_kv_heads, int32_t per_sm) {
+                  int32_t num_kv_heads, int32_t sms, int32_t per_sm) {
     const int64_t per = (int64_t)s.tokens * s.tiles;
     const int64_t units = (int64_t)num_seqs * num_kv_heads * s.sub_groups * ((max_q_len + per - 1) / per);
     const int64_t cost = tree_most(s, max_q_len, max_seq_len);
     const int64_t ctas = (units * cost + s.min_range - 1) / s.min_range;
-    return (int32_t)std::max<int64_t>(
-        1, std::min<int64_t>(ctas, (int64_t)std::max(1, device_sm_count()) * per_sm));
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)sms * per_sm));
 }
 
 size_t tree_workspace(const TreeShape& s, int32_t ctas, int32_t head_dim) {
@@ -241,16 +250,17 @@ bool tree_allow_smem(Kern kern, const TreeInstance& t) {
     return allow_smem(allowed[t.number], kern, t.most);
 }
 
-// CTAs of an instance that one SM holds, per head dim.
+// CTAs of an instance that one SM of the current device holds, per head dim.
 template <typename Kern>
-int32_t tree_per_sm(Kern kern, const TreeInstance& t, int32_t head_dim) {
-    static std::atomic<int> table[kTreeInstances][257];
-    std::atomic<int>* cached = table[t.number];
-    int n = cached[head_dim].load(std::memory_order_relaxed);
+int32_t tree_per_sm(Kern kern, const TreeInstance& t, int32_t device, int32_t head_dim) {
+    static std::atomic<uint8_t> table[kMaxDevices][kTreeInstances][257];
+    if (device < 0) return 1;
+    std::atomic<uint8_t>& cached = table[device][t.number][head_dim];
+    int n = cached.load(std::memory_order_relaxed);
     if (n > 0) return n;
     if (tree_allow_smem(kern, t) && cudaOccupancyMaxActiveBlocksPerMultiprocessor(
                                     &n, kern, t.threads, t.smem) == cudaSuccess && n > 0) {
-        cached[head_dim].store(n, std::memory_order_relaxed);
+        cached.store((uint8_t)n, std::memory_order_relaxed);
         return n;
     }
     cudaGetLastError();
@@ -307,12 +317,12 @@ struct TreeLaunch {
     TreeShape s;
     int32_t ctas, warps;
 };
-TreeLaunch tree_launch(TreeKernel k, const pa_cache_desc* c, int32_t group, int32_t num_seqs,
-                       int32_t max_q_len, int32_t max_seq_len) {
+TreeLaunch tree_launch(TreeKernel k, const TreeDevice& dev, const pa_cache_desc* c, int32_t group,
+                       int32_t num_seqs, int32_t max_q_len, int32_t max_seq_len) {
     TreeLaunch t{};
     t.warps = tree_row_warps(c->head_dim, group, max_q_len);
     int32_t per_sm = 1;
-    auto resident = [&](auto kern, const TreeInstance& x) { return tree_per_sm(kern, x, c->head_dim); };
+    auto resident = [&](auto kern, const TreeInstance& x) { return tree_per_sm(kern, x, dev.id, c->head_dim); };
     if (k == kTreeWs) {
         t.s = tree_ws_tiling(group);
     } else if (k == kTreeMma) {
@@ -337,7 +347,7 @@ TreeLaunch tree_launch(TreeKernel k, const pa_cache_desc* c, int32_t group, int3
         t.s.fixed_cost = (int32_t)tree_most(t.s, max_q_len, max_seq_len);
         t.s.min_range = t.s.fixed_cost;
     }
-    t.ctas = tree_ctas(t.s, num_seqs, max_q_len, max_seq_len, c->num_kv_heads, per_sm);
+    t.ctas = tree_ctas(t.s, num_seqs, max_q_len, max_seq_len, c->num_kv_heads, dev.sms, per_sm);
     return t;
 }
 
@@ -487,13 +497,14 @@ size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t total_q, int32_t
     // of nodes up to max_q_len: CTAs of fewer row warps are more, so the size does
     // not grow with the nodes by itself
     const int32_t group = num_q_heads / cache->num_kv_heads;
+    const TreeDevice dev = tree_device();
     size_t most = 0;
     auto take = [&](TreeKernel k) {
         for (int32_t rows = k == kTreeWs ? 64 : 16; rows <= 64; rows *= 2) {
             // the most nodes that this many rows cover (64 take any number, in turn)
             const int32_t nodes = rows < 64 ? rows / group : max_q_len;
             if (nodes < 1 || nodes > max_q_len) continue;
-            const TreeLaunch t = tree_launch(k, cache, group, num_seqs, nodes, max_seq_len);
+            const TreeLaunch t = tree_launch(k, dev, cache, group, num_seqs, nodes, max_seq_len);
             most = std::max(most, tree_workspace(t.s, t.ctas, cache->head_dim));
         }
     };
@@ -585,7 +596,7 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
                        caches16 && aligned(out, 16);
     if (ws || mma || tf || tiled) {
         const TreeKernel kernel = ws ? kTreeWs : mma ? kTreeMma : tf ? kTreeTf : kTreeTiled;
-        const TreeLaunch t = tree_launch(kernel, cache, a.group, num_seqs, max_q_len, max_seq_len);
+        const TreeLaunch t = tree_launch(kernel, tree_device(), cache, a.group, num_seqs, max_q_len, max_seq_len);
         // unit costs are 32-bit in the kernels
         const int64_t per = (int64_t)t.s.tokens * t.s.tiles;
         if ((int64_t)a.num_kv_heads * t.s.sub_groups * ((max_q_len + per - 1) / per) *
