@@ -101,7 +101,7 @@ typedef struct {
 #define PA_DEVERR_BLOCK_PAIR 16u  /* a copy pair named a block outside its cache       */
 #define PA_DEVERR_GROUP      32u  /* a shared-prefix group, member or length out of range */
 #define PA_DEVERR_POOL       64u  /* a step plan needed more free blocks than there are    */
-#define PA_DEVERR_SHARED    128u  /* a step plan would append into a shared tail block     */
+#define PA_DEVERR_SHARED    128u  /* a step plan would write into a shared block           */
 #define PA_DEVERR_TREE      256u  /* a draft-tree parent or leaf out of range              */
 
 /*
@@ -478,8 +478,9 @@ pa_status pa_check_wait_timeout(int32_t expected, int32_t arrivals, int64_t limi
  * All or nothing: when the step cannot be planned, every output is that of a
  * step with n_i = 0 for all i (the tables, lengths, blocks held and the front
  * stay, all tokens are -1) and a bit is raised: PA_DEVERR_POOL (F + sum of g >
- * num_free, or F < 0), PA_DEVERR_SHARED (with ref_cnt: n_i > 0 and the partly
- * filled tail block's count is above one: copy it first), PA_DEVERR_SEQ_LEN
+ * num_free, or F < 0), PA_DEVERR_SHARED (with ref_cnt: a held block that new
+ * tokens go into, the tail or one behind it, has a count above one: copy it
+ * first), PA_DEVERR_SEQ_LEN
  * (C_i or n_i negative, C_i + n_i past the table or INT32_MAX, h_i outside
  * [ceil(C_i / B), max_blocks_per_seq], or the sum of n above max_tokens).  A
  * table entry or free block outside [0, num_blocks) gives its tokens slot -1

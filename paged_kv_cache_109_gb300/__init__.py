@@ -565,7 +565,7 @@ def plan_step(seq_lens, new_tokens, block_tables, blocks_held, free_blocks, free
     blocks_held and free_head may be the input tensors.  A step that does not
     fit plans nothing and raises a bit of ``last_device_error``
     (DEVERR_POOL, DEVERR_SHARED, DEVERR_SEQ_LEN).  ``ref_cnt`` (int32
-    [num_blocks]) adds the shared-tail check and the counts of taken blocks."""
+    [num_blocks]) adds the check for shared blocks and the counts of taken ones."""
     device = _current(block_tables)
     n = seq_lens.numel()
     if block_tables.dim() != 2 or block_tables.shape[0] != n or new_tokens.numel() != n \

@@ -67,9 +67,13 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, int32_t i, unsign
         return s;
     }
     s.grow = (int32_t)max((int64_t)0, (total + B - 1) / B - s.held);
-    if (a.ref_cnt != nullptr && s.add > 0 && s.len % B != 0) {
-        const int32_t id = a.block_tables[(int64_t)i * a.max_blocks + s.len / B];
-        if (id >= 0 && id < a.num_blocks && a.ref_cnt[id] > 1) bad |= PA_DEVERR_SHARED;
+    if (a.ref_cnt != nullptr && s.add > 0) {
+        // the held blocks that the new tokens go into
+        const int32_t end = min(s.held, (int32_t)((total + B - 1) / B));
+        for (int32_t b = s.len / B; b < end; ++b) {
+            const int32_t id = a.block_tables[(int64_t)i * a.max_blocks + b];
+            if (id >= 0 && id < a.num_blocks && a.ref_cnt[id] > 1) bad |= PA_DEVERR_SHARED;
+        }
     }
     return s;
 }

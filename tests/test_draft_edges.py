@@ -9,7 +9,8 @@ import pytest
 import torch
 
 import paged_kv_cache_109_gb300 as pa
-from tests._draft import Batch, assert_tree_close, path_of, tree_reference
+from tests._draft import (Batch, PlanState, assert_tree_close, path_of, plan_reference,
+                          tree_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -327,3 +328,39 @@ def test_host_threads_with_two_head_dims(cuda_device, dtype, dims, bs):
     assert pa.last_device_error() == 0
     for x, w in enumerate(work):
         assert_tree_close(w[1], *refs[x % 2], dtype)
+
+
+# ---- a plan's shared blocks ---------------------------------------------------------------
+
+@pytest.mark.parametrize("n", [3, 1500])
+@pytest.mark.parametrize("lens0,new0,extra,shared,bit", [
+    (8, 1, 1, 2, "shared"),       # a full tail, the block behind it shared
+    (6, 3, 1, 2, "shared"),       # the tail the sequence's own, the next block not
+    (6, 7, 2, 3, "shared"),       # the last of the blocks that tokens go into
+    (6, 6, 2, 3, 0),              # tokens end before it
+    (6, 0, 2, 2, 0),              # no tokens
+    (8, 3, 1, 1, 0),              # a full tail: nothing goes into it
+])
+def test_plan_never_writes_into_shared_blocks(cuda_device, n, lens0, new0, extra, shared, bit):
+    """Blocks held behind the cached tokens whose count is above one (a fork's)
+    are refused like a shared tail, where new tokens would go into them."""
+    lens, new = [lens0] + [3] * (n - 1), [new0] + [1] * (n - 1)
+    st = PlanState(lens, [extra] + [0] * (n - 1), 4, 3 * n + 12, 5, seed=n)
+    ref_cnt = torch.tensor(st.pool.ref_cnt, dtype=torch.int32, device=cuda_device)
+    ref_cnt[int(st.tables[0, shared])] = 2
+    before = ref_cnt.clone()
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    tables = st.tables.to(cuda_device)
+    plan = pa.plan_step(dev(lens), dev(new), tables, dev(st.held), dev(st.free), dev([0]),
+                        st.num_blocks, 4, max_tokens=sum(new), ref_cnt=ref_cnt)
+    torch.cuda.synchronize()
+    if bit:
+        assert pa.last_device_error() == pa.DEVERR_SHARED
+        assert torch.equal(tables.cpu(), st.tables) and torch.equal(ref_cnt, before)
+        assert plan.seq_lens.tolist() == lens and plan.blocks_held.tolist() == st.held
+        assert plan.free_head.tolist() == [0] and plan.slot_mapping.tolist() == [-1] * sum(new)
+    else:
+        assert pa.last_device_error() == 0
+        want = plan_reference(st, new, 0, sum(new))
+        assert plan.slot_mapping.tolist() == want["slot_mapping"]
+        assert plan.seq_lens.tolist() == want["seq_lens"] and tables.tolist() == want["tables"]
