@@ -542,7 +542,10 @@ class StepPlan:
 
     @classmethod
     def empty(cls, num_seqs: int, max_tokens: int, device="cuda") -> "StepPlan":
-        """Buffers for up to num_seqs sequences' step of max_tokens tokens."""
+        """Buffers for a step of num_seqs sequences, no fewer, and up to
+        max_tokens tokens.  (Views of their first entries make the plan of a
+        smaller batch: [:n] of seq_lens and blocks_held, [:n + 1] of
+        query_start_loc and block_start.)"""
         def i32(n):
             return torch.empty(n, dtype=torch.int32, device=device)
 

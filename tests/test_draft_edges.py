@@ -364,3 +364,26 @@ def test_plan_never_writes_into_shared_blocks(cuda_device, n, lens0, new0, extra
         want = plan_reference(st, new, 0, sum(new))
         assert plan.slot_mapping.tolist() == want["slot_mapping"]
         assert plan.seq_lens.tolist() == want["seq_lens"] and tables.tolist() == want["tables"]
+
+
+@pytest.mark.parametrize("n", [1, 3, 1500])
+def test_a_plan_of_views_serves_a_smaller_batch(cuda_device, n):
+    """A loop's plan for its largest batch, its first entries for a smaller one."""
+    big = pa.StepPlan.empty(n + 5, 4 * n + 9, cuda_device)
+    plan = pa.StepPlan(big.seq_lens[:n], big.blocks_held[:n], big.free_head,
+                       big.query_start_loc[:n + 1], big.block_start[:n + 1], big.slot_mapping,
+                       big.positions, big.seq_ids)
+    st = PlanState([3] * n, [0] * n, 4, 3 * n + 2, 4, seed=n)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    tables = st.tables.to(cuda_device)
+    args = (dev(st.lens), dev([2] * n), tables, dev(st.held), dev(st.free), dev([0]), st.num_blocks,
+            4)
+    with pytest.raises(ValueError):
+        pa.plan_step(*args, big)
+    pa.plan_step(*args, plan)
+    torch.cuda.synchronize()
+    assert pa.last_device_error() == 0
+    ref = plan_reference(st, [2] * n, 0, 4 * n + 9)
+    for k in pa.StepPlan.__slots__:
+        assert getattr(plan, k).tolist() == ref[k], k
+    assert tables.tolist() == ref["tables"]
