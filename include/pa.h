@@ -448,7 +448,10 @@ pa_status pa_check_wait_timeout(int32_t expected, int32_t arrivals, int64_t limi
  * layers and the cache write (pa_write_kv with the plan's slots).  One such
  * step can be captured in a CUDA graph and replayed: lengths, blocks held and
  * the queue's front are device buffers that each call reads and leaves for
- * the next.
+ * the next.  The queue itself only shrinks there: pa_plan_step takes from its
+ * front, and a finished sequence's blocks are put back by the host, between
+ * steps: free_blocks written anew so that the queue ends with the array, free_head
+ * at its first.
  */
 
 /*
@@ -522,16 +525,19 @@ pa_status pa_plan_step(const int32_t* seq_lens, const int32_t* new_tokens,
  * j - 1) is pa_prefill's causal chunk; n_i = 1 is pa_decode's row.  Keys a node
  * does not see leave no trace in its row, whatever their K and V hold.  In fp32,
  * visible values up to the largest, infinities and NaN have the effect that the
- * formula gives them, computed in 32 bits.  In bf16 that holds for the nodes' V;
- * an infinity in a cached token's V makes its column infinite or NaN, as in
- * pa_prefill.
+ * formula gives them in 32 bits, as sum_t w_t v_t / sum_t w_t with the largest w at
+ * one: two values of a column near the largest may add up to an infinity.  In
+ * bf16 that holds for the nodes' V, with a largest w of up to 2^8; an infinity in a
+ * cached token's V makes its column infinite or NaN, as in pa_prefill.
  *
  * q, out           device or pinned [total_q][num_q_heads][head_dim], cache dtype.
  * query_start_loc  device or pinned int32 [num_seqs + 1], non-decreasing.  Rows
  *                  from its last entry up to total_q are left as they were.
  * parents          device or pinned int32 [total_q].
  * max_q_len        host upper bound of n_i, at most PA_MAX_TREE_NODES; 0: no rows.
- * max_seq_len      host upper bound of T_i.
+ * max_seq_len      host upper bound of T_i, at least max_q_len.
+ * (PA_ERR_UNSUPPORTED also where the work of one sequence of these bounds, kv heads
+ * x tiles of rows x blocks of keys weighted by their cost, passes 2^31.)
  * workspace        device, >= pa_decode_tree_workspace_bytes(...) bytes, 256-byte
  *                  aligned; may be NULL when that size is 0.  The size does not
  *                  grow as num_seqs, max_q_len or max_seq_len get smaller.  Two

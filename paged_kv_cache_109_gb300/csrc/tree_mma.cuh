@@ -62,7 +62,7 @@ tree_mma_kernel(const TreeArgs a, const TreeWork w) {
     const int32_t D = a.head_dim, G = a.group, BS = a.block_size;
     const int32_t HT = w.s.heads;
     const int32_t rowb = D * 2, stride = rowb + 16, ppr = rowb / 16;
-    uint8_t* qsm = sm_tm;                                       // [64][stride]
+    uint8_t* qsm = sm_tm;                                       // [rows][stride]
     uint8_t* kvs = sm_tm + C::kRows * stride;               // [2][K, V][KC][stride]
     uint32_t* bits = reinterpret_cast<uint32_t*>(kvs + 4 * KC * stride);   // [tokens][8]
     int32_t* up = reinterpret_cast<int32_t*>(bits + C::kRows * kWords);

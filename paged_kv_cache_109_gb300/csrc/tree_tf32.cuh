@@ -62,7 +62,7 @@ struct TreeTfCfg {
     }
     static __host__ __device__ int32_t v_stride(int32_t D) { return (D + 15) / 16 * 16 + 4; }
     // dynamic shared bytes: q [rows], K [2][KC], V [2][KC] rows | visible nodes
-    // [rows][8] words | parents | odd keys of the chunk
+    // [rows][8] words | parents | odd keys of the chunk | a row to do again
     static size_t smem_bytes(int32_t D) {
         return 4 * ((size_t)(kRows + 2 * KC) * k_stride(D) + 2 * (size_t)KC * v_stride(D) +
                     kRows * (PA_MAX_TREE_NODES / 32) + PA_MAX_TREE_NODES + KC + 1);
@@ -198,7 +198,7 @@ tree_tf32_kernel(const TreeArgs a, const TreeWork w) {
     const int32_t D = a.head_dim, G = a.group, BS = a.block_size;
     const int32_t HT = w.s.heads;
     const int32_t kst = C::k_stride(D), vst = C::v_stride(D), ppr = D / 4;
-    float* qs = sm_tf;                                          // [64][kst]
+    float* qs = sm_tf;                                          // [rows][kst]
     float* ks = qs + C::kRows * kst;                         // [2][KC][kst]
     float* vs = ks + 2 * KC * kst;                              // [2][KC][vst]
     uint32_t* bits = reinterpret_cast<uint32_t*>(vs + 2 * KC * vst);   // [tokens][8]

@@ -14,7 +14,8 @@
 //
 // Bound: the FMAs, 4 D per row and key; K and V are read once per R rows.
 // Measured: D = 72, 38 sequences x 16 kv heads x 4000 tokens, 64 rows 2.46 ms (18
-// TFLOP/s of the 73 that FMAs reach), 16 rows 0.96 ms.
+// TFLOP/s of the 73 that FMAs reach), 16 rows 0.96 ms.  Two rows a thread above 128
+// columns spill (144 bytes stored a thread).
 // RPT is the smallest of 1, 2, 4 (up to 128 columns) that covers a sequence's
 // rows, so a small tree does not pay for idle rows.
 //

@@ -57,6 +57,8 @@
 // Synchronisation is by mbarriers; every wait is bounded, and a timeout raises
 // PA_DEVERR_TIMEOUT and ends the role (the others then time out too) without
 // leaving copies or MMAs in flight past the CTA's end.
+//
+// Registers: 168, the most for 352 threads; 8 to 16 bytes a thread spill.
 #pragma once
 
 #include <type_traits>
