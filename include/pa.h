@@ -101,8 +101,11 @@ typedef struct {
 #define PA_DEVERR_BLOCK_PAIR 16u  /* a copy pair named a block outside its cache       */
 #define PA_DEVERR_GROUP      32u  /* a shared-prefix group, member or length out of range */
 #define PA_DEVERR_POOL       64u  /* a step plan needed more free blocks than there are    */
-#define PA_DEVERR_SHARED    128u  /* a step plan would write into a shared block           */
-#define PA_DEVERR_TREE      256u  /* a draft-tree parent or leaf out of range              */
+#define PA_DEVERR_SHARED    128u  /* a step plan would write into a shared block, or a
+                                     release would take a block's count below none         */
+#define PA_DEVERR_TREE      256u  /* a draft-tree parent, leaf or token out of range       */
+#define PA_DEVERR_LOGITS    512u  /* logits, temperature or noise that give no token       */
+#define PA_DEVERR_FORK     1024u  /* a fork's source is a fork, or its row holds blocks    */
 
 /*
  * pa_write_kv -- cache write through slot_mapping.
@@ -595,6 +598,194 @@ pa_status pa_accept_tree(const int32_t* leaf, const int32_t* parents,
                          const int32_t* block_tables, int32_t max_blocks_per_seq,
                          void* const* k_caches, void* const* v_caches, int32_t num_layers,
                          int32_t* new_lens, int32_t* accepted_rows, const pa_cache_desc* cache,
+                         void* stream);
+
+/* ---- around the attention ---------------------------------------------------
+ *
+ * What a serving loop runs between its layers' products and the attention calls,
+ * and between its steps.  Memory as for the drafted steps above: of the current
+ * device, managed or page-locked.  Outputs may not share memory with inputs or with
+ * one another but where it says so (PA_ERR_INVALID_ARG).
+ */
+
+/* Rotation of pa_rope_write. */
+typedef struct {
+    int32_t rot_dim;      /* leading dimensions that are rotated: even, 0 .. head_dim    */
+    int32_t num_axes;     /* position axes, 1 .. 3 (time, height, width)                 */
+    int32_t sections[3];  /* pairs of each axis, rot_dim / 2 in all (one axis: not read) */
+    int32_t cyclic;       /* 0: the axes' pairs follow one another; else they alternate  */
+    int32_t neighbours;   /* 0: pair j is (j, j + rot_dim / 2); else (2 j, 2 j + 1)      */
+    float scale;          /* factor on cos and sin (1 for plain rotary positions)        */
+    float eps;            /* of the norms, >= 0                                          */
+} pa_rope_desc;
+
+/*
+ * pa_rope_write -- a layer's projected rows on their way to its attention, in one
+ * pass: per-head norms of queries and keys, their rotation by the tokens'
+ * positions, and the cache write of pa_write_kv.  (The cache holds keys as the
+ * attention calls take them; "vLLM PagedAttention: from memory fragmentation to
+ * slot mapping" §6: the backend writes new K/V to physical slots.)
+ *
+ * For a head's row x of head_dim D and its weight w:
+ *   y = x / sqrt(mean(x^2) + eps) * w         (y = x where the weight is NULL)
+ *   angle_j = positions[a(j)][t] * inv_freq[j]           j < rot_dim / 2
+ *   pair j of y: (y1, y2) -> scale * (y1 cos - y2 sin, y1 sin + y2 cos)
+ * in 32 bits, rounded once to the cache's type.  a(j) is 0 for one axis; with
+ * sections (s_0, s_1, ..) in order, the first s_0 pairs have axis 0, the next s_1
+ * axis 1, ..; cyclic: pair j has axis j mod num_axes where j < num_axes * sections
+ * of that axis, else axis 0 (pairs that no rot_dim / 2 holds are refused).
+ * Angles are reduced from 64-bit fractions of a turn, so that far positions lose
+ * nothing.  |inv_freq| < 2^32; other values give NaN.
+ * Queries go to out, keys to k_cache and values (bit-exact) to v_cache at
+ * slot_mapping[t].
+ *
+ * q, k, v        device or pinned, [num_tokens][heads][head_dim], cache dtype;
+ *                consecutive tokens are q_stride, k_stride, v_stride elements apart
+ *                (slices of one projection's rows).
+ * positions      device or pinned int32 [num_axes][num_tokens].  A token whose first
+ *                position is negative is skipped: its row of out stays as it was.
+ *                (pa_plan_step's positions are those of slots; a node of a drafted tree
+ *                is at the cached tokens' count plus its ancestors'.)
+ * inv_freq       device or pinned float [rot_dim / 2], radians a position.
+ * q_weight, k_weight  device or pinned [head_dim], cache dtype, or NULL.
+ * slot_mapping   device or pinned int64 [num_tokens], as pa_write_kv.  A negative slot:
+ *                the token's query is computed, nothing is cached.  A slot past the pool
+ *                is reported (PA_DEVERR_SLOT) and treated so.
+ * out            device or pinned [num_tokens][num_q_heads][head_dim]; may be q itself
+ *                where q_stride is a row (num_q_heads * head_dim).
+ * head_dim up to 256 (else PA_ERR_UNSUPPORTED); any alignment of whole elements.
+ */
+pa_status pa_rope_write(const void* q, const void* k, const void* v, int64_t q_stride,
+                        int64_t k_stride, int64_t v_stride, int32_t num_tokens,
+                        int32_t num_q_heads, const int32_t* positions, const float* inv_freq,
+                        const void* q_weight, const void* k_weight, const pa_rope_desc* rope,
+                        const int64_t* slot_mapping, void* out, void* k_cache, void* v_cache,
+                        const pa_cache_desc* cache, void* stream);
+
+/*
+ * pa_verify_tree -- which drafted tokens hold against the target's probabilities,
+ * and the token that follows, from given random numbers.  Its leaf is what
+ * pa_accept_tree takes.
+ *
+ * Trees as in pa_decode_tree.  Node 0 of a sequence is the token that was sampled
+ * last: it holds, and the walk starts there (other nodes with parent -1 are never
+ * reached).  Row r of logits is the target's at node r, for the token behind it; row
+ * r of draft_logits the draft's, which r's children were drawn from.  With
+ * T = temperature of the sequence, P = softmax(logits / T), q = softmax(draft / T) at
+ * the node reached, its children are tried in ascending order: the child of row r with
+ * token t holds when
+ *   uniforms[r] * q(t) * S < max(P(t) - c q(t), 0)
+ * with c = 0 and S = 1 at first; a child that fails adds S to c, and S becomes
+ * sum_x max(P(x) - c q(x), 0).  The walk goes on at the first child that holds.  Where
+ * none does, leaf is the node and
+ *   next = argmax_x max(P(x) - c q(x), 0) / noise[i][x]       (ties: the lowest x),
+ * or of P(x) / noise where rounding leaves no rest.  With uniforms in [0, 1) and
+ * exponential noise, held tokens and next are distributed as the target's own
+ * samples, whatever the draft.  draft_logits NULL: the children were chosen, not
+ * drawn (q is one at the child's token): t holds when uniforms[r] * S < P(t), 0 for a
+ * token tried before; a token that fails leaves P and takes its share off S.
+ * T <= 0: greedy, all of P on the lowest of the largest logits (no random numbers and
+ * no draft rows are read).  A sequence of one node is plain sampling.
+ *
+ * logits, draft_logits  device or pinned [total_q][vocab_size], dtype PA_F32 or PA_BF16,
+ *                  rows logit_stride and draft_stride elements apart.  -inf is a token
+ *                  that cannot be drawn; only rows on the walk are read.
+ * tokens           device or pinned int32 [total_q]; node 0's is not read.
+ * uniforms         device or pinned float [total_q].
+ * noise            device or pinned float [num_seqs][vocab_size], rows noise_stride apart.
+ * temperature      device or pinned float [num_seqs], or NULL for 1.
+ * leaf, next_tokens  device or pinned int32 [num_seqs]; a sequence without nodes gets -1
+ *                  in both.
+ * Refused sequences get -1 in both: rows out of range as in pa_decode_tree
+ * (PA_DEVERR_SEQ_LEN); a row on the walk with a NaN, +inf or nothing above -inf, a
+ * temperature that is NaN or so near to zero or to infinity that log2(e) / T is not
+ * a finite positive number, noise that leaves no token (PA_DEVERR_LOGITS).  A parent
+ * outside [-1, own node) is reported (PA_DEVERR_TREE) and read as -1; a child whose
+ * token is outside the vocabulary is reported when it is met (PA_DEVERR_TREE) and
+ * passed over.
+ * The result is reproducible for fixed arguments on a fixed device.
+ */
+pa_status pa_verify_tree(const void* logits, const void* draft_logits, int64_t logit_stride,
+                         int64_t draft_stride, int32_t vocab_size, int32_t dtype,
+                         const int32_t* tokens, const int32_t* parents,
+                         const int32_t* query_start_loc, int32_t num_seqs, int32_t total_q,
+                         int32_t max_q_len, const float* uniforms, const float* noise,
+                         int64_t noise_stride, const float* temperature, int32_t* leaf,
+                         int32_t* next_tokens, void* stream);
+
+/*
+ * pa_release_blocks -- blocks that sequences no longer need go back to the free
+ * queue, on the device (BlockPool.release; "vLLM source walkthrough: PagedAttention
+ * and Continuous Batching" §1.6: a block is free when its count drops to zero).
+ *
+ * Sequence i keeps the K_i = ceil(seq_lens[i] / B) blocks of the tokens that stay (0
+ * for a finished request) and drops the entries [K_i, h_i) of its row, h_i =
+ * blocks_held[i].  With ref_cnt each takes one off its block's count, and a block
+ * whose count drops to zero is freed, at its last entry in the order of sequences and
+ * entries; without, each entry's block is.  The m freed blocks go in front of the
+ * queue in that order:
+ *   free_blocks[F - m .. F), F = *free_head,  *free_head_out = F - m,
+ *   blocks_held_out[i] = K_i
+ * (the entries themselves stay as they were).  So pa_plan_step takes them next, and
+ * an array with room for every block of the pool always has room in front.
+ *
+ * All or nothing: where seq_lens[i] < 0, h_i outside [K_i, max_blocks_per_seq]
+ * (PA_DEVERR_SEQ_LEN), m > F or F outside [0, num_free] (PA_DEVERR_POOL), or a count
+ * would drop below zero (PA_DEVERR_SHARED), nothing changes and both outputs are the
+ * inputs.  An entry outside [0, num_blocks) is passed over (PA_DEVERR_TABLE_ENTRY).
+ *
+ * seq_lens, blocks_held  device or pinned int32 [num_seqs], num_seqs <= 65535.
+ * block_tables     device int32 [num_seqs][max_blocks_per_seq].
+ * free_blocks, free_head  as pa_plan_step.
+ * ref_cnt          device int32 [num_blocks] or NULL (no block is in two rows).
+ * outputs          device or pinned; blocks_held_out and free_head_out may be the
+ *                  inputs themselves.
+ */
+pa_status pa_release_blocks(const int32_t* seq_lens, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, const int32_t* blocks_held,
+                            int32_t num_seqs, int32_t* free_blocks, int32_t num_free,
+                            const int32_t* free_head, int32_t* ref_cnt, int32_t num_blocks,
+                            int32_t block_size, int32_t* blocks_held_out, int32_t* free_head_out,
+                            void* stream);
+
+/*
+ * pa_fork_blocks -- sequences that start as copies of others, on the device
+ * (BlockPool.fork; PagedAttention engineering notes, nxmr.cn, §4.1-4.2: branches of
+ * one prompt point at its blocks; a partly filled block is copied before it is
+ * written).
+ *
+ * Row i with p = src[i] >= 0 becomes a fork of sequence p of T = seq_lens[p] tokens:
+ * its first T / B entries are p's (one is added to each block's count); where T % B is
+ * not zero, the next is a fresh block from the queue's front (count 1) whose first
+ * T % B rows of every kv head, K and V, are copied from p's in every layer.  Fresh
+ * blocks are taken in the order of the rows.
+ *   seq_lens_out[i] = T, blocks_held_out[i] = ceil(T / B)   (others: as they were)
+ *   *free_head_out = *free_head + fresh blocks
+ *   block_pairs[i] = (p's block, the fresh one) or (-1, -1)
+ * block_pairs are pairs of pa_copy_blocks once the rows of -1 are left out, for
+ * further caches of the same tables.
+ *
+ * All or nothing: where src[i] is not a row, is itself forked by this call, or row i
+ * holds blocks (PA_DEVERR_FORK), where seq_lens[p] < 0 or blocks_held[p] is outside
+ * [ceil(T / B), max_blocks_per_seq] (PA_DEVERR_SEQ_LEN), or the queue is too short
+ * (PA_DEVERR_POOL), nothing changes: the outputs are the inputs, all pairs -1.  An entry
+ * outside [0, num_blocks) is reported (PA_DEVERR_TABLE_ENTRY): a shared one is
+ * taken over without a count, a tail's is not copied, a fresh one becomes -1.
+ *
+ * src              device or pinned int32 [num_seqs]; negative: the row stays.
+ * k_caches, v_caches  host arrays of num_layers (1 .. 1024) device caches, as
+ *                  pa_accept_tree.
+ * ref_cnt          device int32 [num_blocks].
+ * outputs          device or pinned; seq_lens_out, blocks_held_out and free_head_out may
+ *                  be the inputs themselves.  block_pairs: int64 [num_seqs][2].
+ * num_seqs <= 65535; others as pa_release_blocks.
+ */
+pa_status pa_fork_blocks(const int32_t* src, const int32_t* seq_lens, int32_t* block_tables,
+                         int32_t max_blocks_per_seq, const int32_t* blocks_held, int32_t num_seqs,
+                         int32_t* ref_cnt, const int32_t* free_blocks, int32_t num_free,
+                         const int32_t* free_head, void* const* k_caches, void* const* v_caches,
+                         int32_t num_layers, int32_t* seq_lens_out, int32_t* blocks_held_out,
+                         int32_t* free_head_out, int64_t* block_pairs, const pa_cache_desc* cache,
                          void* stream);
 
 /* Human-readable name of a status code (static string). */

@@ -26,6 +26,7 @@ __all__ = ["write_kv", "write_kv_positions", "copy_blocks", "decode", "decode_ap
            "decode_shared_prefix_mode", "prefill",
            "plan_step", "StepPlan", "decode_tree", "decode_tree_workspace_bytes", "accept_tree",
            "MAX_TREE_NODES",
+           "rope_write", "verify_tree", "release_blocks", "fork_blocks",
            "decode_workspace_bytes", "decode_partition_tokens",
            "decode_path", "last_device_error", "PaError", "build", "BlockPool",
            "SharedTailWrite", "LIBRARY_PATH", "load_library", "CacheDesc"]
@@ -34,6 +35,7 @@ PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA = r
 PA_F32, PA_BF16 = 0, 1
 DEVERR_TABLE_ENTRY, DEVERR_SEQ_LEN, DEVERR_SLOT, DEVERR_TIMEOUT, DEVERR_BLOCK_PAIR = 1, 2, 4, 8, 16
 DEVERR_GROUP, DEVERR_POOL, DEVERR_SHARED, DEVERR_TREE = 32, 64, 128, 256
+DEVERR_LOGITS, DEVERR_FORK = 512, 1024
 MAX_TREE_NODES = 256
 SHARED_AUTO, SHARED_ONCE, SHARED_PLAIN = 0, 1, 2
 
@@ -42,6 +44,13 @@ class CacheDesc(ctypes.Structure):
     _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * 3), ("cyclic", ctypes.c_int32),
+                ("neighbours", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("eps", ctypes.c_float)]
 
 
 class PaError(RuntimeError):
@@ -101,6 +110,17 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.pa_decode_tree.restype = ctypes.c_int
     lib.pa_accept_tree.argtypes = [P, P, P, P, I32, I32, I32, P, I32, P, P, I32, P, P, DP, P]
     lib.pa_accept_tree.restype = ctypes.c_int
+    lib.pa_rope_write.argtypes = [P, P, P, I64, I64, I64, I32, I32, P, P, P, P,
+                                  ctypes.POINTER(RopeDesc), P, P, P, P, DP, P]
+    lib.pa_rope_write.restype = ctypes.c_int
+    lib.pa_verify_tree.argtypes = [P, P, I64, I64, I32, I32, P, P, P, I32, I32, I32, P, P, I64, P,
+                                   P, P, P]
+    lib.pa_verify_tree.restype = ctypes.c_int
+    lib.pa_release_blocks.argtypes = [P, P, I32, P, I32, P, I32, P, P, I32, I32, P, P, P]
+    lib.pa_release_blocks.restype = ctypes.c_int
+    lib.pa_fork_blocks.argtypes = [P, P, P, I32, P, I32, P, P, I32, P, P, P, I32, P, P, P, P, DP,
+                                   P]
+    lib.pa_fork_blocks.restype = ctypes.c_int
     lib.pa_decode_path.argtypes = [I32, DP]
     lib.pa_decode_path.restype = I32
     lib.pa_status_str.argtypes = [ctypes.c_int]
@@ -754,3 +774,252 @@ def accept_tree(leaf, parents, query_start_loc, seq_lens, k_caches, v_caches, bl
     if st != PA_OK:
         raise PaError(st, "pa_accept_tree")
     return new_lens, accepted_rows
+
+
+# ---- around the attention -----------------------------------------------------------
+
+def _token_rows(t, d: int, what: str):
+    """(tokens, heads, elements from token to token) of [n, heads, D] rows whose
+    heads follow one another; tokens may be apart (slices of a projection)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError(f"{what} must be [num_tokens, heads, {d}]")
+    n, heads, _ = shape
+    if (d > 1 and stride[2] != 1) or (heads > 1 and stride[1] != d) \
+            or (n > 1 and stride[0] < heads * d):
+        raise ValueError(f"the heads of {what} must follow one another, tokens without overlap")
+    return n, heads, stride[0] if n > 1 else heads * d
+
+
+def rope_write(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, q_weight=None,
+               k_weight=None, eps: float = 1e-6, sections=None, cyclic: bool = False,
+               neighbours: bool = False, scale: float = 1.0, out=None, stream=None):
+    """A layer's projected rows to its attention in one pass: each head of q
+    [n, Hq, D] and k [n, Hkv, D] is normed (``q_weight``, ``k_weight`` [D]; None:
+    not normed) and its first 2 * len(``inv_freq``) dimensions rotated by the
+    token's position; the keys and v [n, Hkv, D] go to the caches at
+    ``slot_mapping``.  Returns the queries, ``out`` [n, Hq, D].
+
+    ``positions`` is int32 [n], or [axes, n] with ``sections``, the pairs of each of
+    2 or 3 axes (in order; ``cyclic``: the axes alternate).  Pair j is (j, j +
+    len(inv_freq)), with ``neighbours`` (2 j, 2 j + 1).  ``scale`` multiplies cos and
+    sin.  q, k and v may be slices of one projection's rows (tokens apart, heads
+    together).  A token with a negative (first) position is skipped, its row of
+    ``out`` left as it was; one with a negative slot is not cached.  ``out`` may be
+    q itself where its tokens follow one another."""
+    device = _current(k_cache)
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache are [num_blocks, num_kv_heads, block_size, "
+                         "head_dim], of one shape")
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported cache dtype {dtype}")
+    blocks, heads, block, d = shape
+    n, hq, q_stride = _token_rows(q, d, "q")
+    kn, k_heads, k_stride = _token_rows(k, d, "k")
+    vn, v_heads, v_stride = _token_rows(v, d, "v")
+    if kn != n or vn != n or k_heads != heads or v_heads != heads:
+        raise ValueError(f"k, v must be [{n}, {heads}, {d}]")
+    if q.dtype is not dtype or k.dtype is not dtype or v.dtype is not dtype \
+            or v_cache.dtype is not dtype:
+        raise ValueError("q, k, v and caches must share one dtype")
+    for w in (q_weight, k_weight):
+        if w is not None:
+            if w.dtype is not dtype or w.numel() != d:
+                raise ValueError(f"norm weights must be [{d}], of the caches' dtype")
+            _contiguous(w)
+    axes = 1 if sections is None else len(sections)
+    if not 1 <= axes <= 3:
+        raise ValueError("sections are the pairs of 1 to 3 axes")
+    if positions.numel() != axes * n or slot_mapping.numel() != n \
+            or (positions.dim() == 2 and positions.shape[0] != axes):
+        raise ValueError("positions ([n], or [axes, n] with sections) and slot_mapping [n] must "
+                         "have an entry per token")
+    if slot_mapping.dtype is not torch.int64 or inv_freq.dtype is not torch.float32:
+        raise ValueError("slot_mapping must be int64 and inv_freq float32")
+    _int32(positions)
+    if out is None:
+        out = _empty((n, hq, d), dtype, device, stream)
+    elif out.shape != q.shape or out.dtype is not dtype:
+        raise ValueError("out must have q's shape and dtype")
+    _contiguous(k_cache, v_cache, positions, inv_freq, slot_mapping, out)
+    desc = CacheDesc(blocks, block, heads, d, _DTYPES[dtype])
+    rope = RopeDesc(2 * inv_freq.numel(), axes, (ctypes.c_int32 * 3)(*(sections or ())),
+                    bool(cyclic), bool(neighbours), scale, eps)
+    st = load_library().pa_rope_write(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, n, hq,
+        positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight), _ptr(k_weight),
+        ctypes.byref(rope), slot_mapping.data_ptr(), out.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), ctypes.byref(desc), _raw_stream(stream, device))
+    if st != PA_OK:
+        raise PaError(st, "pa_rope_write")
+    return out
+
+
+def _rows(t, what: str) -> int:
+    """Elements from row to row of a matrix whose rows' elements follow one another."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions")
+    width, (step, one) = t.shape[1], t.stride()
+    if (width > 1 and one != 1) or (t.shape[0] > 1 and step < width):
+        raise ValueError(f"the elements of a row of {what} must follow one another, rows without "
+                         "overlap")
+    return step if t.shape[0] > 1 else width
+
+
+def verify_tree(logits, tokens, parents, query_start_loc, uniforms, noise, max_q_len: int,
+                draft_logits=None, temperature=None, leaf=None, next_tokens=None, stream=None):
+    """Which drafted tokens hold against the target's probabilities, and the token
+    that follows, from given random numbers.  Returns (leaf, next_tokens), int32
+    [N]: each tree's deepest node that holds (what ``accept_tree`` takes) and the
+    token drawn behind it.
+
+    Sequence i's nodes are the rows query_start_loc[i]..query_start_loc[i+1]; node 0
+    is its last sampled token, whose drafted continuations are the nodes below it
+    (``parents`` as in ``decode_tree``, ``tokens`` [total_q]).  ``logits``
+    [total_q, V] are the target's behind each node, ``draft_logits`` the draft's
+    that the node's children were drawn from (None: the children were chosen, not
+    drawn).  ``uniforms`` [total_q] in [0, 1) decide each drafted token, exponential
+    ``noise`` [N, V] the next one; ``temperature`` [N] divides both logits (0:
+    greedy; None: 1).  With one node a sequence it samples plainly."""
+    device = _current(logits)
+    dtype = logits.dtype
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported logits dtype {dtype}")
+    step = _rows(logits, "logits")
+    noise_step = _rows(noise, "noise")
+    total, vocab = logits.shape
+    n = query_start_loc.numel() - 1
+    draft_step = 0
+    if draft_logits is not None:
+        draft_step = _rows(draft_logits, "draft_logits")
+        if draft_logits.shape != logits.shape or draft_logits.dtype is not dtype:
+            raise ValueError("draft_logits must have the shape and dtype of logits")
+    if n < 0 or tokens.numel() != total or parents.numel() != total \
+            or uniforms.numel() != total or tuple(noise.shape) != (n, vocab):
+        raise ValueError("logits, tokens, parents and uniforms must have a row per node, noise "
+                         "[N, V] one per sequence")
+    f32 = torch.float32
+    if uniforms.dtype is not f32 or noise.dtype is not f32 \
+            or (temperature is not None and temperature.dtype is not f32):
+        raise ValueError("uniforms, noise and temperature must be float32")
+    if temperature is not None:
+        if temperature.numel() != n:
+            raise ValueError("temperature must have an entry per sequence")
+        _contiguous(temperature)
+    if leaf is None:
+        leaf = _empty(n, torch.int32, device, stream)
+    if next_tokens is None:
+        next_tokens = _empty(n, torch.int32, device, stream)
+    if leaf.numel() != n or next_tokens.numel() != n:
+        raise ValueError("leaf and next_tokens must have an entry per sequence")
+    _int32(tokens, parents, query_start_loc, leaf, next_tokens)
+    _contiguous(tokens, parents, query_start_loc, uniforms, leaf, next_tokens)
+    st = load_library().pa_verify_tree(
+        logits.data_ptr(), _ptr(draft_logits), step, draft_step, vocab, _DTYPES[dtype],
+        tokens.data_ptr(), parents.data_ptr(), query_start_loc.data_ptr(), n, total, max_q_len,
+        uniforms.data_ptr(), noise.data_ptr(), noise_step, _ptr(temperature), leaf.data_ptr(),
+        next_tokens.data_ptr(), _raw_stream(stream, device))
+    if st != PA_OK:
+        raise PaError(st, "pa_verify_tree")
+    return leaf, next_tokens
+
+
+def release_blocks(seq_lens, block_tables, blocks_held, free_blocks, free_head, num_blocks: int,
+                   block_size: int, ref_cnt=None, blocks_held_out=None, free_head_out=None,
+                   stream=None):
+    """Blocks that sequences no longer need go back to the free queue of
+    ``plan_step``, on the device (``BlockPool.release``).  Sequence i keeps the
+    blocks of its first seq_lens[i] tokens (0 for a finished request); the others
+    of its blocks_held[i] lose a reference in ``ref_cnt`` (int32 [num_blocks]; None:
+    no block is shared), and those at none are put in front of the queue, in the
+    order of sequences and table entries.  Returns (blocks_held, free_head) after
+    it, new tensors or the given ones, which may be the inputs.  All or nothing,
+    with a bit of ``last_device_error`` (DEVERR_SEQ_LEN, DEVERR_POOL,
+    DEVERR_SHARED)."""
+    device = _current(block_tables)
+    n = seq_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != n or blocks_held.numel() != n \
+            or free_head.numel() != 1:
+        raise ValueError("seq_lens, blocks_held and block_tables disagree on the sequence count")
+    if blocks_held_out is None:
+        blocks_held_out = _empty(n, torch.int32, device, stream)
+    if free_head_out is None:
+        free_head_out = _empty(1, torch.int32, device, stream)
+    if blocks_held_out.numel() != n or free_head_out.numel() != 1:
+        raise ValueError("blocks_held_out must have N entries, free_head_out one")
+    ints = (seq_lens, block_tables, blocks_held, free_blocks, free_head, blocks_held_out,
+            free_head_out)
+    if ref_cnt is not None:
+        ints += (ref_cnt,)
+        if ref_cnt.numel() != num_blocks:
+            raise ValueError("ref_cnt must have num_blocks entries")
+    _int32(*ints)
+    _contiguous(*ints)
+    st = load_library().pa_release_blocks(
+        seq_lens.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+        blocks_held.data_ptr(), n, free_blocks.data_ptr(), free_blocks.numel(),
+        free_head.data_ptr(), _ptr(ref_cnt), num_blocks, block_size, blocks_held_out.data_ptr(),
+        free_head_out.data_ptr(), _raw_stream(stream, device))
+    if st != PA_OK:
+        raise PaError(st, "pa_release_blocks")
+    return blocks_held_out, free_head_out
+
+
+def fork_blocks(src, seq_lens, block_tables, blocks_held, ref_cnt, free_blocks, free_head,
+                k_caches, v_caches, seq_lens_out=None, blocks_held_out=None, free_head_out=None,
+                block_pairs=None, stream=None):
+    """Sequences that start as copies of others, on the device
+    (``BlockPool.fork``): row i with src[i] >= 0, which holds no blocks, shares the
+    full blocks of sequence src[i] (``ref_cnt`` int32 [num_blocks] counts them) and
+    gets a fresh block of the queue with a copy of its partly filled one, in every
+    layer of ``k_caches`` and ``v_caches`` (as in ``accept_tree``).  Rows of
+    ``block_tables`` are written in place.  Returns (seq_lens, blocks_held,
+    free_head, block_pairs) after it, new tensors or the given ones, the first
+    three of which may be the inputs; block_pairs int64 [N, 2] are the copied blocks
+    (source, fresh), -1 where none was.  All or nothing, with a bit of
+    ``last_device_error`` (DEVERR_FORK, DEVERR_SEQ_LEN, DEVERR_POOL)."""
+    shape, dtype, device, keys = _layer_caches(k_caches)
+    v_shape, v_dtype, v_device, values = _layer_caches(v_caches)
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors live on device {device}, which is not the current one")
+    if len(keys) != len(values) or v_shape != shape or v_dtype is not dtype \
+            or v_device != device:
+        raise ValueError("k_caches and v_caches must have the same layers, shape and dtype")
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported cache dtype {dtype}")
+    n = seq_lens.numel()
+    if src.numel() != n or blocks_held.numel() != n or block_tables.dim() != 2 \
+            or block_tables.shape[0] != n or free_head.numel() != 1:
+        raise ValueError("src, seq_lens, blocks_held and block_tables disagree on the sequence "
+                         "count")
+    if ref_cnt.numel() != shape[0]:
+        raise ValueError("ref_cnt must have num_blocks entries")
+    i32 = torch.int32
+    if seq_lens_out is None:
+        seq_lens_out = _empty(n, i32, device, stream)
+    if blocks_held_out is None:
+        blocks_held_out = _empty(n, i32, device, stream)
+    if free_head_out is None:
+        free_head_out = _empty(1, i32, device, stream)
+    if block_pairs is None:
+        block_pairs = _empty((n, 2), torch.int64, device, stream)
+    if seq_lens_out.numel() != n or blocks_held_out.numel() != n or free_head_out.numel() != 1 \
+            or block_pairs.numel() != 2 * n or block_pairs.dtype is not torch.int64:
+        raise ValueError("seq_lens_out and blocks_held_out must have N entries, free_head_out one, "
+                         "block_pairs int64 [N, 2]")
+    ints = (src, seq_lens, block_tables, blocks_held, ref_cnt, free_blocks, free_head,
+            seq_lens_out, blocks_held_out, free_head_out)
+    _int32(*ints)
+    _contiguous(block_pairs, *ints)
+    ptrs = ctypes.c_void_p * len(keys)
+    desc = CacheDesc(shape[0], shape[2], shape[1], shape[3], _DTYPES[dtype])
+    st = load_library().pa_fork_blocks(
+        src.data_ptr(), seq_lens.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+        blocks_held.data_ptr(), n, ref_cnt.data_ptr(), free_blocks.data_ptr(),
+        free_blocks.numel(), free_head.data_ptr(), ptrs(*keys), ptrs(*values), len(keys),
+        seq_lens_out.data_ptr(), blocks_held_out.data_ptr(), free_head_out.data_ptr(),
+        block_pairs.data_ptr(), ctypes.byref(desc), _raw_stream(stream, device))
+    if st != PA_OK:
+        raise PaError(st, "pa_fork_blocks")
+    return seq_lens_out, blocks_held_out, free_head_out, block_pairs

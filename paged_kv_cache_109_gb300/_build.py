@@ -34,19 +34,32 @@ def stale(lib: str = LIB) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Build libpa.so next to this file unless it is up to date."""
+    """Build libpa.so next to this file unless it is up to date: the source files
+    compile at the same time, then link."""
     if not force and not stale():
         return LIB
+    units = [f for f in sources() if f.endswith(".cu")]
+    objects = [os.path.join(PKG, os.path.basename(f)[:-3] + ".tmp.o") for f in units]
+    jobs = []
+    for src, obj in zip(units, objects):
+        cmd = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
+               "-I", INCLUDE, *extra_flags, "-c", "-o", obj, src]
+        if verbose:
+            cmd.insert(1, "-Xptxas=-v")
+        jobs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True))
+    outputs = [job.communicate()[1] for job in jobs]
+    for job, err in zip(jobs, outputs):
+        if job.returncode != 0:
+            raise RuntimeError(f"nvcc failed ({job.returncode}):\n{err[-4000:]}")
+        if verbose:
+            print(err)
     tmp = LIB + ".tmp"
-    cmd = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-           "-I", INCLUDE, *extra_flags, "-o", tmp, os.path.join(CSRC, "pa.cu")]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    res = subprocess.run([_nvcc(), *ARCH, "-shared", "-o", tmp, *objects],
+                         capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stderr[-4000:]}")
-    if verbose:
-        print(res.stderr)
+    for obj in objects:
+        os.remove(obj)
     os.replace(tmp, LIB)
     return LIB
 

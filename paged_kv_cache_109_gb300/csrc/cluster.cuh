@@ -1,0 +1,51 @@
+// cluster.cuh -- thread-block clusters: rank, barrier, stores into another CTA's
+// shared memory.
+#pragma once
+
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace pa {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+
+// Every thread of every CTA of the cluster: what they wrote before (shared memory of
+// any of the CTAs, global memory) is seen by all behind it.
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();                       // (.aligned: a warp's threads arrive together)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+}
+
+// Address of the same shared variable in CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_map(const void* p, uint32_t rank) {
+    uint32_t out;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(smem_u32(p)), "r"(rank));
+    return out;
+}
+
+__device__ __forceinline__ void cluster_store(uint32_t at, uint32_t x) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+}
+__device__ __forceinline__ void cluster_store(uint32_t at, int32_t x) {
+    cluster_store(at, (uint32_t)x);
+}
+__device__ __forceinline__ void cluster_store(uint32_t at, float x) {
+    cluster_store(at, __float_as_uint(x));
+}
+__device__ __forceinline__ void cluster_store(uint32_t at, double x) {
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(x) : "memory");
+}
+
+}  // namespace pa

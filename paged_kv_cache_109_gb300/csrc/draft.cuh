@@ -28,53 +28,6 @@ bool allow_smem(std::atomic<uint64_t>& done, Kern kern, size_t bytes) {
     return true;
 }
 
-// Device memory of the current device (or managed memory).
-bool current_device_memory(const void* p) {
-    if (!p) return false;
-    cudaPointerAttributes at;
-    int dev = -1;
-    if (cudaPointerGetAttributes(&at, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    return at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == dev);
-}
-
-// map_step_arg for memory that a kernel of the current device may touch: its
-// own, managed or page-locked (nullptr passes).
-template <typename T>
-bool map_current_arg(T*& p) {
-    if (!p) return true;
-    cudaPointerAttributes at;
-    int dev = -1;
-    if (cudaPointerGetAttributes(&at, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    if (at.type == cudaMemoryTypeDevice) return at.device == dev;
-    if (at.type == cudaMemoryTypeHost && at.devicePointer) {
-        p = static_cast<T*>(at.devicePointer);
-        return true;
-    }
-    return at.type == cudaMemoryTypeManaged;
-}
-
-// A debug pass, whose host copies may throw: no exception leaves the library.
-template <typename F>
-pa_status debug_pass(F f) {
-    try {
-        return f();
-    } catch (...) {
-        return PA_ERR_CUDA;
-    }
-}
-
-// Arrays of na and nb bytes share a byte.
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && na && nb && x < y + nb && y < x + na;
-}
-
 pa_status plan_impl(PlanArgs a, cudaStream_t st) {
     const bool small = a.num_seqs <= kPlanSmallSeqs && a.max_tokens <= kPlanSmallTokens;
     cudaError_t err = launch_pdl(small ? plan_scan_kernel<true> : plan_scan_kernel<false>, dim3(1),

@@ -1,0 +1,105 @@
+// host_util.cuh -- host-side helpers of the entry points: argument checks, launches,
+// NVTX ranges.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
+
+#include <utility>
+
+#include "decode_config.cuh"
+
+namespace pa {
+namespace {
+
+bool desc_ok(const pa_cache_desc* c) {
+    return c && c->num_blocks > 0 && c->block_size > 0 && c->num_kv_heads > 0 &&
+           c->head_dim > 0 && (c->dtype == PA_F32 || c->dtype == PA_BF16);
+}
+
+int elem_bytes(const pa_cache_desc* c) { return c->dtype == PA_F32 ? 4 : 2; }
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// ---- launches ------------------------------------------------------------------
+
+// Launch with programmatic stream serialization: the kernel may be scheduled
+// while the previous kernel in the stream finishes; it waits for that kernel
+// (griddepcontrol.wait) before reading any input.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                       cudaStream_t st, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PA_USE_PDL ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// An NVTX range over one library call (host side: argument checks and
+// launches), so profilers can attribute the kernels to the call that made them.
+struct CallRange {
+    explicit CallRange(const char* name) { nvtxRangePushA(name); }
+    ~CallRange() { nvtxRangePop(); }
+    CallRange(const CallRange&) = delete;
+    CallRange& operator=(const CallRange&) = delete;
+};
+
+// ---- memory of the arguments ---------------------------------------------------
+
+// Device memory of the current device (or managed memory).
+bool current_device_memory(const void* p) {
+    if (!p) return false;
+    cudaPointerAttributes at;
+    int dev = -1;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == dev);
+}
+
+// A step argument: replaces p by the address that kernels of the current device
+// use; false for memory they may not touch (allowed: the device's own, managed or
+// page-locked memory; nullptr passes).
+template <typename T>
+bool map_current_arg(T*& p) {
+    if (!p) return true;
+    cudaPointerAttributes at;
+    int dev = -1;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    if (at.type == cudaMemoryTypeDevice) return at.device == dev;
+    if (at.type == cudaMemoryTypeHost && at.devicePointer) {
+        p = static_cast<T*>(at.devicePointer);
+        return true;
+    }
+    return at.type == cudaMemoryTypeManaged;
+}
+
+// A debug pass, whose host copies may throw: no exception leaves the library.
+template <typename F>
+pa_status debug_pass(F f) {
+    try {
+        return f();
+    } catch (...) {
+        return PA_ERR_CUDA;
+    }
+}
+
+// Arrays of na and nb bytes share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+}  // namespace
+}  // namespace pa

@@ -6,13 +6,11 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
 #include <atomic>
 #include <cstring>
 #include <mutex>
-#include <utility>
 
 #include "common.cuh"
 #include "debug_checks.h"
@@ -21,6 +19,7 @@
 #include "decode_config.cuh"
 #include "decode_mma.cuh"
 #include "decode_tma_mma.cuh"
+#include "host_util.cuh"
 #include "merge.cuh"
 #include "prefill_generic.cuh"
 #include "prefill_mma.cuh"
@@ -30,16 +29,12 @@
 #include "write_kv.cuh"
 
 namespace pa {
+
+// Reads and clears the device error word of serving.cu (each source file's kernels
+// have a word of their own).
+bool take_serving_error(unsigned int* bits);
+
 namespace {
-
-bool desc_ok(const pa_cache_desc* c) {
-    return c && c->num_blocks > 0 && c->block_size > 0 && c->num_kv_heads > 0 &&
-           c->head_dim > 0 && (c->dtype == PA_F32 || c->dtype == PA_BF16);
-}
-
-int elem_bytes(const pa_cache_desc* c) { return c->dtype == PA_F32 ? 4 : 2; }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // ---- TMA descriptors -----------------------------------------------------------
 
@@ -97,25 +92,6 @@ bool cached_map(CUtensorMap* out, const void* base, const pa_cache_desc* c, int 
 }
 
 // ---- launches ------------------------------------------------------------------
-
-// Launch with programmatic stream serialization: the kernel may be scheduled
-// while the previous kernel in the stream finishes; it waits for that kernel
-// (griddepcontrol.wait) before reading any input.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                       cudaStream_t st, Args&&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = PA_USE_PDL ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
-}
 
 template <typename E, int W, int VEC>
 cudaError_t launch_merge_k(dim3 grid, cudaStream_t st, const DecodeArgs& a) {
@@ -413,15 +389,6 @@ pa_status launch_write(const void* k, const void* v, SlotFn slot_of, int32_t num
     }
     return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
-
-// An NVTX range over one library call (host side: argument checks and
-// launches), so profilers can attribute the kernels to the call that made them.
-struct CallRange {
-    explicit CallRange(const char* name) { nvtxRangePushA(name); }
-    ~CallRange() { nvtxRangePop(); }
-    CallRange(const CallRange&) = delete;
-    CallRange& operator=(const CallRange&) = delete;
-};
 
 }  // namespace
 }  // namespace pa
@@ -1016,7 +983,9 @@ int32_t pa_last_device_error(void) {
     if (cudaDeviceSynchronize() != cudaSuccess) return -1;
     if (cudaMemcpyFromSymbol(&bits, pa::g_device_error, sizeof(bits)) != cudaSuccess) return -1;
     if (cudaMemcpyToSymbol(pa::g_device_error, &zero, sizeof(zero)) != cudaSuccess) return -1;
-    return (int32_t)bits;
+    unsigned int more = 0;                    // the word of serving.cu's kernels
+    if (!pa::take_serving_error(&more)) return -1;
+    return (int32_t)(bits | more);
 }
 
 }  // extern "C"
