@@ -28,6 +28,16 @@ __device__ __forceinline__ void cluster_sync() {
                  ::: "memory");
 }
 
+// The same in two steps, for work in between.
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Address of the same shared variable in CTA `rank`.
 __device__ __forceinline__ uint32_t cluster_map(const void* p, uint32_t rank) {
     uint32_t out;
