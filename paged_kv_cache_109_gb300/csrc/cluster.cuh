@@ -54,8 +54,18 @@ __device__ __forceinline__ void cluster_store(uint32_t at, int32_t x) {
 __device__ __forceinline__ void cluster_store(uint32_t at, float x) {
     cluster_store(at, __float_as_uint(x));
 }
-__device__ __forceinline__ void cluster_store(uint32_t at, double x) {
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(x) : "memory");
+__device__ __forceinline__ void cluster_store(uint32_t at, float2 x) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(x.x), "f"(x.y) : "memory");
+}
+__device__ __forceinline__ void cluster_store(uint32_t at, float4 x) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(x.x), "f"(x.y),
+                 "f"(x.z), "f"(x.w)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_store(uint32_t at, int4 x) {
+    asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y),
+                 "r"(x.z), "r"(x.w)
+                 : "memory");
 }
 
 }  // namespace pa

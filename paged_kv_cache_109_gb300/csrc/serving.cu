@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
@@ -23,13 +24,28 @@ bool take_serving_error(unsigned int* bits) {
 
 namespace {
 
+// Lets `kern` use `bytes` of dynamic shared memory on the current device: asked for once
+// per instance (`done`, a bit a device).
+template <typename Kern>
+bool allow_smem(std::atomic<uint64_t>& done, Kern kern, size_t bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+        return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
+}
+
 // launch_pdl of a grid whose CTAs form clusters of `ctas` along x.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, unsigned ctas,
+cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, unsigned ctas, size_t smem,
                            cudaStream_t st, Args&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -109,8 +125,10 @@ template <typename E, bool DRAFT, bool WIDE>
 cudaError_t launch_verify(const VerifyArgs& a, int32_t num_seqs, cudaStream_t st) {
     unsigned ctas = 1;
     while (ctas < 8 && num_seqs * ctas < 152 * 2 && a.vocab / (ctas * 2) >= 4096) ctas *= 2;
-    return launch_cluster(verify_tree_kernel<E, DRAFT, WIDE>, dim3(num_seqs * ctas),
-                          dim3(kVerifyThreads), ctas, st, a);
+    auto kern = verify_tree_kernel<E, DRAFT, WIDE>;
+    static std::atomic<uint64_t> allowed;
+    if (!allow_smem(allowed, kern, kVerifyRing)) return cudaErrorUnknown;
+    return launch_cluster(kern, dim3(num_seqs * ctas), dim3(kVerifyThreads), ctas, kVerifyRing, st, a);
 }
 
 template <typename E>
@@ -339,7 +357,7 @@ pa_status pa_release_blocks(const int32_t* seq_lens, const int32_t* block_tables
         return PA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t err = launch_cluster(release_blocks_kernel, dim3(kPoolMaxCluster), dim3(kPoolThreads),
-                                           kPoolMaxCluster, st, a);
+                                           kPoolMaxCluster, 0, st, a);
     return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -395,7 +413,7 @@ pa_status pa_fork_blocks(const int32_t* src, const int32_t* seq_lens, int32_t* b
         if (bases[x] - bases[x - 1] < cache_bytes) return PA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t err = launch_cluster(fork_blocks_kernel, dim3(kPoolMaxCluster), dim3(kPoolThreads),
-                                     kPoolMaxCluster, st, a);
+                                     kPoolMaxCluster, 0, st, a);
     for (int32_t l0 = 0; err == cudaSuccess && num_seqs > 0 && l0 < num_layers; l0 += kForkLayers) {
         const int32_t nl = std::min(kForkLayers, num_layers - l0);
         err = nl <= 16 ? launch_fork_copy<16>(a, cache, k_caches + l0, v_caches + l0, nl, vec, st)

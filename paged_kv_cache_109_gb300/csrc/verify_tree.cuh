@@ -25,6 +25,7 @@
 
 #include "cluster.cuh"
 #include "common.cuh"
+#include "cp_async.cuh"
 #include "ptx.cuh"
 
 namespace pa {
@@ -51,20 +52,33 @@ static_assert(kVerifyThreads >= PA_MAX_TREE_NODES, "a thread per node");
 
 // What a warp tells the CTAs: the largest logit of its share and the sum of
 // exponentials relative to it, of the target's and the draft's row.
-struct VerifyPart {
+struct __align__(16) VerifyPart {
     float top, sum, draft_top, draft_sum;
+};
+
+// A node as the first CTA tells it: first child and next sibling, -1 where there is
+// none.
+struct __align__(16) VerifyNode {
+    int32_t token, child, sibling;
+    float uniform;
+};
+
+// What a CTA's first warp decides for its other warps.
+enum VerifyVerdict : int32_t { kVerifyHolds, kVerifyRest, kVerifyNext, kVerifyFinely, kVerifyDone };
+struct VerifyStep {
+    int32_t verdict, node;                           // node: that holds, to try next; token
+    float top, draft_top, inv, draft_inv;            // the node's rows
+    float spent, rest;                               // c, S
+    float floor;
 };
 
 struct VerifyShared {
     VerifyPart part[2][kVerifyMaxCluster * kVerifyWarps];
-    // the tree, from the first CTA
-    float logit[PA_MAX_TREE_NODES], draft_logit[PA_MAX_TREE_NODES];   // of a node's token
-    float uniform[PA_MAX_TREE_NODES];
-    int32_t token[PA_MAX_TREE_NODES];
-    int32_t child[PA_MAX_TREE_NODES], sibling[PA_MAX_TREE_NODES];     // first, next; -1: none
+    VerifyNode node[PA_MAX_TREE_NODES];
+    float2 logit[PA_MAX_TREE_NODES];                 // of a node's token: target, draft
     int32_t parent[PA_MAX_TREE_NODES];
-    int32_t first, nodes;                            // rows of the sequence (nodes -1: refused)
-    float heat;
+    VerifyStep step;
+    int4 tree;                                       // first row, nodes (-1: refused), temperature
 };
 
 // ---- packed pairs of floats ------------------------------------------------------------
@@ -85,6 +99,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
 
@@ -111,6 +131,21 @@ struct RowVec {
             return fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));
         }
     }
+    // the same, NaN where one is
+    __device__ __forceinline__ float top_or_nan() const {
+        if constexpr (sizeof(E) == 2) {
+            const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
+            const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+            const float x = __low2float(m), y = __high2float(m);
+            return x != x ? x : y != y ? y : fmaxf(x, y);
+        } else {
+            const float* f = reinterpret_cast<const float*>(&r);
+            float m = f[0];
+#pragma unroll
+            for (int i = 1; i < 4; ++i) asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(f[i]));
+            return m;
+        }
+    }
     // elements 2 i and 2 i + 1
     __device__ __forceinline__ uint64_t pair(int i) const {
         const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
@@ -122,21 +157,22 @@ struct RowVec {
 };
 
 // The running maximum of a share and its sum of exponentials.  A NaN or +inf makes
-// the sum NaN; -inf counts as nothing.
+// the sum NaN; -inf counts as nothing.  The maximum starts at the lowest finite value:
+// a row of nothing but that has weights of one, and no -inf is subtracted from another.
+constexpr float kLowest = -3.402823466e38f;
 struct RowSum {
     float top, scale;
     uint64_t sum;                   // two parts
     __device__ __forceinline__ void start(float s) {
-        top = -INFINITY;
+        top = kLowest;
         scale = s;
         sum = 0;
     }
     __device__ __forceinline__ void raise(float m) {
-        if (m > top) {
-            const float f = ex2_approx((top - m) * scale);
-            sum = mul2(sum, pack2(f, f));
-            top = m;
-        }
+        m = fmaxf(m, top);
+        const float f = ex2_approx((top - m) * scale);
+        sum = mul2(sum, pack2(f, f));
+        top = m;
     }
     template <typename E, int U>
     __device__ __forceinline__ void take(const RowVec<E> (&v)[U]) {
@@ -144,35 +180,45 @@ struct RowSum {
 #pragma unroll
         for (int u = 1; u < U; ++u) m = fmaxf(m, v[u].top());
         raise(m);
-        const float base = top == -INFINITY ? 0.f : -top;
-        const uint64_t off = pack2(base, base), by = pack2(scale, scale);
+        const uint64_t off = pack2(-top, -top), by = pack2(scale, scale);
+        uint64_t part[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            part[u] = 0;
 #pragma unroll
             for (int i = 0; i < RowVec<E>::kCount / 2; ++i) {
                 float a, b;
                 unpack2(mul2(add2(v[u].pair(i), off), by), a, b);
-                sum = add2(sum, pack2(ex2_approx(a), ex2_approx(b)));
+                const uint64_t w = pack2(ex2_approx(a), ex2_approx(b));
+                part[u] = i == 0 ? w : add2(part[u], w);
             }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) sum = add2(sum, part[u]);
     }
     __device__ __forceinline__ void take(float x) {
         raise(x);
-        const float w = ex2_approx((x - (top == -INFINITY ? 0.f : top)) * scale);
-        sum = add2(sum, pack2(w, 0.f));
+        sum = add2(sum, pack2(ex2_approx((x - top) * scale), 0.f));
     }
-    // of the warp: top and sum in all lanes
-    __device__ __forceinline__ void reduce(float& all_top, float& all_sum) const {
-        float a, b, m = top;
+    __device__ __forceinline__ float total() const {
+        float a, b;
         unpack2(sum, a, b);
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        // (a share without a finite value keeps its zero or NaN)
-        float s = a + b;
-        if (top != -INFINITY) s *= ex2_approx((top - m) * scale);
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        all_top = m;
-        all_sum = s;
+        return a + b;
     }
 };
+
+// Two sums of the warp (their tops and totals in all lanes).
+__device__ __forceinline__ void reduce_sums(const RowSum& x, const RowSum& y, float& top_x, float& sum_x,
+                                            float& top_y, float& sum_y) {
+    top_x = warp_max(x.top);
+    top_y = warp_max(y.top);
+    sum_x = x.total() * ex2_approx((x.top - top_x) * x.scale);
+    sum_y = y.total() * ex2_approx((y.top - top_y) * y.scale);
+    for (int off = 16; off > 0; off >>= 1) {
+        sum_x += __shfl_xor_sync(0xffffffffu, sum_x, off);
+        sum_y += __shfl_xor_sync(0xffffffffu, sum_y, off);
+    }
+}
 
 // A share [lo, hi) of a row: the 16-byte pieces inside it, and the elements before and
 // behind them.
@@ -201,53 +247,91 @@ struct RowShare {
     }
 };
 
-// One row, or two at once (their shares may be cut differently).
-constexpr int kRowUnroll = 4;
+// The rows' sums of a step: one row, or two at once (their shares may be cut
+// differently).  Pieces come by asynchronous copies into shared memory, each thread's
+// own ones, so that none waits for another; kVerifyDepth steps of four pieces are under
+// way at a time, which registers would not hold.
+constexpr int kVerifyDepth = 2;
+constexpr size_t kVerifyRing = (size_t)kVerifyDepth * 4 * kVerifyThreads * 16;
+
 template <typename E, bool TWO>
-__device__ __forceinline__ void row_sums(const RowShare<E>& x, const RowShare<E>& y, RowSum& sx,
-                                         RowSum& sy) {
-    constexpr int U = kRowUnroll;
-    const int32_t n = TWO ? max(x.pieces, y.pieces) : x.pieces;
-    for (int32_t v = threadIdx.x; v < n; v += U * kVerifyThreads) {
-        RowVec<E> a[U], b[TWO ? U : 1];
+__device__ __forceinline__ void row_sums(uint4* ring, const RowShare<E>& x, const RowShare<E>& y,
+                                         RowSum& sx, RowSum& sy) {
+    constexpr int N = RowVec<E>::kCount, T = kVerifyThreads;
+    constexpr int X = TWO ? 2 : 4;      // x's pieces of a step
+    const int32_t tid = threadIdx.x;
+    const int32_t most = TWO ? max(x.pieces, y.pieces) : x.pieces;
+    uint4* mine = ring + tid;
+    auto issue = [&](int32_t at, uint4* slot) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int32_t at = v + u * kVerifyThreads;
-            if (at < x.pieces) a[u].load(x.body + (int64_t)at * RowVec<E>::kCount);
-            else a[u].clear();
+        for (int u = 0; u < 4; ++u) {
+            const RowShare<E>& r = u < X ? x : y;
+            const int32_t p = at + (u < X ? u : u - X) * T;
+            if (p < r.pieces) cp_async16(smem_u32(slot + u * T), r.body + (int64_t)p * N, 16);
+        }
+        cp_async_commit();
+    };
+    int32_t ahead = tid;
+#pragma unroll
+    for (int d = 0; d < kVerifyDepth; ++d, ahead += X * T) issue(ahead, mine + d * 4 * T);
+    int d = 0;
+    for (int32_t at = tid; at < most; at += X * T, ahead += X * T) {
+        cp_async_wait<kVerifyDepth - 1>();
+        uint4* slot = mine + d * 4 * T;
+        RowVec<E> a[X], b[TWO ? 2 : 1];
+#pragma unroll
+        for (int u = 0; u < X; ++u) {
+            a[u].clear();
+            if (at + u * T < x.pieces) a[u].r = slot[u * T];
         }
         if constexpr (TWO) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int32_t at = v + u * kVerifyThreads;
-                if (at < y.pieces) b[u].load(y.body + (int64_t)at * RowVec<E>::kCount);
-                else b[u].clear();
+            for (int u = 0; u < 2; ++u) {
+                b[u].clear();
+                if (at + u * T < y.pieces) b[u].r = slot[(X + u) * T];
             }
         }
+        issue(ahead, slot);
+        d = d + 1 == kVerifyDepth ? 0 : d + 1;
         sx.take(a);
         if constexpr (TWO) sy.take(b);
     }
+    cp_async_wait<0>();
     x.ends(sx);
     if constexpr (TWO) y.ends(sy);
 }
 
-// 8 elements from p on, -inf past `count`.
+// 8 elements of a row as they are stored.
 template <typename E, bool WIDE>
-__device__ __forceinline__ void load8(const E* p, int32_t count, float (&x)[8]) {
-    if (WIDE && count >= 8) {
-        constexpr int N = RowVec<E>::kCount;
+struct Octet {
+    static constexpr int N = RowVec<E>::kCount;
+    RowVec<E> v[8 / N];
+    // from p on, -inf past `count`
+    __device__ __forceinline__ void load(const E* p, int32_t count) {
+        if (WIDE && count >= 8) {
 #pragma unroll
-        for (int u = 0; u < 8 / N; ++u) {
-            RowVec<E> v;
-            v.load(p + u * N);
+            for (int u = 0; u < 8 / N; ++u) v[u].load(p + u * N);
+        } else {
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) unpack2(v.pair(i), x[u * N + 2 * i], x[u * N + 2 * i + 1]);
+            for (int u = 0; u < 8 / N; ++u) v[u].clear();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < count) reinterpret_cast<E*>(&v[i / N])[i % N] = p[i];
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < count ? Elem<E>::to_float(p[i]) : -INFINITY;
     }
-}
+    __device__ __forceinline__ uint64_t pair(int i) const { return v[2 * i / N].pair(i % (N / 2)); }
+    // exponentials relative to the largest
+    __device__ __forceinline__ void powers(float top, float scale, float (&w)[8]) const {
+        const uint64_t off = pack2(-top, -top), by = pack2(scale, scale);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            unpack2(mul2(add2(pair(i), off), by), a, b);
+            w[2 * i] = ex2_approx(a);
+            w[2 * i + 1] = ex2_approx(b);
+        }
+    }
+};
 
 // (value, index): the larger value, the lower index of equal ones.
 __device__ __forceinline__ void take_better(float& v, int32_t& i, float w, int32_t j) {
@@ -265,6 +349,7 @@ __device__ __forceinline__ void warp_best(float& v, int32_t& i) {
 // it: the product's rounding is taken into the result.
 struct FineScale {
     float hi, lo;
+    __device__ __forceinline__ FineScale() {}
     __device__ __forceinline__ explicit FineScale(float heat) {
         constexpr float kLog2eRest = (float)(1.4426950408889634 - (double)kLog2e);
         hi = kLog2e / heat;
@@ -279,17 +364,169 @@ struct FineScale {
 
 __device__ __forceinline__ float rcp_approx(float x) {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
-// A node's row: largest logit, 1 / sum.
-struct VerifyRow {
-    float top, inv;
+// The race for the next token: the largest key, its place and least value, and the
+// next largest key (all >= 0).
+struct Race {
+    float first, least, second;
+    int32_t index;
+    __device__ __forceinline__ void start() {
+        first = least = second = 0.f;
+        index = INT32_MAX;
+    }
+    __device__ __forceinline__ void take(float key, float low, int32_t at) {
+        second = fmaxf(second, fminf(first, key));
+        if (key > first) {
+            index = at;
+            least = low;
+        }
+        first = fmaxf(first, key);
+    }
+    __device__ __forceinline__ void join(const Race& o) {
+        second = fmaxf(fmaxf(second, o.second), fminf(first, o.first));
+        if (o.first > first || (o.first == first && o.index < index)) {
+            first = o.first;
+            least = o.least;
+            index = o.index;
+        }
+    }
+    // of the warp, in all lanes
+    __device__ __forceinline__ void reduce() {
+        const float m = warp_max(first);
+        const int32_t at = __reduce_min_sync(0xffffffffu, first == m ? index : INT32_MAX);
+        const bool mine = first == m && index == at;
+        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+        second = warp_max((threadIdx.x & 31) == __ffs(who) - 1 ? second : fmaxf(first, second));
+        least = __shfl_sync(0xffffffffu, least, __ffs(who) - 1);
+        first = m;
+        index = at;
+    }
+};
+
+// What a race runs over: a share of the node's rows and of the noise.  The weights are
+// those of P, or (with a share) of max(P - c q, 0), relative to P's largest.
+//
+// Keys are first taken with short exponentials and reciprocals.  A weight's exponent y
+// is off by 2^-23 |y|, its exponential, the reciprocal and the products by less: kOpen
+// = 2^-16 of each term covers them for weights down to 2^-64.  A key is the most that
+// this leaves open, divided by 1 + kOpen; only where another key reaches the least
+// value of the best one are those that can still win computed finely.  (Noise below
+// 2^-126 counts as zero.)
+constexpr float kOpen = 0x1p-16f;
+
+template <typename E, bool DRAFT, bool WIDE>
+struct RaceField {
+    const E* row;
+    const E* drow;
+    const float* noise;
+    const VerifyNode* node;         // the tree
+    FineScale fine;
+    float top, draft_top, share;    // share: c sum(P) / sum(q)
+    int32_t lo, hi, child;          // child: first of the tokens that are out (DRAFT: none)
+
+    struct Tokens {                 // 8 of them
+        Octet<E, WIDE> x, y;
+        Octet<float, WIDE> e;
+    };
+    __device__ __forceinline__ void load(Tokens& t, int32_t o) const {
+        t.x.load(row + o, hi - o);
+        t.e.load(noise + o, hi - o);
+        if (DRAFT && share != 0.f) t.y.load(drow + o, hi - o);
+    }
+    // Their keys, with `share` times `bound`.
+    __device__ __forceinline__ void keys(const Tokens& t, int32_t o, float bound, float (&key)[8]) const {
+        float up[8];
+        t.x.powers(top, fine.hi, up);
+        if (DRAFT && share != 0.f) {
+            float down[8];
+            t.y.powers(draft_top, fine.hi, down);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) up[i] = fmaf(down[i], -share * bound, up[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            unpack2(t.e.pair(i), a, b);
+            key[2 * i] = up[2 * i] * rcp_approx(a);
+            key[2 * i + 1] = up[2 * i + 1] * rcp_approx(b);
+        }
+        if (!DRAFT)
+            for (int32_t j = child; j >= 0; j = node[j].sibling) {
+                const int32_t at = node[j].token - o;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (at == i) key[i] = 0.f;
+            }
+    }
+    __device__ __forceinline__ Race run() const {
+        constexpr float kMost = (1.f - kOpen) / (1.f + kOpen), kLeast = (1.f + kOpen) / (1.f - kOpen);
+        constexpr int32_t kStep = 8 * kVerifyThreads;
+        float first = 0.f, second = 0.f;
+        int32_t at = -1;                // group of the largest
+        int32_t o = lo + 8 * (int32_t)threadIdx.x;
+        // (the next 8 are on their way meanwhile; fp32 rows have no registers for that)
+        constexpr bool kNext = sizeof(E) == 2;
+        Tokens t;
+        if (kNext && o < hi) load(t, o);
+        while (o < hi) {
+            Tokens next;
+            if (!kNext) load(t, o);
+            if (kNext && o + kStep < hi) load(next, o + kStep);
+            float key[8];
+            keys(t, o, kMost, key);
+            // (a NaN, as of no weight and no noise, is left out)
+            const float m = fmaxf(fmaxf(fmaxf(key[0], key[1]), fmaxf(key[2], key[3])),
+                                  fmaxf(fmaxf(key[4], key[5]), fmaxf(key[6], key[7])));
+            second = fmaxf(second, fminf(first, m));
+            if (m > first) at = o;
+            first = fmaxf(first, m);
+            if (kNext) t = next;
+            o += kStep;
+        }
+        Race r;
+        r.start();
+        if (at >= 0) {
+            float key[8], low[8];
+            load(t, at);
+            keys(t, at, kMost, key);
+            keys(t, at, kLeast, low);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                r.take(fmaxf(key[i], 0.f), low[i] * (1.f - 2.f * kOpen), at + i);
+        }
+        r.second = fmaxf(r.second, second);
+        return r;
+    }
+    // Finely, those whose key is `floor` or more.
+    __device__ __forceinline__ Race run_finely(float floor) const {
+        constexpr float kMost = (1.f - kOpen) / (1.f + kOpen);
+        Race r;
+        r.start();
+#pragma unroll 1
+        for (int32_t o = lo + (int32_t)threadIdx.x; o < hi; o += kVerifyThreads) {
+            const float x = Elem<E>::to_float(row[o]), e = noise[o];
+            const float y = DRAFT && share != 0.f ? Elem<E>::to_float(drow[o]) : -INFINITY;
+            float key = ex2_approx((x - top) * fine.hi);
+            if (DRAFT && share != 0.f) key = fmaf(ex2_approx((y - draft_top) * fine.hi), -share * kMost, key);
+            if (!(key * rcp_approx(e) >= floor)) continue;
+            bool out = false;
+            if (!DRAFT)
+                for (int32_t j = child; j >= 0; j = node[j].sibling) out |= node[j].token == o;
+            if (out) continue;
+            float w = fine.power(x, top);
+            if (DRAFT && share != 0.f) w -= fine.power(y, draft_top) * share;
+            r.take(fmaxf(w / (e < 0x1p-126f ? 0.f : e), 0.f), 0.f, o);
+        }
+        return r;
+    }
 };
 
 template <typename E, bool DRAFT, bool WIDE>
 __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const VerifyArgs a) {
+    extern __shared__ uint4 ring[];     // kVerifyRing
     __shared__ VerifyShared s;
     griddep_wait();
     griddep_launch_dependents();
@@ -341,63 +578,54 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
     const bool inner = __syncthreads_or(parent == 0);        // node 0 has children
     if (tid == 0 && nodes > 0 && DRAFT && inner && !(heat <= 0.f))
         RowShare<E>(draft + (int64_t)q0 * a.draft_stride, lo, hi).prefetch();
-    int32_t child = -1, sibling = -1;
     if (rank == 0) {
         s.parent[tid] = parent;
         __syncthreads();
+        VerifyNode n{token, -1, -1, uniform};
         for (int32_t j = nodes - 1; j > tid; --j) {
             const int32_t p = s.parent[j];
-            if (p == tid) child = j;
-            if (p == parent) sibling = j;
+            if (p == tid) n.child = j;
+            if (p == parent) n.sibling = j;
         }
+        s.node[tid] = n;
     }
 
     uint32_t turn = 0;                  // exchanges so far
     // the warp's part to every CTA; all warps' parts
     auto exchange = [&](const VerifyPart& mine) -> const VerifyPart* {
         const uint32_t at = turn++ & 1;
-        if (lane < (int32_t)ctas) {
-            const uint32_t to = cluster_map(&s.part[at][rank * kVerifyWarps + warp], lane);
-            cluster_store(to, mine.top);
-            cluster_store(to + 4, mine.sum);
-            cluster_store(to + 8, mine.draft_top);
-            cluster_store(to + 12, mine.draft_sum);
-        }
+        if (lane < (int32_t)ctas)
+            cluster_store(cluster_map(&s.part[at][rank * kVerifyWarps + warp], lane),
+                          make_float4(mine.top, mine.sum, mine.draft_top, mine.draft_sum));
         cluster_sync();
         return s.part[at];
     };
     const int32_t parts = (int32_t)ctas * kVerifyWarps;
-    auto best_of = [&](const VerifyPart* all, float floor, int32_t& index) {
-        float v = floor;
-        index = INT32_MAX;
-        for (int32_t e = lane; e < parts; e += 32) take_better(v, index, all[e].top, __float_as_int(all[e].sum));
-        warp_best(v, index);
-        return v;
-    };
-    auto give_up = [&](unsigned int why) {
+    // the first CTA gives the sequence's results
+    auto finish = [&](unsigned int why, int32_t leaf, int32_t next) {
         if (rank == 0 && tid == 0) {
             if (why) raise_error(why);
-            a.leaf[seq] = a.next[seq] = -1;
+            a.leaf[seq] = leaf;
+            a.next[seq] = next;
         }
     };
 
     int32_t cur = 0;
     bool any = inner;
-    VerifyRow p{}, q{};
-    float spent = 0.f;                  // c, once no child holds
+    FineScale fine(heat <= 0.f ? 1.f : heat);
     for (bool begin = true;; begin = false) {
         const bool cold = heat <= 0.f;
         const E* row = target + (int64_t)(q0 + cur) * a.logit_stride;
         const E* drow = DRAFT ? draft + (int64_t)(q0 + cur) * a.draft_stride : nullptr;
         // the children's logits
         const bool told = rank == 0 && !cold && parent == cur && token >= 0 && token < vocab;
-        float tl = 0.f, dl = 0.f;
+        float2 logit = make_float2(0.f, 0.f);
         if (told) {
-            tl = Elem<E>::to_float(row[token]);
-            if (DRAFT) dl = Elem<E>::to_float(drow[token]);
+            logit.x = Elem<E>::to_float(row[token]);
+            if (DRAFT) logit.y = Elem<E>::to_float(drow[token]);
         }
-        VerifyPart mine{-INFINITY, 0.f, -INFINITY, 0.f};
-        const float scale = cold ? 1.f : kLog2e / heat;
+        VerifyPart mine{kLowest, 0.f, kLowest, 0.f};
+        const float scale = fine.hi;
         if (nodes > 0 && cold) {
             // the first largest logit; a NaN counts as an infinity
             int32_t best = INT32_MAX;
@@ -411,13 +639,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
             for (int32_t u = tid; u < x.pieces; u += kVerifyThreads) {
                 RowVec<E> w;
                 w.load(x.body + (int64_t)u * RowVec<E>::kCount);
-                float m = 0.f;          // (a NaN leaves one in the sum)
-                float y[RowVec<E>::kCount];
-#pragma unroll
-                for (int i = 0; i < RowVec<E>::kCount / 2; ++i) unpack2(w.pair(i), y[2 * i], y[2 * i + 1]);
-#pragma unroll
-                for (int i = 0; i < RowVec<E>::kCount; ++i) m += y[i] * 0.f;
-                if (w.top() > v || m != m) {
+                if (!(w.top_or_nan() <= v)) {
                     const int32_t at = lo + x.front + u * RowVec<E>::kCount;
                     for (int i = 0; i < RowVec<E>::kCount; ++i) one(at + i);
                 }
@@ -432,195 +654,199 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
             sy.start(scale);
             const RowShare<E> x(row, lo, hi);
             if (DRAFT && any) {
-                row_sums<E, true>(x, RowShare<E>(drow, lo, hi), sx, sy);
-                sy.reduce(mine.draft_top, mine.draft_sum);
+                row_sums<E, true>(ring, x, RowShare<E>(drow, lo, hi), sx, sy);
             } else {
-                row_sums<E, false>(x, x, sx, sx);
+                row_sums<E, false>(ring, x, x, sx, sx);
             }
-            sx.reduce(mine.top, mine.sum);
+            reduce_sums(sx, sy, mine.top, mine.sum, mine.draft_top, mine.draft_sum);
         }
         if (begin) cluster_wait();      // all CTAs run: their shared memory is there
         if (begin && rank == 0) {
-            for (uint32_t r = 0; r < ctas; ++r) {
-                if (tid < nodes) {
-                    cluster_store(cluster_map(&s.token[tid], r), token);
-                    cluster_store(cluster_map(&s.uniform[tid], r), uniform);
-                    cluster_store(cluster_map(&s.child[tid], r), child);
-                    cluster_store(cluster_map(&s.sibling[tid], r), sibling);
-                }
-                if (tid == 0) {
-                    cluster_store(cluster_map(&s.first, r), q0);
-                    cluster_store(cluster_map(&s.nodes, r), nodes);
-                    cluster_store(cluster_map(&s.heat, r), heat);
-                }
+            __syncthreads();
+            for (int32_t x = tid; x < nodes * (int32_t)ctas; x += kVerifyThreads) {
+                const int32_t r = x / nodes, j = x - r * nodes;
+                cluster_store(cluster_map(&s.node[j], r), *reinterpret_cast<const int4*>(&s.node[j]));
             }
+            if (tid < (int32_t)ctas)
+                cluster_store(cluster_map(&s.tree, tid), make_int4(q0, nodes, __float_as_int(heat), 0));
         }
-        if (told)
-            for (uint32_t r = 0; r < ctas; ++r) {
-                cluster_store(cluster_map(&s.logit[tid], r), tl);
-                if (DRAFT) cluster_store(cluster_map(&s.draft_logit[tid], r), dl);
-            }
+        for (uint32_t m = __ballot_sync(0xffffffffu, told); m != 0; m &= m - 1) {
+            const int32_t l = __ffs(m) - 1;
+            const float2 x = make_float2(__shfl_sync(0xffffffffu, logit.x, l), __shfl_sync(0xffffffffu, logit.y, l));
+            if (lane < (int32_t)ctas) cluster_store(cluster_map(&s.logit[warp * 32 + l], lane), x);
+        }
         const VerifyPart* all = exchange(mine);
         if (begin) {
-            q0 = s.first;
-            nodes = s.nodes;
-            heat = s.heat;
+            q0 = s.tree.x;
+            nodes = s.tree.y;
+            heat = __int_as_float(s.tree.z);
+            fine = FineScale(heat <= 0.f ? 1.f : heat);
             if (nodes <= 0) {
-                give_up(bad);
+                finish(bad, -1, -1);
                 return;
             }
-            any = s.child[0] >= 0;
+            any = s.node[0].child >= 0;
         }
         if (heat <= 0.f) {
-            int32_t best;
-            const float v = best_of(all, -INFINITY, best);
+            int32_t best = INT32_MAX;
+            float v = -INFINITY;
+            for (int32_t e = lane; e < parts; e += 32) take_better(v, best, all[e].top, __float_as_int(all[e].sum));
+            warp_best(v, best);
             if (!(v > -INFINITY && v < INFINITY)) {
-                give_up(PA_DEVERR_LOGITS);
+                finish(PA_DEVERR_LOGITS, -1, -1);
                 return;
             }
-            int32_t j = s.child[cur];
-            while (j >= 0 && s.token[j] != best) j = s.sibling[j];
+            int32_t j = s.node[cur].child;
+            while (j >= 0 && s.node[j].token != best) j = s.node[j].sibling;
             if (j < 0) {
-                if (rank == 0 && tid == 0) {
-                    a.leaf[seq] = cur;
-                    a.next[seq] = best;
-                }
+                finish(0, cur, best);
                 return;
             }
             cur = j;
+            any = s.node[cur].child >= 0;
             continue;
         }
-        const FineScale fine(heat);
-        {
-            float top = -INFINITY, dtop = -INFINITY, sum = 0.f, dsum = 0.f;
-            for (int32_t e = lane; e < parts; e += 32) {
-                top = fmaxf(top, all[e].top);
-                dtop = fmaxf(dtop, all[e].draft_top);
-            }
-            for (int off = 16; off > 0; off >>= 1) {
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                dtop = fmaxf(dtop, __shfl_xor_sync(0xffffffffu, dtop, off));
-            }
-            for (int32_t e = lane; e < parts; e += 32) {
-                const VerifyPart x = all[e];
-                sum += x.top == -INFINITY ? x.sum : x.sum * ex2_approx((x.top - top) * scale);
-                dsum += x.draft_top == -INFINITY ? x.draft_sum
-                                                 : x.draft_sum * ex2_approx((x.draft_top - dtop) * scale);
-            }
-            for (int off = 16; off > 0; off >>= 1) {
-                sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                dsum += __shfl_xor_sync(0xffffffffu, dsum, off);
-            }
-            // (NaN, an infinity, or nothing to choose from)
-            if (!(sum >= 0.5f) || (DRAFT && any && !(dsum >= 0.5f))) {
-                give_up(PA_DEVERR_LOGITS);
-                return;
-            }
-            p = VerifyRow{top, 1.f / sum};
-            q = VerifyRow{dtop, DRAFT && any ? 1.f / dsum : 0.f};
-        }
-        // the children in order
-        int32_t held = -1;
-        float rest = 1.f;
-        spent = 0.f;
-        for (int32_t j = s.child[cur]; j >= 0; j = s.sibling[j]) {
-            const int32_t t = s.token[j];
-            if (t < 0 || t >= vocab) {
-                if (rank == 0 && tid == 0) raise_error(PA_DEVERR_TREE);
-                continue;
-            }
-            float left = fine.power(s.logit[j], p.top) * p.inv, ask = s.uniform[j] * rest;
-            if (DRAFT) {
-                const float qt = fine.power(s.draft_logit[j], q.top) * q.inv;
-                left = fmaxf(fmaf(-spent, qt, left), 0.f);
-                ask *= qt;
-            } else {
-                for (int32_t k = s.child[cur]; k != j; k = s.sibling[k])      // tried before
-                    if (s.token[k] == t) left = 0.f;
-            }
-            if (ask < left) {
-                held = j;
-                break;
-            }
-            if (!DRAFT) {
-                rest = fmaxf(rest - left, 0.f);
-                continue;
-            }
-            spent += rest;
-            if (s.sibling[j] < 0) break;
-            // what is left of P
-            float sum = 0.f;
-            const float pi = p.inv, qi = spent * q.inv;
-            for (int32_t o = lo + 8 * tid; o < hi; o += 8 * kVerifyThreads) {
-                float x[8], y[8];
-                load8<E, WIDE>(row + o, hi - o, x);
-                load8<E, WIDE>(drow + o, hi - o, y);
+        // the children in order: the first warp decides, for all with its numbers
+        int32_t verdict = kVerifyNext;
+        while (true) {
+            if (warp == 0) {
+                VerifyStep step;
+                if (verdict != kVerifyRest) {
+                    // (up to four parts a lane)
+                    VerifyPart x[kVerifyMaxCluster * kVerifyWarps / 32];
+                    RowSum sx, sy;
+                    sx.start(scale);
+                    sy.start(scale);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    sum += fmaxf(ex2_approx((x[i] - p.top) * scale) * pi - ex2_approx((y[i] - q.top) * scale) * qi, 0.f);
-            }
-            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            const VerifyPart* sums = exchange(VerifyPart{0.f, sum, 0.f, 0.f});
-            rest = 0.f;
-            for (int32_t e = lane; e < parts; e += 32) rest += sums[e].sum;
-            for (int off = 16; off > 0; off >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, off);
-        }
-        if (held < 0) break;
-        cur = held;
-        any = s.child[cur] >= 0;
-    }
-
-    // the next token: the best of the rest, of P itself where rounding left nothing
-    const E* row = target + (int64_t)(q0 + cur) * a.logit_stride;
-    const E* drow = DRAFT ? draft + (int64_t)(q0 + cur) * a.draft_stride : nullptr;
-    const FineScale fine(heat);
-    for (int round = 0; round < 2; ++round) {
-        float v = 0.f;
-        int32_t best = INT32_MAX;
-        const bool rest = round == 0;
-        const float scale = fine.hi, pi = p.inv, qi = rest ? spent * q.inv : 0.f;
-        for (int32_t o = lo + 8 * tid; o < hi; o += 8 * kVerifyThreads) {
-            float x[8], y[8], e[8];
-            load8<E, WIDE>(row + o, hi - o, x);
-            load8<float, WIDE>(noise + o, hi - o, e);
-            if (DRAFT && qi != 0.f) load8<E, WIDE>(drow + o, hi - o, y);
+                    for (int u = 0; u < kVerifyMaxCluster * kVerifyWarps / 32; ++u) {
+                        x[u] = VerifyPart{kLowest, 0.f, kLowest, 0.f};
+                        if (lane + 32 * u < parts) x[u] = all[lane + 32 * u];
+                        sx.top = fmaxf(sx.top, x[u].top);
+                        sy.top = fmaxf(sy.top, x[u].draft_top);
+                    }
+                    float sum = 0.f, dsum = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                // (first about, without the exponent's second part)
-                const float up = ex2_approx((x[i] - p.top) * scale) * pi;
-                float w = up;
-                float room = up;
-                if (DRAFT && qi != 0.f) {
-                    const float down = ex2_approx((y[i] - q.top) * scale) * qi;
-                    w = up - down;
-                    room = up + down;
+                    for (int u = 0; u < kVerifyMaxCluster * kVerifyWarps / 32; ++u) {
+                        sum += x[u].sum * ex2_approx((x[u].top - sx.top) * scale);
+                        dsum += x[u].draft_sum * ex2_approx((x[u].draft_top - sy.top) * scale);
+                    }
+                    sx.sum = pack2(sum, 0.f);
+                    sy.sum = pack2(dsum, 0.f);
+                    step = VerifyStep{kVerifyNext, any ? s.node[cur].child : -1, 0.f, 0.f, 0.f, 0.f, 0.f, 1.f, 0.f};
+                    reduce_sums(sx, sy, step.top, sum, step.draft_top, dsum);
+                    step.inv = __frcp_rn(sum);
+                    step.draft_inv = DRAFT && any ? __frcp_rn(dsum) : 0.f;
+                    // (NaN, an infinity, or nothing to choose from)
+                    if (!(sum >= 0.5f) || (DRAFT && any && !(dsum >= 0.5f))) step.verdict = kVerifyDone;
+                } else {
+                    step = s.step;
+                    step.rest = 0.f;
+                    for (int32_t e = lane; e < parts; e += 32) step.rest += all[e].sum;
+                    for (int off = 16; off > 0; off >>= 1) step.rest += __shfl_xor_sync(0xffffffffu, step.rest, off);
+                    step.verdict = kVerifyNext;
                 }
-                if (o + i >= hi || !(fmaf(room, 0x1p-14f, w) * rcp_approx(e[i]) > v)) continue;
-                w = fine.power(x[i], p.top) * pi;
-                if (DRAFT && qi != 0.f) w -= fine.power(y[i], q.top) * qi;
-                w = w / e[i];
-                if (w > v) {
-                    bool out = false;
-                    if (!DRAFT && rest)
-                        for (int32_t j = s.child[cur]; j >= 0; j = s.sibling[j]) out |= s.token[j] == o + i;
-                    if (!out) {
-                        v = w;
-                        best = o + i;
+                while (step.verdict == kVerifyNext && step.node >= 0) {
+                    const int32_t j = step.node;
+                    const VerifyNode n = s.node[j];
+                    step.node = n.sibling;
+                    if (n.token < 0 || n.token >= vocab) {
+                        if (rank == 0 && lane == 0) raise_error(PA_DEVERR_TREE);
+                        continue;
+                    }
+                    const float2 l = s.logit[j];
+                    float left = fine.power(l.x, step.top) * step.inv, ask = n.uniform * step.rest;
+                    if (DRAFT) {
+                        const float qt = fine.power(l.y, step.draft_top) * step.draft_inv;
+                        left = fmaxf(fmaf(-step.spent, qt, left), 0.f);
+                        ask *= qt;
+                    } else {
+                        for (int32_t k = s.node[cur].child; k != j; k = s.node[k].sibling)   // tried before
+                            if (s.node[k].token == n.token) left = 0.f;
+                    }
+                    if (ask < left) {
+                        step.verdict = kVerifyHolds;
+                        step.node = j;
+                    } else if (DRAFT) {
+                        step.spent += step.rest;
+                        if (step.node >= 0) step.verdict = kVerifyRest;
+                    } else {
+                        step.rest = fmaxf(step.rest - left, 0.f);
                     }
                 }
+                __syncwarp();
+                if (lane == 0) s.step = step;
+            }
+            __syncthreads();
+            verdict = s.step.verdict;
+            if (!DRAFT || verdict != kVerifyRest) break;
+            // what is left of P
+            float sum = 0.f;
+            const float top = s.step.top, draft_top = s.step.draft_top, inv = s.step.inv;
+            const float share = s.step.spent * s.step.draft_inv;
+            for (int32_t o = lo + 8 * tid; o < hi; o += 8 * kVerifyThreads) {
+                Octet<E, WIDE> x, y;
+                float up[8], down[8];
+                x.load(row + o, hi - o);
+                y.load(drow + o, hi - o);
+                x.powers(top, scale, up);
+                y.powers(draft_top, scale, down);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum += fmaxf(fmaf(down[i], -share, up[i] * inv), 0.f);
+            }
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            all = exchange(VerifyPart{0.f, sum, 0.f, 0.f});
+        }
+        if (verdict == kVerifyDone) {
+            finish(PA_DEVERR_LOGITS, -1, -1);
+            return;
+        }
+        if (verdict != kVerifyHolds) break;
+        cur = s.step.node;
+        any = s.node[cur].child >= 0;
+    }
+
+    // the next token: of the rest, or of P itself where rounding left none
+    RaceField<E, DRAFT, WIDE> field{target + (int64_t)(q0 + cur) * a.logit_stride,
+                                    DRAFT ? draft + (int64_t)(q0 + cur) * a.draft_stride : nullptr,
+                                    noise, s.node, fine, s.step.top, s.step.draft_top,
+                                    s.step.spent * s.step.draft_inv / s.step.inv, lo, hi,
+                                    any ? s.node[cur].child : -1};
+    bool finely = false;
+    while (true) {
+        Race best = finely ? field.run_finely(s.step.floor) : field.run();
+        best.reduce();
+        // the warps' best
+        const VerifyPart* all = exchange(VerifyPart{best.first, __int_as_float(best.index), best.second, best.least});
+        if (warp == 0) {
+            best.start();
+            for (int32_t e = lane; e < parts; e += 32) {
+                const VerifyPart x = all[e];
+                best.join(Race{x.top, x.draft_sum, x.draft_top, __float_as_int(x.sum)});
+            }
+            best.reduce();
+            // all have it
+            if (lane == 0) {
+                s.step.node = best.index;
+                s.step.floor = fmaxf(best.least, 0x1p-149f);
+                s.step.verdict = best.index == INT32_MAX ? kVerifyRest
+                                 : !finely && best.second >= best.least ? kVerifyFinely
+                                                                        : kVerifyDone;
             }
         }
-        warp_best(v, best);
-        const VerifyPart* all = exchange(VerifyPart{v, __int_as_float(best), 0.f, 0.f});
-        best_of(all, 0.f, best);
-        if (best != INT32_MAX || round == 1) {
-            if (rank == 0 && tid == 0) {
-                const bool none = best == INT32_MAX;
-                if (none) raise_error(PA_DEVERR_LOGITS);
-                a.leaf[seq] = none ? -1 : cur;
-                a.next[seq] = none ? -1 : best;
-            }
+        __syncthreads();
+        const int32_t verdict = s.step.verdict;
+        if (verdict == kVerifyDone) {
+            finish(0, cur, s.step.node);
             return;
+        }
+        finely = verdict == kVerifyFinely;
+        if (!finely) {
+            if (field.share == 0.f && field.child < 0) {
+                finish(PA_DEVERR_LOGITS, -1, -1);
+                return;
+            }
+            field.share = 0.f;
+            field.child = -1;
         }
     }
 }
