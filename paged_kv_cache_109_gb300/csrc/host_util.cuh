@@ -101,5 +101,39 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return a && b && na && nb && x < y + nb && y < x + na;
 }
 
+// The same checks of one call, the current device asked for once.
+struct CallDevice {
+    int id = -1;
+    CallDevice() {
+        if (cudaGetDevice(&id) != cudaSuccess) {
+            cudaGetLastError();
+            id = -1;
+        }
+    }
+    bool attributes(const void* p, cudaPointerAttributes& at) const {
+        if (id >= 0 && cudaPointerGetAttributes(&at, p) == cudaSuccess) return true;
+        cudaGetLastError();
+        return false;
+    }
+    // map_current_arg, current_device_memory
+    template <typename T>
+    bool map(T*& p) const {
+        cudaPointerAttributes at;
+        if (!p) return true;
+        if (!attributes(p, at)) return false;
+        if (at.type == cudaMemoryTypeDevice) return at.device == id;
+        if (at.type == cudaMemoryTypeHost && at.devicePointer) {
+            p = static_cast<T*>(at.devicePointer);
+            return true;
+        }
+        return at.type == cudaMemoryTypeManaged;
+    }
+    bool memory(const void* p) const {
+        cudaPointerAttributes at;
+        return p && attributes(p, at) &&
+               (at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == id));
+    }
+};
+
 }  // namespace
 }  // namespace pa

@@ -8,8 +8,9 @@
 // the queue needs no other end and what was used last is taken first.
 //
 // Both number a list of table entries (those dropped, those shared) over all sequences
-// and give equal shares of it to the CTAs of one cluster.  A CTA keeps the running
-// sums of a round of sequences in shared memory and finds an entry's sequence there.
+// and give equal shares of it to the warps of one cluster.  A CTA keeps the running
+// sums of a round of sequences in shared memory; a warp finds the sequences of its
+// first and last of 256 entries there together, its lanes those in between.
 //
 // Release with reference counts: every dropped entry takes one off its block's count.
 // A block that reaches none is freed once, at its last entry e in the list's order:
@@ -34,6 +35,7 @@ struct ReleaseArgs {
     int32_t* blocks_held_out;       // may be blocks_held
     int32_t* free_head_out;         // may be free_head
     int32_t num_seqs, num_free, num_blocks, block_size, max_blocks;
+    int32_t kept;                   // entries that a CTA has room to keep
 };
 
 struct ForkArgs {
@@ -52,25 +54,32 @@ struct ForkArgs {
 };
 
 constexpr int kPoolThreads = 1024;
+constexpr int kPoolWarps = kPoolThreads / 32;
 constexpr int kPoolPer = 4;                             // sequences a thread scans
 constexpr int kPoolRound = kPoolThreads * kPoolPer;     // sequences of a round
-constexpr int kPoolMaxCluster = 8;
+constexpr int kPoolMaxCluster = 16;
+constexpr int kPoolMaxWarps = kPoolMaxCluster * kPoolWarps;
+constexpr int kPoolKept = 40960;                        // entries that a CTA keeps at most (160 KB)
+constexpr int kPoolChunk = 8, kForkChunk = 4;           // entries a lane has under way
 
 struct PoolShared {
     int32_t start[kPoolRound + 1];  // running sum of the entries, from the round's first
     int32_t first[kPoolRound];      // release: a sequence's first entry; fork: its source
-    int64_t warp_a[32], warp_b[32];
-    unsigned int bad;
-    int64_t from_cta[2][kPoolMaxCluster];
+    int64_t warp_a[kPoolWarps], warp_b[kPoolWarps];
+    int32_t count[kPoolMaxWarps];   // freed blocks, by warp of the cluster
+    unsigned int bad[kPoolMaxCluster];
+    int32_t head;                   // the queue's front, from the first CTA
 };
 
-// Exclusive running sums of two values over the CTA's threads; the totals too.
+// Exclusive running sums of one or two values over the CTA's threads; the totals too.
+template <bool TWO>
 __device__ __forceinline__ void pool_scan(PoolShared& s, int64_t& a, int64_t& b, int64_t& sum_a,
                                           int64_t& sum_b) {
     const int32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t a0 = a, b0 = b;
     for (int off = 1; off < 32; off <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, a, off), y = __shfl_up_sync(0xffffffffu, b, off);
+        const int64_t x = __shfl_up_sync(0xffffffffu, a, off);
+        const int64_t y = TWO ? __shfl_up_sync(0xffffffffu, b, off) : 0;
         if (lane >= off) {
             a += x;
             b += y;
@@ -79,44 +88,70 @@ __device__ __forceinline__ void pool_scan(PoolShared& s, int64_t& a, int64_t& b,
     __syncthreads();
     if (lane == 31) {
         s.warp_a[warp] = a;
-        s.warp_b[warp] = b;
+        if (TWO) s.warp_b[warp] = b;
     }
     __syncthreads();
-    int64_t wa = s.warp_a[lane], wb = s.warp_b[lane];
+    int64_t wa = s.warp_a[lane], wb = TWO ? s.warp_b[lane] : 0;
     for (int off = 1; off < 32; off <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, wa, off), y = __shfl_up_sync(0xffffffffu, wb, off);
+        const int64_t x = __shfl_up_sync(0xffffffffu, wa, off);
+        const int64_t y = TWO ? __shfl_up_sync(0xffffffffu, wb, off) : 0;
         if (lane >= off) {
             wa += x;
             wb += y;
         }
     }
     sum_a = __shfl_sync(0xffffffffu, wa, 31);
-    sum_b = __shfl_sync(0xffffffffu, wb, 31);
     const int64_t ca = __shfl_sync(0xffffffffu, wa, max(warp - 1, 0));
-    const int64_t cb = __shfl_sync(0xffffffffu, wb, max(warp - 1, 0));
     a += (warp ? ca : 0) - a0;
-    b += (warp ? cb : 0) - b0;
+    if (TWO) {
+        sum_b = __shfl_sync(0xffffffffu, wb, 31);
+        const int64_t cb = __shfl_sync(0xffffffffu, wb, max(warp - 1, 0));
+        b += (warp ? cb : 0) - b0;
+    }
 }
 
-// x of every CTA of the cluster, by rank (turn: 0 and 1 in turn).
-__device__ __forceinline__ const int64_t* pool_exchange(PoolShared& s, int32_t turn, int64_t x) {
-    const uint32_t rank = cluster_rank(), ctas = cluster_size();
-    if (threadIdx.x < ctas)
-        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(
-                         cluster_map(&s.from_cta[turn & 1][rank], threadIdx.x)), "l"(x)
-                     : "memory");
-    cluster_sync();
-    return s.from_cta[turn & 1];
+// The warp's word (a count, a CTA's bad bits) to every CTA of the cluster.
+__device__ __forceinline__ void pool_tell(const void* at, int32_t x) {
+    if ((threadIdx.x & 31) < cluster_size()) cluster_store(cluster_map(at, threadIdx.x & 31), x);
 }
 
-// Sequence of entry e of the round (s.start[0] <= e < s.start[n]).
-__device__ __forceinline__ int32_t pool_find(const PoolShared& s, int32_t n, int32_t e) {
-    int32_t lo = 0, hi = n - 1;
+// Last i in [lo, hi] with start[i] <= e (start[lo] <= e), all lanes of a warp with one e.
+__device__ __forceinline__ int32_t pool_find_warp(const int32_t* start, int32_t lo, int32_t hi, int32_t e) {
     while (lo < hi) {
-        const int32_t mid = (lo + hi + 1) / 2;
-        if (s.start[mid] <= e) lo = mid; else hi = mid - 1;
+        const int32_t step = (hi - lo + 32) / 32;
+        const int32_t at = lo + ((int32_t)(threadIdx.x & 31) + 1) * step;
+        const uint32_t yes = __ballot_sync(0xffffffffu, at <= hi && start[min(at, hi)] <= e);
+        lo += __popc(yes) * step;
+        hi = min(hi, lo + step - 1);
     }
     return lo;
+}
+
+// The sequences of entries e0 + 32 u + lane of a round, below `end` (-1: none).
+template <int CHUNK>
+__device__ __forceinline__ void pool_seqs(const PoolShared& s, int32_t e0, int32_t end,
+                                          int32_t (&seq)[CHUNK]) {
+    const int32_t lane = threadIdx.x & 31;
+    const int32_t last = min(end, e0 + 32 * CHUNK) - 1;
+    const int32_t lo = pool_find_warp(s.start, 0, kPoolRound - 1, e0);
+    const int32_t hi = s.start[lo + 1] > last ? lo : pool_find_warp(s.start, lo, kPoolRound - 1, last);
+    int32_t top[CHUNK];
+#pragma unroll
+    for (int u = 0; u < CHUNK; ++u) {
+        seq[u] = lo;
+        top[u] = hi;
+    }
+    // (a lane's searches go on side by side)
+    for (int32_t left = hi - lo; left > 0; left >>= 1) {
+#pragma unroll
+        for (int u = 0; u < CHUNK; ++u) {
+            const int32_t mid = (seq[u] + top[u] + 1) / 2;
+            if (s.start[mid] <= e0 + 32 * u + lane) seq[u] = mid; else top[u] = mid - 1;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < CHUNK; ++u)
+        if (e0 + 32 * u + lane >= end) seq[u] = -1;
 }
 
 // ---- release -------------------------------------------------------------------------
@@ -135,7 +170,7 @@ __device__ __forceinline__ ReleaseSeq release_seq(const ReleaseArgs& a, int32_t 
     return {(int32_t)keep, held};
 }
 
-// The round's entries into s.start and s.first; their number and how many there are.
+// The round's entries into s.start and s.first; how many there are.
 __device__ __forceinline__ int64_t release_round(PoolShared& s, const ReleaseArgs& a, int32_t i0,
                                                  unsigned int& bad) {
     ReleaseSeq q[kPoolPer];
@@ -147,7 +182,7 @@ __device__ __forceinline__ int64_t release_round(PoolShared& s, const ReleaseArg
         if (i < a.num_seqs) q[u] = release_seq(a, i, bad);
         mine += q[u].held - q[u].keep;
     }
-    pool_scan(s, mine, none, total, ignored);
+    pool_scan<false>(s, mine, none, total, ignored);
 #pragma unroll
     for (int u = 0; u < kPoolPer; ++u) {
         const int32_t x = (int32_t)threadIdx.x * kPoolPer + u;
@@ -160,127 +195,154 @@ __device__ __forceinline__ int64_t release_round(PoolShared& s, const ReleaseArg
     return total;
 }
 
+template <bool COUNTED>
 __global__ void __launch_bounds__(kPoolThreads) release_blocks_kernel(const ReleaseArgs a) {
+    extern __shared__ int32_t s_ids[];  // [a.kept]: the CTA's entries, where they fit
     __shared__ PoolShared s;
     griddep_wait();
     griddep_launch_dependents();
-    const int32_t tid = threadIdx.x;
+    cluster_arrive();                   // this CTA runs
+    const int32_t tid = threadIdx.x, lane = tid & 31;
     const int32_t rank = (int32_t)cluster_rank(), ctas = (int32_t)cluster_size();
-    const int32_t head = *a.free_head;
+    const int32_t warp = rank * kPoolWarps + (tid >> 5), warps = ctas * kPoolWarps;   // of the cluster
+    int32_t head = *a.free_head;
     const int32_t rounds = (a.num_seqs + kPoolRound - 1) / kPoolRound;
     unsigned int bad = 0;
     int64_t total = 0;
-    if (tid == 0) s.bad = 0;
     for (int32_t r = 0; r < rounds; ++r) total += release_round(s, a, r * kPoolRound, bad);
-    __syncthreads();
-    if (bad) atomicOr(&s.bad, bad);
-    __syncthreads();
-    bad = s.bad;
+    bad = __syncthreads_or(bad) ? PA_DEVERR_SEQ_LEN : 0;
     if (head < 0 || head > a.num_free) bad |= PA_DEVERR_POOL;
     if (total > INT32_MAX / 2) bad |= PA_DEVERR_SEQ_LEN;
-    cluster_sync();                     // all CTAs run
-    int32_t turn = 0;
-    // (the first CTA's word goes, whatever happens to the inputs meanwhile)
-    bad = (unsigned int)pool_exchange(s, turn++, bad)[0];
+    const bool off = bad != 0;          // (as this CTA sees it)
 
-    // Entries [e0, e1) of the list are this CTA's: f(e, id, there) for each, tiles of
-    // the CTA in order (there: this thread has one, with a valid id).
-    const int64_t per = (total + ctas - 1) / ctas;
-    const int64_t e0 = min(total, rank * per), e1 = min(total, e0 + per);
+    // Entries [e0, e1) of the list are this warp's: f(e, id, in) for 32 at a time, in
+    // order, all lanes together (in: the lane has one; id: -1 for none or a bad one).
+    const int64_t per = (((total + warps - 1) / warps) + 31) / 32 * 32;
+    const int64_t e0 = min(total, warp * per), e1 = off ? e0 : min(total, e0 + per);
+    const bool keep = per * kPoolWarps <= a.kept;
+    int32_t* const ids = s_ids + (keep ? (tid >> 5) * per : 0);
+    bool have = false;
     auto each = [&](auto f) {
         int64_t base = 0;
         for (int32_t r = 0; r < rounds; ++r) {
             unsigned int ignored = 0;
-            if (rounds > 1) {
+            if (rounds > 1 && !(keep && have)) {
                 __syncthreads();
                 release_round(s, a, r * kPoolRound, ignored);
             }
-            const int64_t n = s.start[kPoolRound];
-            const int64_t end = min(base + n, e1);
-            for (int64_t t = max(base, e0); t < end; t += kPoolThreads) {
-                const int64_t e = t + tid;
-                int32_t id = -1;
-                if (e < end) {
-                    const int32_t x = (int32_t)(e - base), i = pool_find(s, kPoolRound, x);
-                    id = a.block_tables[(int64_t)(r * kPoolRound + i) * a.max_blocks + s.first[i] + (x - s.start[i])];
+            const bool again = keep && have;
+            if (again && r > 0) break;  // (all rounds at once)
+            const int64_t n = again ? total : s.start[kPoolRound], end = min(base + n, e1);
+            for (int64_t t = max(base, e0); t < end; t += 32 * kPoolChunk) {
+                int32_t id[kPoolChunk];
+                if (again) {
+#pragma unroll
+                    for (int u = 0; u < kPoolChunk; ++u)
+                        id[u] = t + 32 * u + lane < end ? ids[t - e0 + 32 * u + lane] : -1;
+                } else {
+                    int32_t seq[kPoolChunk];
+                    pool_seqs(s, (int32_t)(t - base), (int32_t)(end - base), seq);
+#pragma unroll
+                    for (int u = 0; u < kPoolChunk; ++u) {
+                        const int32_t x = (int32_t)(t - base) + 32 * u + lane;
+                        id[u] = -1;
+                        if (seq[u] >= 0)
+                            id[u] = a.block_tables[(int64_t)(r * kPoolRound + seq[u]) * a.max_blocks +
+                                                   s.first[seq[u]] + (x - s.start[seq[u]])];
+                    }
+#pragma unroll
+                    for (int u = 0; u < kPoolChunk; ++u)
+                        if (keep && seq[u] >= 0) ids[t - e0 + 32 * u + lane] = id[u];
                 }
-                f((int32_t)e, id, e < end && id >= 0 && id < a.num_blocks, e < end);
+#pragma unroll
+                for (int u = 0; u < kPoolChunk; ++u) {
+                    const int64_t e = t + 32 * u + lane;
+                    if (t + 32 * u >= end) break;
+                    const bool there = e < end && id[u] >= 0 && id[u] < a.num_blocks;
+                    f((int32_t)e, there ? id[u] : -1, e < end);
+                }
             }
             base += n;
         }
+        have = true;
     };
     auto undo = [&]() {
-        each([&](int32_t, int32_t id, bool there, bool) {
-            if (there) atomicAdd(&a.ref_cnt[id], 1);
+        each([&](int32_t, int32_t id, bool) {
+            if (id >= 0) atomicAdd(&a.ref_cnt[id], 1);
         });
     };
-    int64_t freed = 0;
-    if (bad == 0 && a.ref_cnt != nullptr) {
+    cluster_wait();                     // all CTAs run: their shared memory is there
+    if constexpr (COUNTED) {
         unsigned int over = 0;
-        each([&](int32_t, int32_t id, bool there, bool) {
-            if (there && atomicSub(&a.ref_cnt[id], 1) <= 0) over = PA_DEVERR_SHARED;
+        each([&](int32_t, int32_t id, bool) {
+            if (id >= 0 && atomicSub(&a.ref_cnt[id], 1) <= 0) over = PA_DEVERR_SHARED;
         });
-        over = __syncthreads_or(over) ? PA_DEVERR_SHARED : 0;
-        const int64_t* all = pool_exchange(s, turn++, over);
-        for (int32_t c = 0; c < ctas; ++c) bad |= (unsigned int)all[c];
-        if (bad) {
+        bad |= __syncthreads_or(over) ? PA_DEVERR_SHARED : 0;
+        if (tid < 32) pool_tell(&s.bad[rank], (int32_t)bad);
+        if (rank == 0 && tid < 32) pool_tell(&s.head, head);
+        cluster_sync();
+        for (int32_t c = 0; c < ctas; ++c) bad |= s.bad[c];
+        if (bad)
             undo();
-        } else {
-            each([&](int32_t e, int32_t id, bool there, bool) {
-                if (there && __ldcg(&a.ref_cnt[id]) <= 0) atomicMin(&a.ref_cnt[id], -1 - e);
+        else
+            each([&](int32_t e, int32_t id, bool) {
+                if (id >= 0 && __ldcg(&a.ref_cnt[id]) <= 0) atomicMin(&a.ref_cnt[id], -1 - e);
             });
-        }
         cluster_sync();
     }
-    auto owns = [&](int32_t e, int32_t id, bool there) {
-        return there && (a.ref_cnt == nullptr || __ldcg(&a.ref_cnt[id]) == -1 - e);
+    auto owns = [&](int32_t e, int32_t id) {
+        return id >= 0 && (!COUNTED || __ldcg(&a.ref_cnt[id]) == -1 - e);
     };
-    if (bad == 0) {
-        int32_t mine = 0;
-        each([&](int32_t e, int32_t id, bool there, bool in) {
-            if (in && !there) raise_error(PA_DEVERR_TABLE_ENTRY);
-            mine += owns(e, id, there);
+    int32_t mine = 0;
+    if (bad == 0)
+        each([&](int32_t e, int32_t id, bool in) {
+            if (in && id < 0) raise_error(PA_DEVERR_TABLE_ENTRY);
+            mine += __popc(__ballot_sync(0xffffffffu, owns(e, id)));
         });
-        int64_t x = mine, none = 0, sum, ignored;
-        pool_scan(s, x, none, sum, ignored);
-        const int64_t* all = pool_exchange(s, turn++, sum);
-        int64_t before = 0;
-        for (int32_t c = 0; c < ctas; ++c) {
-            if (c < rank) before += all[c];
-            freed += all[c];
-        }
-        if (freed > head) {
-            bad = PA_DEVERR_POOL;
-            if (a.ref_cnt != nullptr) {
-                each([&](int32_t e, int32_t id, bool there, bool) {
-                    if (owns(e, id, there)) a.ref_cnt[id] = 0;
-                });
-                cluster_sync();
-                undo();
-            }
-            freed = 0;
-        } else {
-            int64_t at = head - freed + before;
-            each([&](int32_t e, int32_t id, bool there, bool) {
-                const bool own = owns(e, id, there);
-                int64_t rank_in = own, zero = 0, got, none2;
-                pool_scan(s, rank_in, zero, got, none2);
-                if (own) {
-                    a.free_blocks[at + rank_in] = id;
-                    if (a.ref_cnt != nullptr) a.ref_cnt[id] = 0;
-                }
-                at += got;
+    pool_tell(&s.count[warp], mine);
+    if (!COUNTED && tid < 32) pool_tell(&s.bad[rank], (int32_t)bad);
+    if (!COUNTED && rank == 0 && tid < 32) pool_tell(&s.head, head);
+    cluster_sync();
+    head = s.head;                      // (all CTAs decide by the same numbers)
+    if (!COUNTED)
+        for (int32_t c = 0; c < ctas; ++c) bad |= s.bad[c];
+    int32_t freed = 0, before = 0;
+    for (int32_t w = lane; w < warps; w += 32) {
+        const int32_t n = s.count[w];
+        freed += n;
+        before += w < warp ? n : 0;
+    }
+    freed = __reduce_add_sync(0xffffffffu, freed);
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (bad == 0 && freed > head) {
+        bad = PA_DEVERR_POOL;
+        if constexpr (COUNTED) {
+            each([&](int32_t e, int32_t id, bool) {
+                if (owns(e, id)) a.ref_cnt[id] = 0;
             });
+            cluster_sync();
+            undo();
         }
+    } else if (bad == 0) {
+        int32_t at = head - freed + before;
+        each([&](int32_t e, int32_t id, bool) {
+            const bool own = owns(e, id);
+            const uint32_t mask = __ballot_sync(0xffffffffu, own);
+            if (own) {
+                a.free_blocks[at + __popc(mask & ((1u << lane) - 1))] = id;
+                if (COUNTED) a.ref_cnt[id] = 0;
+            }
+            at += __popc(mask);
+        });
     }
     if (rank == 0 && tid == 0 && bad) raise_error(bad);
-    cluster_sync();                     // the inputs have been read: they may be the outputs
+    if (rounds > 1) cluster_sync();     // the inputs have been read: they may be the outputs
     for (int32_t i = rank * kPoolThreads + tid; i < a.num_seqs; i += ctas * kPoolThreads) {
         unsigned int ignored = 0;
         const int32_t held = a.blocks_held[i];
         a.blocks_held_out[i] = bad ? held : release_seq(a, i, ignored).keep;
     }
-    if (rank == 0 && tid == 0) *a.free_head_out = head - (int32_t)freed;
+    if (rank == 0 && tid == 0) *a.free_head_out = head - (bad ? 0 : freed);
 }
 
 // ---- fork ------------------------------------------------------------------------------
@@ -306,8 +368,8 @@ __device__ __forceinline__ ForkSeq fork_seq(const ForkArgs& a, int32_t i, unsign
     return {p, len, len / a.block_size, len % a.block_size != 0};
 }
 
-// The round's shared entries into s; their number, and the fresh blocks before each
-// of this thread's sequences in `take`.
+// The round's shared entries into s; how many there are, and the fresh blocks before
+// this thread's first sequence in `take`.
 __device__ __forceinline__ int64_t fork_round(PoolShared& s, const ForkArgs& a, int32_t i0,
                                               unsigned int& bad, ForkSeq (&q)[kPoolPer],
                                               int64_t& take, int64_t& fresh) {
@@ -321,7 +383,7 @@ __device__ __forceinline__ int64_t fork_round(PoolShared& s, const ForkArgs& a, 
         mine += q[u].full;
         take += q[u].tail;
     }
-    pool_scan(s, mine, take, total, fresh);
+    pool_scan<true>(s, mine, take, total, fresh);
 #pragma unroll
     for (int u = 0; u < kPoolPer; ++u) {
         const int32_t x = (int32_t)threadIdx.x * kPoolPer + u;
@@ -334,34 +396,45 @@ __device__ __forceinline__ int64_t fork_round(PoolShared& s, const ForkArgs& a, 
     return total;
 }
 
+// (Every CTA finds out by itself whether the call can be done, and its one cluster
+// barrier is met on every path.)
 __global__ void __launch_bounds__(kPoolThreads) fork_blocks_kernel(const ForkArgs a) {
     __shared__ PoolShared s;
     griddep_wait();
     griddep_launch_dependents();
-    const int32_t tid = threadIdx.x;
+    const int32_t tid = threadIdx.x, lane = tid & 31;
     const int32_t rank = (int32_t)cluster_rank(), ctas = (int32_t)cluster_size();
+    const int32_t warp = rank * kPoolWarps + (tid >> 5), warps = ctas * kPoolWarps;   // of the cluster
     const int32_t head = *a.free_head;
     const int32_t rounds = (a.num_seqs + kPoolRound - 1) / kPoolRound;
     unsigned int bad = 0;
-    int64_t total = 0, fresh = 0, take, more;
+    int64_t total = 0, fresh = 0, take = 0, more = 0;
     ForkSeq q[kPoolPer];
-    if (tid == 0) s.bad = 0;
     for (int32_t r = 0; r < rounds; ++r) {
         total += fork_round(s, a, r * kPoolRound, bad, q, take, more);
         fresh += more;
     }
-    __syncthreads();
-    if (bad) atomicOr(&s.bad, bad);
-    __syncthreads();
-    bad = s.bad;
+    bad = (__syncthreads_or(bad & PA_DEVERR_FORK) ? PA_DEVERR_FORK : 0) |
+          (__syncthreads_or(bad & PA_DEVERR_SEQ_LEN) ? PA_DEVERR_SEQ_LEN : 0);
     if (bad == 0 && (head < 0 || head + fresh > a.num_free)) bad = PA_DEVERR_POOL;
     if (bad == 0 && total > INT32_MAX / 2) bad = PA_DEVERR_SEQ_LEN;
-    cluster_sync();                     // all CTAs run
-    bad = (unsigned int)pool_exchange(s, 0, bad)[0];
     if (bad && rank == 0 && tid == 0) raise_error(bad);
+    // (what a row becomes is read before any output is written: they may be the inputs)
+    auto becomes = [&](int32_t i, int32_t& len, int32_t& held) {
+        const int32_t p = a.src[i];
+        const int32_t from = bad || p < 0 ? i : p;
+        len = a.seq_lens[from];
+        held = from == i ? a.blocks_held[i] : (int32_t)(((int64_t)len + a.block_size - 1) / a.block_size);
+    };
+    const int32_t own = rank * kPoolThreads + tid;
+    int32_t len0 = 0, held0 = 0;
+    if (rounds <= 1) {
+        if (own < a.num_seqs) becomes(own, len0, held0);
+        cluster_arrive();
+    }
 
-    const int64_t per = (total + ctas - 1) / ctas;
-    const int64_t e0 = min(total, rank * per), e1 = min(total, e0 + per);
+    const int64_t per = (((total + warps - 1) / warps) + 31) / 32 * 32;
+    const int64_t e0 = min(total, warp * per), e1 = min(total, e0 + per);
     int64_t base = 0, taken = 0;
     for (int32_t r = 0; r < rounds; ++r) {
         unsigned int ignored = 0;
@@ -370,54 +443,70 @@ __global__ void __launch_bounds__(kPoolThreads) fork_blocks_kernel(const ForkArg
             fork_round(s, a, r * kPoolRound, ignored, q, take, more);
         }
         const int64_t n = s.start[kPoolRound], end = bad ? 0 : min(base + n, e1);
-        // shared entries
-        for (int64_t e = max(base, e0) + tid; e < end; e += kPoolThreads) {
-            const int32_t x = (int32_t)(e - base), i = pool_find(s, kPoolRound, x);
-            const int32_t b = x - s.start[i];
-            const int32_t id = a.block_tables[(int64_t)s.first[i] * a.max_blocks + b];
-            a.block_tables[(int64_t)(r * kPoolRound + i) * a.max_blocks + b] = id;
-            if (id >= 0 && id < a.num_blocks)
-                atomicAdd(&a.ref_cnt[id], 1);
-            else
-                raise_error(PA_DEVERR_TABLE_ENTRY);
-        }
-        // tails, lengths
+        // tails
         if (rank == 0) {
             int64_t at = head + taken + take;
+            int32_t old[kPoolPer], id[kPoolPer];
+#pragma unroll
+            for (int u = 0; u < kPoolPer; ++u) {
+                old[u] = id[u] = -1;
+                if (!bad && q[u].tail) {
+                    old[u] = a.block_tables[(int64_t)q[u].src * a.max_blocks + q[u].full];
+                    id[u] = a.free_blocks[at++];
+                }
+            }
 #pragma unroll
             for (int u = 0; u < kPoolPer; ++u) {
                 const int32_t i = r * kPoolRound + tid * kPoolPer + u;
                 if (i >= a.num_seqs) continue;
                 int64_t from = -1, to = -1;
                 if (!bad && q[u].tail) {
-                    const int32_t old = a.block_tables[(int64_t)q[u].src * a.max_blocks + q[u].full];
-                    int32_t id = a.free_blocks[at++];
-                    const bool ok = id >= 0 && id < a.num_blocks;
-                    if (!ok) id = -1;
-                    a.block_tables[(int64_t)i * a.max_blocks + q[u].full] = id;
-                    if (ok) a.ref_cnt[id] = 1;
-                    if (!ok || old < 0 || old >= a.num_blocks) {
+                    const bool ok = id[u] >= 0 && id[u] < a.num_blocks;
+                    a.block_tables[(int64_t)i * a.max_blocks + q[u].full] = ok ? id[u] : -1;
+                    if (ok) a.ref_cnt[id[u]] = 1;
+                    if (!ok || old[u] < 0 || old[u] >= a.num_blocks) {
                         raise_error(PA_DEVERR_TABLE_ENTRY);
                     } else {
-                        from = old;
-                        to = id;
+                        from = old[u];
+                        to = id[u];
                     }
                 }
                 a.block_pairs[2 * (int64_t)i] = from;
                 a.block_pairs[2 * (int64_t)i + 1] = to;
             }
         }
+        // shared entries
+        for (int64_t t = max(base, e0); t < end; t += 32 * kForkChunk) {
+            int32_t seq[kForkChunk], id[kForkChunk];
+            pool_seqs(s, (int32_t)(t - base), (int32_t)(end - base), seq);
+#pragma unroll
+            for (int u = 0; u < kForkChunk; ++u) {
+                const int32_t x = (int32_t)(t - base) + 32 * u + lane;
+                if (seq[u] >= 0)
+                    id[u] = a.block_tables[(int64_t)s.first[seq[u]] * a.max_blocks + x - s.start[seq[u]]];
+            }
+#pragma unroll
+            for (int u = 0; u < kForkChunk; ++u) {
+                const int32_t x = (int32_t)(t - base) + 32 * u + lane;
+                if (seq[u] < 0) continue;
+                a.block_tables[(int64_t)(r * kPoolRound + seq[u]) * a.max_blocks + x - s.start[seq[u]]] = id[u];
+                if (id[u] >= 0 && id[u] < a.num_blocks)
+                    atomicAdd(&a.ref_cnt[id[u]], 1);
+                else
+                    raise_error(PA_DEVERR_TABLE_ENTRY);
+            }
+        }
         base += n;
         taken += more;
     }
-    cluster_sync();                     // the inputs have been read: they may be the outputs
-    // (a source's row is no fork, so nobody writes the length read here)
-    for (int32_t i = rank * kPoolThreads + tid; i < a.num_seqs; i += ctas * kPoolThreads) {
-        const int32_t p = a.src[i];
-        const int32_t from = bad || p < 0 ? i : p;
-        const int32_t len = a.seq_lens[from];
-        const int32_t held = from == i ? a.blocks_held[i]
-                                       : (int32_t)(((int64_t)len + a.block_size - 1) / a.block_size);
+    if (rounds <= 1)
+        cluster_wait();
+    else
+        cluster_sync();
+    // (a source's row is no fork, so its length stays what it is)
+    for (int32_t i = own; i < a.num_seqs; i += ctas * kPoolThreads) {
+        int32_t len = len0, held = held0;
+        if (rounds > 1 || i != own) becomes(i, len, held);
         a.seq_lens_out[i] = len;
         a.blocks_held_out[i] = held;
     }
@@ -429,6 +518,7 @@ __global__ void __launch_bounds__(kPoolThreads) fork_blocks_kernel(const ForkArg
 // layer, K or V).
 constexpr int kForkThreads = 128;
 constexpr int kForkLayers = 128;    // layers of one launch
+constexpr int kForkUnroll = 4;
 
 template <int LAYERS>
 struct ForkCaches {
@@ -444,18 +534,36 @@ fork_copy_kernel(const ForkArgs a, int32_t num_kv_heads, int32_t row_bytes,
     griddep_wait();
     griddep_launch_dependents();
     const int32_t i = blockIdx.x;
-    const int64_t from = a.block_pairs[2 * (int64_t)i], to = a.block_pairs[2 * (int64_t)i + 1];
-    if (from < 0 || to < 0) return;
+    const int64_t src = a.block_pairs[2 * (int64_t)i], dst = a.block_pairs[2 * (int64_t)i + 1];
+    if (src < 0 || dst < 0) return;
     const int32_t rows = a.seq_lens_out[i] % a.block_size;
     uint8_t* cache = (blockIdx.y & 1) ? caches.v[blockIdx.y >> 1] : caches.k[blockIdx.y >> 1];
     const int64_t head_bytes = (int64_t)a.block_size * row_bytes;
     const int64_t block_bytes = num_kv_heads * head_bytes;
-    const int32_t vecs = (int32_t)((int64_t)rows * row_bytes / VEC);      // of one head
-    for (int64_t x = threadIdx.x; x < (int64_t)num_kv_heads * vecs; x += kForkThreads) {
-        const int64_t h = x / vecs, c = x - h * vecs;
-        const int64_t off = h * head_bytes + c * VEC;
-        *reinterpret_cast<V*>(cache + to * block_bytes + off) =
-            *reinterpret_cast<const V*>(cache + from * block_bytes + off);
+    const uint8_t* from = cache + src * block_bytes;
+    uint8_t* to = cache + dst * block_bytes;
+    const int64_t vecs = (int64_t)rows * row_bytes / VEC;        // of one head
+    const int64_t total = num_kv_heads * vecs;
+    if (total <= INT32_MAX / 2) {
+        const uint32_t per = (uint32_t)vecs, all = (uint32_t)total;
+        for (uint32_t x0 = threadIdx.x; x0 < all; x0 += kForkUnroll * kForkThreads) {
+            V buf[kForkUnroll];
+            int64_t off[kForkUnroll];
+#pragma unroll
+            for (int u = 0; u < kForkUnroll; ++u) {
+                const uint32_t x = x0 + u * kForkThreads, h = x / per;
+                off[u] = h * head_bytes + (int64_t)(x - h * per) * VEC;
+                if (x < all) buf[u] = *reinterpret_cast<const V*>(from + off[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kForkUnroll; ++u)
+                if (x0 + u * kForkThreads < all) *reinterpret_cast<V*>(to + off[u]) = buf[u];
+        }
+    } else {
+        for (int64_t x = threadIdx.x; x < total; x += kForkThreads) {
+            const int64_t off = x / vecs * head_bytes + x % vecs * VEC;
+            *reinterpret_cast<V*>(to + off) = *reinterpret_cast<const V*>(from + off);
+        }
     }
 }
 

@@ -17,6 +17,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "cp_async.cuh"
 #include "ptx.cuh"
 #include "write_kv.cuh"
 
@@ -81,14 +82,18 @@ __device__ __forceinline__ float2 turn_cos_sin(uint64_t t) {
     return make_float2((quarter == 1 || quarter == 2) ? -x : x, (quarter & 2) ? -y : y);
 }
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxDim = 256;
-
 template <typename E, int VEC>
 struct RopeVec {
     static constexpr int kBytes = VEC * (int)sizeof(E);
     using Raw = typename VecType<kBytes>::T;
     Raw raw;
+    __device__ __forceinline__ void clear() { raw = Raw{}; }
+    // Unpacked again from here on: keeping what was unpacked would cost more registers
+    // than it saves time.
+    __device__ __forceinline__ void repack() {
+        if constexpr (kBytes == 16)
+            asm volatile("" : "+r"(raw.x), "+r"(raw.y), "+r"(raw.z), "+r"(raw.w));
+    }
     __device__ __forceinline__ void load(const E* p) { raw = *reinterpret_cast<const Raw*>(p); }
     __device__ __forceinline__ void store(E* p) const { *reinterpret_cast<Raw*>(p) = raw; }
     __device__ __forceinline__ float get(int i) const {
@@ -99,146 +104,279 @@ struct RopeVec {
     }
 };
 
-// A row is D / (2 VEC) pairs of VEC-element pieces, whose rotated pairs lie inside it
-// (neighbours) or between its two pieces (halves).  2^LOG lanes share a row, a lane
-// has up to C of its piece pairs.  One CTA: `tile` tokens.
-template <typename E, int VEC, int C>
-__global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeArgs a, int32_t tile,
-                                                                  int32_t log_lanes) {
-    extern __shared__ float2 s_turn[];              // [tile][rot_dim / 2] cos, sin
+// A warp works on one token (`splits` warps share one where there are few), so that
+// each lane computes and keeps the cos and sin of its own pairs for all heads.  A row
+// is D / (2 VEC) pairs of VEC-element pieces, whose rotated pairs lie inside a piece
+// (neighbours) or between its two pieces (halves); `lanes` lanes share a row (as many as
+// it has piece pairs, so that other dims than powers of two leave few lanes idle: 5001 tokens of
+// 15 + 5 heads of 80 on fp32 take 16.1 us in 10 lanes a row, 20.3 in 16) and a lane has up to C of its piece pairs.
+constexpr int kRopeWarps = 8;
+constexpr int kRopeThreads = 32 * kRopeWarps;
+constexpr int kRopeMaxDim = 256;
+
+template <typename E, int VEC, int C, bool NEIGHBOURS>
+struct RopeRows {
     using Vec = RopeVec<E, VEC>;
+    int32_t dim, lanes, lane, pieces, across;   // `lanes` lanes share a row, this one is `lane`
+    int32_t at0[C], at1[C];         // a piece pair's two places (dim: none)
+    float cs[C][VEC], sn[C][VEC];   // of its pairs
+    uint32_t turned;                // bit c * VEC + i: that pair is rotated
+
+    __device__ __forceinline__ int32_t piece(int c) const {
+        return lane + c * lanes;
+    }
+    __device__ __forceinline__ void place(const RopeArgs& a, int32_t of, int32_t mine) {
+        dim = a.head_dim;
+        lanes = of;
+        lane = mine;
+        pieces = VEC == 1 ? (dim + 1) / 2 : dim / (2 * VEC);
+        across = a.rot_dim / (2 * VEC);              // rotated piece pairs, halves
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int32_t p = piece(c);
+            if (NEIGHBOURS) {
+                at0[c] = VEC == 1 ? 2 * p : p * VEC;
+                at1[c] = VEC == 1 ? 2 * p + 1 : (p + pieces) * VEC;
+            } else {
+                at0[c] = (p < across ? p : across + p) * VEC;
+                at1[c] = (p < across ? p + across : pieces + p) * VEC;
+            }
+            if (p >= pieces) at0[c] = at1[c] = dim;
+            if (at1[c] >= dim) at1[c] = dim;
+        }
+    }
+    // The pairs' cos and sin.
+    __device__ __forceinline__ void turn(int32_t half, const float2* of) {
+        turned = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                // pair i of the pieces (halves), of one piece, then the other (neighbours)
+                const int32_t p = piece(c);
+                int32_t j;
+                if (VEC > 1 && NEIGHBOURS)
+                    j = (i < VEC / 2 ? at0[c] : at1[c]) / 2 + i % (VEC > 1 ? VEC / 2 : 1);
+                else
+                    j = NEIGHBOURS ? p : p < across ? p * VEC + i : half;
+                const bool in = p < pieces && j < half;
+                const float2 x = in ? of[j] : make_float2(1.f, 0.f);
+                cs[c][i] = x.x;
+                sn[c][i] = x.y;
+                turned |= in ? 1u << (c * VEC + i) : 0u;
+            }
+    }
+    __device__ __forceinline__ void turn_piece(int c, float (&y0)[VEC], float (&y1)[VEC]) const {
+        constexpr uint32_t kAll = (1u << VEC) - 1;
+        const uint32_t bits = turned >> (c * VEC) & kAll;
+        if (bits == 0) return;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const bool one = VEC > 1 && NEIGHBOURS;
+            float& a = !one ? y0[i] : i < VEC / 2 ? y0[2 * i % VEC] : y1[2 * i % VEC];
+            float& b = !one ? y1[i] : i < VEC / 2 ? y0[(2 * i + 1) % VEC] : y1[(2 * i + 1) % VEC];
+            const float x = a, y = b;
+            const float u = x * cs[c][i] - y * sn[c][i], w = x * sn[c][i] + y * cs[c][i];
+            const bool in = bits == kAll || (bits >> i & 1);
+            a = in ? u : x;
+            b = in ? w : y;
+        }
+    }
+    struct Weights {
+        Vec lo[C], hi[C];
+    };
+    __device__ __forceinline__ void load(Weights& w, const E* weight) const {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            w.lo[c].clear();
+            w.hi[c].clear();
+            if (weight != nullptr && at0[c] < dim) w.lo[c].load(weight + at0[c]);
+            if (weight != nullptr && at1[c] < dim) w.hi[c].load(weight + at1[c]);
+        }
+    }
+    // One row of each group of lanes, normed (NORM) and rotated.
+    template <bool NORM>
+    __device__ __forceinline__ void row(Vec (&lo)[C], Vec (&hi)[C], const Weights& w, float inv_dim,
+                                        float eps) const {
+        float norm = 1.f;
+        if constexpr (NORM) {
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    sum = fmaf(lo[c].get(i), lo[c].get(i), sum);
+                    sum = fmaf(hi[c].get(i), hi[c].get(i), sum);
+                }
+            if ((lanes & (lanes - 1)) == 0) {
+                for (int32_t off = lanes >> 1; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            } else {
+                for (int32_t off = 16; off > 0; off >>= 1) {
+                    if (off >= lanes) continue;
+                    const float x = __shfl_down_sync(0xffffffffu, sum, off);
+                    if (lane < off && lane + off < lanes) sum += x;
+                }
+                sum = __shfl_sync(0xffffffffu, sum, (threadIdx.x & 31) - lane);
+            }
+            norm = rsqrtf(fmaf(sum, inv_dim, eps));
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if constexpr (NORM && sizeof(E) == 2) {
+                lo[c].repack();
+                hi[c].repack();
+            }
+            float y0[VEC], y1[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                y0[i] = lo[c].get(i);
+                y1[i] = hi[c].get(i);
+                if constexpr (NORM) {
+                    y0[i] = y0[i] * norm * w.lo[c].get(i);
+                    y1[i] = y1[i] * norm * w.hi[c].get(i);
+                }
+            }
+            turn_piece(c, y0, y1);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                lo[c].set(i, y0[i]);
+                hi[c].set(i, y1[i]);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(const Vec (&lo)[C], const Vec (&hi)[C], E* dst) const {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (at0[c] < dim) lo[c].store(dst + at0[c]);
+            if (at1[c] < dim) hi[c].store(dst + at1[c]);
+        }
+    }
+};
+
+// Rows come by asynchronous copies into shared memory, each lane's own pieces, so that
+// kRopeDepth rows a lane are under way without registers to hold them (16-byte
+// pieces; smaller ones are loaded as they are needed).
+constexpr int kRopeDepth = 3;
+
+template <typename E, int VEC, int C, bool NEIGHBOURS>
+__global__ void __launch_bounds__(kRopeThreads, sizeof(E) == 2 && VEC == 8 ? 3 : 4) rope_write_kernel(const RopeArgs a, int32_t splits,
+                                                                    int32_t lanes) {
+    constexpr bool kRing = VEC * sizeof(E) == 16;
+    using Rows = RopeRows<E, VEC, C, NEIGHBOURS>;
+    extern __shared__ uint4 s_ring[];               // [kRopeDepth][2][kRopeThreads], then cos, sin
+    float2* s_turn = reinterpret_cast<float2*>(s_ring + (kRing ? kRopeDepth * 2 * kRopeThreads : 0));
     griddep_wait();
     griddep_launch_dependents();
+    const int32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t D = a.head_dim, half = a.rot_dim / 2, B = a.block_size;
-    const int32_t t0 = blockIdx.x * tile;
-    const int32_t tokens = min(tile, a.num_tokens - t0);
-    for (int32_t x = threadIdx.x; x < half * tokens; x += kRopeThreads) {
-        const int32_t t = x / half, j = x - t * half;
-        const int32_t p = a.positions[(int64_t)rope_axis(a, j) * a.num_tokens + t0 + t];
+    const int64_t id = (int64_t)blockIdx.x * kRopeWarps + warp;
+    const int64_t tok = id / splits;
+    const int32_t part = (int32_t)(id - tok * splits);
+    if (tok >= a.num_tokens) return;
+    Rows rows;
+    // This warp's groups of lanes take heads base + group, then those a step further,
+    // ...: of the queries, the keys, the values.  (Lanes left over are of no group.)
+    const int32_t groups = 32 / lanes, base = part * groups, step = splits * groups;
+    const int32_t group = lane / lanes < groups ? lane / lanes : INT32_MAX / 2;
+    rows.place(a, lanes, lane % lanes);
+    const E* const q = reinterpret_cast<const E*>(a.q) + tok * a.q_stride;
+    const E* const k = reinterpret_cast<const E*>(a.k) + tok * a.k_stride;
+    const E* const v = reinterpret_cast<const E*>(a.v) + tok * a.v_stride;
+    // the next row to fetch: its kind (3: none left), first head of the warp, slots
+    int32_t kind = base < a.num_q_heads ? 0 : base < a.num_kv_heads ? 1 : 3, head = base, fetched = 0;
+    uint4* const mine = s_ring + threadIdx.x;
+    auto fetch = [&]() {
+        if constexpr (kRing) {
+            if (kind < 3) {
+                const int32_t h = head + group, heads = kind == 0 ? a.num_q_heads : a.num_kv_heads;
+                const E* src = (kind == 0 ? q : kind == 1 ? k : v) + (int64_t)h * D;
+                uint4* slots = mine + fetched * 2 * kRopeThreads;
+                if (h < heads && rows.at0[0] < D) cp_async16(smem_u32(slots), src + rows.at0[0], 16);
+                if (h < heads && rows.at1[0] < D) cp_async16(smem_u32(slots + kRopeThreads), src + rows.at1[0], 16);
+                head += step;
+                if (head >= heads) {
+                    head = base;
+                    kind = base < a.num_kv_heads ? kind + 1 : 3;
+                }
+            }
+            fetched = fetched + 1 == kRopeDepth ? 0 : fetched + 1;
+            cp_async_commit();
+        }
+    };
+#pragma unroll
+    for (int x = 0; x < kRopeDepth; ++x) fetch();
+    // (the rows are on their way before anything is known of the token: nothing below
+    // waits for more than one load)
+    int64_t slot = a.slot_mapping[tok];
+    const int32_t pos = a.positions[tok];
+    float2* turn = s_turn + warp * half;
+    for (int32_t j = lane; j < half; j += 32) {
+        const int32_t axis = rope_axis(a, j);
+        const int32_t p = axis == 0 ? pos : a.positions[(int64_t)axis * a.num_tokens + tok];
         bool ok;
         const uint64_t f = turn_fraction(a.inv_freq[j], ok);
         float2 cs = turn_cos_sin((uint64_t)((int64_t)p) * f);
         if (!ok) cs = make_float2(NAN, NAN);
-        s_turn[x] = make_float2(a.scale * cs.x, a.scale * cs.y);
+        turn[j] = make_float2(a.scale * cs.x, a.scale * cs.y);
     }
-    __syncthreads();
-    const int32_t lanes = 1 << log_lanes;
-    const int32_t lane = threadIdx.x & (lanes - 1);
-    const int32_t pieces = VEC == 1 ? (D + 1) / 2 : D / (2 * VEC);
-    const int32_t turned = a.neighbours ? 0 : a.rot_dim / (2 * VEC);   // piece pairs, halves
-    const int32_t rows = a.num_q_heads + 2 * a.num_kv_heads;
-    const int32_t groups = kRopeThreads >> log_lanes;
-    const float inv_dim = 1.0f / (float)D;
-    // (whole warps go round together: the sums are taken by shuffles)
-    for (int32_t x0 = 0; x0 < tokens * rows; x0 += groups) {
-        const int32_t x = x0 + (threadIdx.x >> log_lanes);
-        const int32_t t = min(x / rows, tokens - 1), r = x - t * rows;
-        const int64_t tok = t0 + t;
-        bool live = x < tokens * rows && a.positions[tok] >= 0;
-        const int32_t kind = r < a.num_q_heads ? 0 : r < a.num_q_heads + a.num_kv_heads ? 1 : 2;
-        const int32_t h = kind == 0 ? r : r - a.num_q_heads - (kind - 1) * a.num_kv_heads;
-        const E* src;
-        E* dst;
-        if (kind == 0) {
-            src = reinterpret_cast<const E*>(a.q) + tok * a.q_stride + (int64_t)h * D;
-            dst = reinterpret_cast<E*>(a.out) + (tok * a.num_q_heads + h) * D;
-        } else {
-            src = reinterpret_cast<const E*>(kind == 1 ? a.k : a.v) +
-                  tok * (kind == 1 ? a.k_stride : a.v_stride) + (int64_t)h * D;
-            const int64_t slot = a.slot_mapping[tok];
-            if (live && slot >= a.num_slots && lane == 0) raise_error(PA_DEVERR_SLOT);
-            live = live && slot >= 0 && slot < a.num_slots;
-            const int64_t block = slot / B;
-            dst = reinterpret_cast<E*>(kind == 1 ? a.k_cache : a.v_cache) +
-                  ((block * a.num_kv_heads + h) * B + (slot - block * B)) * (int64_t)D;
+    __syncwarp();
+    rows.turn(half, turn);
+    if (slot >= a.num_slots) {
+        if (pos >= 0 && lane == 0 && part == 0) raise_error(PA_DEVERR_SLOT);
+        slot = -1;
+    }
+    const int64_t block = slot / B;
+    const int64_t at = (block * a.num_kv_heads * B + (slot - block * B)) * (int64_t)D;
+    const float inv_dim = 1.f / (float)D;
+    typename Rows::Weights w;
+    int32_t taken = 0;
+    // the rows of one kind, f(lo, hi) between the fetch and the store
+    auto each = [&](const E* src, E* dst, int64_t apart, int32_t heads, auto f) {
+        for (int32_t h0 = base; h0 < heads; h0 += step) {
+            const int32_t h = h0 + group;
+            RopeVec<E, VEC> lo[C], hi[C];
+            if constexpr (kRing) cp_async_wait<kRopeDepth - 1>();
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                lo[c].clear();
+                hi[c].clear();
+                if constexpr (kRing) {
+                    const uint4* slots = mine + taken * 2 * kRopeThreads;
+                    if (h < heads && rows.at0[c] < D) lo[c].raw = slots[0];
+                    if (h < heads && rows.at1[c] < D) hi[c].raw = slots[kRopeThreads];
+                } else {
+                    if (h < heads && rows.at0[c] < D) lo[c].load(src + (int64_t)h * D + rows.at0[c]);
+                    if (h < heads && rows.at1[c] < D) hi[c].load(src + (int64_t)h * D + rows.at1[c]);
+                }
+            }
+            taken = taken + 1 == kRopeDepth ? 0 : taken + 1;
+            fetch();
+            f(lo, hi);
+            if (h < heads) rows.store(lo, hi, dst + h * apart);
         }
-        Vec lo[C], hi[C];
-        int32_t at0[C], at1[C];
-        float sum = 0.f;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int32_t p = lane + (c << log_lanes);
-            // the piece pair's two places
-            if (a.neighbours) {
-                at0[c] = VEC == 1 ? 2 * p : p * VEC;
-                at1[c] = VEC == 1 ? 2 * p + 1 : (p + pieces) * VEC;
-            } else {
-                at0[c] = (p < turned ? p : turned + p) * VEC;
-                at1[c] = (p < turned ? p + turned : pieces + p) * VEC;
-            }
-            if (p >= pieces) at0[c] = at1[c] = D;
-            if (live && at0[c] < D) lo[c].load(src + at0[c]);
-            if (live && at1[c] < D) hi[c].load(src + at1[c]);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                if (at0[c] < D) sum += lo[c].get(i) * lo[c].get(i);
-                if (at1[c] < D) sum += hi[c].get(i) * hi[c].get(i);
-            }
-        }
-        for (int32_t off = lanes >> 1; off > 0; off >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (!live) continue;
-        const E* weight = reinterpret_cast<const E*>(kind == 0 ? a.q_weight : a.k_weight);
-        const float norm = rsqrtf(sum * inv_dim + a.eps);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (at0[c] >= D) continue;
-            const int32_t p = lane + (c << log_lanes);
-            const bool two = at1[c] < D;
-            if (kind < 2) {
-                float y0[VEC], y1[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    y0[i] = lo[c].get(i);
-                    y1[i] = two ? hi[c].get(i) : 0.f;
-                }
-                if (weight != nullptr) {
-                    Vec w0, w1;
-                    w0.load(weight + at0[c]);
-                    if (two) w1.load(weight + at1[c]);
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        y0[i] = y0[i] * norm * w0.get(i);
-                        if (two) y1[i] = y1[i] * norm * w1.get(i);
-                    }
-                }
-                const float2* turn = s_turn + t * half;
-                if (a.neighbours && VEC > 1) {
-#pragma unroll
-                    for (int i = 0; i < VEC; i += 2) {
-                        const int32_t j0 = (at0[c] + i) / 2, j1 = (at1[c] + i) / 2;
-                        if (j0 < half) {
-                            const float2 cs = turn[j0];
-                            const float u = y0[i], w = y0[i + 1];
-                            y0[i] = u * cs.x - w * cs.y;
-                            y0[i + 1] = u * cs.y + w * cs.x;
-                        }
-                        if (j1 < half) {
-                            const float2 cs = turn[j1];
-                            const float u = y1[i], w = y1[i + 1];
-                            y1[i] = u * cs.x - w * cs.y;
-                            y1[i + 1] = u * cs.y + w * cs.x;
-                        }
-                    }
-                } else if (a.neighbours ? p < half : p < turned) {
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        const float2 cs = turn[p * VEC + i];
-                        const float u = y0[i], w = y1[i];
-                        y0[i] = u * cs.x - w * cs.y;
-                        y1[i] = u * cs.y + w * cs.x;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    lo[c].set(i, y0[i]);
-                    if (two) hi[c].set(i, y1[i]);
-                }
-            }
-            lo[c].store(dst + at0[c]);
-            if (two) hi[c].store(dst + at1[c]);
+    };
+    auto turned = [&](const E* src, E* dst, int64_t apart, int32_t heads, const E* weight) {
+        // (fp32 rows leave registers for the weights; else they come from L1 each time)
+        constexpr bool kKeep = sizeof(E) == 4;
+        if (kKeep) rows.load(w, weight);
+        if (weight != nullptr)
+            each(src, dst, apart, heads, [&](auto& lo, auto& hi) {
+                if (!kKeep) rows.load(w, weight);
+                rows.template row<true>(lo, hi, w, inv_dim, a.eps);
+            });
+        else
+            each(src, dst, apart, heads, [&](auto& lo, auto& hi) { rows.template row<false>(lo, hi, w, inv_dim, a.eps); });
+    };
+    if (pos >= 0) {
+        turned(q, reinterpret_cast<E*>(a.out) + tok * a.num_q_heads * D, D, a.num_q_heads,
+               reinterpret_cast<const E*>(a.q_weight));
+        if (slot >= 0) {
+            turned(k, reinterpret_cast<E*>(a.k_cache) + at, (int64_t)B * D, a.num_kv_heads,
+                   reinterpret_cast<const E*>(a.k_weight));
+            each(v, reinterpret_cast<E*>(a.v_cache) + at, (int64_t)B * D, a.num_kv_heads, [](auto&, auto&) {});
         }
     }
+    if constexpr (kRing) cp_async_wait<0>();
 }
 
 }  // namespace pa

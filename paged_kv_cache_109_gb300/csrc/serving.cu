@@ -94,12 +94,19 @@ template <typename E, int VEC>
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
     constexpr int C = std::max(1, 4 / VEC);
     const int32_t pieces = VEC == 1 ? (a.head_dim + 1) / 2 : a.head_dim / (2 * VEC);
-    int32_t log_lanes = 0;
-    while ((1 << log_lanes) < pieces && log_lanes < 5) ++log_lanes;
-    const int32_t tile = a.num_tokens <= 1024 ? 1 : 4;
-    const size_t smem = (size_t)tile * (a.rot_dim / 2) * sizeof(float2);
-    return launch_pdl(rope_write_kernel<E, VEC, C>, dim3((a.num_tokens + tile - 1) / tile),
-                      dim3(kRopeThreads), smem, st, a, tile, log_lanes);
+    const int32_t per = (pieces + 31) / 32, lanes = (pieces + per - 1) / per;
+    // warps of a token: more while the GPU has room for them and they find a row each
+    const int32_t rows = std::max(a.num_q_heads, a.num_kv_heads), groups = 32 / lanes;
+    const int64_t room = (int64_t)std::max(1, device_sm_count()) * 2 * kRopeWarps;
+    int32_t splits = 1;
+    while (splits < 16 && (int64_t)a.num_tokens * splits < room && splits * groups < rows) splits *= 2;
+    const size_t ring = VEC * sizeof(E) == 16 ? (size_t)kRopeDepth * 2 * kRopeThreads * 16 : 0;
+    const size_t smem = ring + (size_t)kRopeWarps * (a.rot_dim / 2) * sizeof(float2);
+    const int64_t ctas = ((int64_t)a.num_tokens * splits + kRopeWarps - 1) / kRopeWarps;
+    const dim3 grid((unsigned)ctas), block(kRopeThreads);
+    return a.neighbours
+               ? launch_pdl(rope_write_kernel<E, VEC, C, true>, grid, block, smem, st, a, splits, lanes)
+               : launch_pdl(rope_write_kernel<E, VEC, C, false>, grid, block, smem, st, a, splits, lanes);
 }
 
 // Widest pieces that the head dim and the rotated part hold whole, and the pointers
@@ -123,8 +130,15 @@ int rope_vec(const RopeArgs& a, int elem) {
 
 template <typename E, bool DRAFT, bool WIDE>
 cudaError_t launch_verify(const VerifyArgs& a, int32_t num_seqs, cudaStream_t st) {
+    // CTAs of a sequence: up to 8, each with 2048 tokens of the vocabulary or more while
+    // all CTAs find room at once (4 a SM), else with 8192 or more, where a step's fixed
+    // costs count once a CTA.  1, 2, 4 and 8 CTAs, chains of 5 nodes on bf16: one of 16000
+    // tokens 18.2, 13.8, 11.8, 11.4 us, one of 131072 84, 47, 29, 19; 128 of 8000 18.3,
+    // 17.7, 22.1, 34.5, of 32000 35, 30, 30, 40; 400 of 32000 83, 69, 76, 109, of 131072
+    // 295, 241, 217, 211.
+    const int64_t room = (int64_t)std::max(1, device_sm_count()) * 4;
     unsigned ctas = 1;
-    while (ctas < 8 && num_seqs * ctas < 152 * 2 && a.vocab / (ctas * 2) >= 4096) ctas *= 2;
+    while (ctas < 8 && a.vocab / (2 * (int32_t)ctas) >= ((int64_t)num_seqs * 2 * ctas <= room ? 2048 : 8192)) ctas *= 2;
     auto kern = verify_tree_kernel<E, DRAFT, WIDE>;
     static std::atomic<uint64_t> allowed;
     if (!allow_smem(allowed, kern, kVerifyRing)) return cudaErrorUnknown;
@@ -139,6 +153,62 @@ cudaError_t dispatch_verify(const VerifyArgs& a, int32_t num_seqs, bool wide, cu
 }
 
 // ---- release, fork -----------------------------------------------------------------------
+
+// Whether the current device runs clusters of 16 of the release kernel (8 is what every
+// device does), asked for once.
+bool pool_sixteen() {
+    static std::atomic<uint8_t> known[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    uint8_t x = known[dev].load(std::memory_order_acquire);
+    if (x == 0) {
+        auto can = [](auto kern) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(kPoolMaxCluster);
+            cfg.blockDim = dim3(kPoolThreads);
+            cfg.dynamicSmemBytes = kPoolKept * 4;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = kPoolMaxCluster;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPoolKept * 4) == cudaSuccess &&
+                   cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                   cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0;
+        };
+        x = can(release_blocks_kernel<false>) && can(release_blocks_kernel<true>) ? 2 : 1;
+        cudaGetLastError();
+        known[dev].store(x, std::memory_order_release);
+    }
+    return x == 2;
+}
+
+// CTAs of the cluster, by the entries that there can be: a CTA for every 2048 of them up
+// to 8, then 16 where each has 16384 or more.  (256 rows of 258, of which 1800 entries
+// come back: 8.1 us with 2 CTAs, 8.3 with 8, 8.5 with 16.  96 forks in 128 rows of 130 and
+// their release with counts: 40 us with 2, 34 with 8.  2048 rows of 377, 220000 entries
+// back: 91 us with 2, 20.8 with 8, 14.8 with 16.)
+unsigned pool_ctas(int32_t num_seqs, int32_t max_blocks, unsigned most) {
+    const int64_t entries = (int64_t)num_seqs * max_blocks;
+    unsigned ctas = 1;
+    while (ctas < most && entries > (int64_t)ctas * (ctas < 8 ? 2048 : 16384)) ctas *= 2;
+    return ctas;
+}
+
+// The entries of a CTA stay in shared memory between the kernel's passes, up to 160 KB.
+template <bool COUNTED>
+cudaError_t launch_release(ReleaseArgs a, cudaStream_t st) {
+    auto kern = release_blocks_kernel<COUNTED>;
+    const unsigned ctas = pool_ctas(a.num_seqs, a.max_blocks, pool_sixteen() ? 16 : 8);
+    // (a warp's share is rounded up to 32)
+    const int64_t share = ((int64_t)a.num_seqs * a.max_blocks + ctas - 1) / ctas + 33 * kPoolWarps;
+    a.kept = (int32_t)std::min<int64_t>(share, kPoolKept);
+    static std::atomic<uint64_t> allowed;
+    if (!allow_smem(allowed, kern, kPoolKept * 4)) return cudaErrorUnknown;
+    return launch_cluster(kern, dim3(ctas), dim3(kPoolThreads), ctas, (size_t)a.kept * 4, st, a);
+}
 
 template <int LAYERS>
 cudaError_t launch_fork_copy(const ForkArgs& a, const pa_cache_desc* cache, void* const* k,
@@ -246,11 +316,12 @@ pa_status pa_rope_write(const void* q, const void* k, const void* v, int64_t q_s
     for (int x = 0; x < 3; ++x) a.section[x] = x < rope->num_axes ? rope->sections[x] : 0;
     a.eps = rope->eps;
     a.scale = rope->scale;
-    if (!map_current_arg(a.q) || !map_current_arg(a.k) || !map_current_arg(a.v) ||
-        !map_current_arg(a.q_weight) || !map_current_arg(a.k_weight) ||
-        !map_current_arg(a.positions) || !map_current_arg(a.inv_freq) ||
-        !map_current_arg(a.slot_mapping) || !map_current_arg(a.out) ||
-        !current_device_memory(k_cache) || !current_device_memory(v_cache))
+    const CallDevice dev;
+    if (!dev.map(a.q) || !dev.map(a.k) || !dev.map(a.v) ||
+        !dev.map(a.q_weight) || !dev.map(a.k_weight) ||
+        !dev.map(a.positions) || !dev.map(a.inv_freq) ||
+        !dev.map(a.slot_mapping) || !dev.map(a.out) ||
+        !dev.memory(k_cache) || !dev.memory(v_cache))
         return PA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (debug::enabled()) {
@@ -306,10 +377,11 @@ pa_status pa_verify_tree(const void* logits, const void* draft_logits, int64_t l
     VerifyArgs a{logits, draft_logits, logit_stride, draft_stride, noise_stride, tokens, parents,
                  query_start_loc, uniforms, noise, temperature, leaf, next_tokens, total_q,
                  max_q_len, vocab_size};
-    if (!map_current_arg(a.logits) || !map_current_arg(a.draft) || !map_current_arg(a.tokens) ||
-        !map_current_arg(a.parents) || !map_current_arg(a.query_start) ||
-        !map_current_arg(a.uniforms) || !map_current_arg(a.noise) ||
-        !map_current_arg(a.temperature) || !map_current_arg(a.leaf) || !map_current_arg(a.next))
+    const CallDevice dev;
+    if (!dev.map(a.logits) || !dev.map(a.draft) || !dev.map(a.tokens) ||
+        !dev.map(a.parents) || !dev.map(a.query_start) ||
+        !dev.map(a.uniforms) || !dev.map(a.noise) ||
+        !dev.map(a.temperature) || !dev.map(a.leaf) || !dev.map(a.next))
         return PA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (debug::enabled()) {
@@ -349,15 +421,15 @@ pa_status pa_release_blocks(const int32_t* seq_lens, const int32_t* block_tables
     if (!spans_ok(in, outs)) return PA_ERR_INVALID_ARG;
     ReleaseArgs a{seq_lens, block_tables, blocks_held, free_blocks, free_head, ref_cnt,
                   blocks_held_out, free_head_out, num_seqs, num_free, num_blocks, block_size,
-                  max_blocks_per_seq};
-    if (!map_current_arg(a.seq_lens) || !map_current_arg(a.blocks_held) || !map_current_arg(a.free_head) ||
-        !map_current_arg(a.blocks_held_out) || !map_current_arg(a.free_head_out) ||
-        !map_current_arg(a.free_blocks) || (block_tables && !current_device_memory(block_tables)) ||
-        (ref_cnt && !current_device_memory(ref_cnt)))
+                  max_blocks_per_seq, 0};
+    const CallDevice dev;
+    if (!dev.map(a.seq_lens) || !dev.map(a.blocks_held) || !dev.map(a.free_head) ||
+        !dev.map(a.blocks_held_out) || !dev.map(a.free_head_out) ||
+        !dev.map(a.free_blocks) || (block_tables && !dev.memory(block_tables)) ||
+        (ref_cnt && !dev.memory(ref_cnt)))
         return PA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t err = launch_cluster(release_blocks_kernel, dim3(kPoolMaxCluster), dim3(kPoolThreads),
-                                           kPoolMaxCluster, 0, st, a);
+    const cudaError_t err = ref_cnt ? launch_release<true>(a, st) : launch_release<false>(a, st);
     return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -388,11 +460,12 @@ pa_status pa_fork_blocks(const int32_t* src, const int32_t* seq_lens, int32_t* b
     ForkArgs a{src, seq_lens, block_tables, blocks_held, ref_cnt, free_blocks, free_head,
                seq_lens_out, blocks_held_out, free_head_out, block_pairs, num_seqs, num_free,
                cache->num_blocks, cache->block_size, max_blocks_per_seq};
-    if (!map_current_arg(a.src) || !map_current_arg(a.seq_lens) || !map_current_arg(a.blocks_held) ||
-        !map_current_arg(a.free_blocks) || !map_current_arg(a.free_head) ||
-        !map_current_arg(a.seq_lens_out) || !map_current_arg(a.blocks_held_out) ||
-        !map_current_arg(a.free_head_out) || !map_current_arg(a.block_pairs) ||
-        (block_tables && !current_device_memory(block_tables)) || !current_device_memory(ref_cnt))
+    const CallDevice dev;
+    if (!dev.map(a.src) || !dev.map(a.seq_lens) || !dev.map(a.blocks_held) ||
+        !dev.map(a.free_blocks) || !dev.map(a.free_head) ||
+        !dev.map(a.seq_lens_out) || !dev.map(a.blocks_held_out) ||
+        !dev.map(a.free_head_out) || !dev.map(a.block_pairs) ||
+        (block_tables && !dev.memory(block_tables)) || !dev.memory(ref_cnt))
         return PA_ERR_INVALID_ARG;
     // the caches, none of which may share a byte with another
     const int32_t row = cache->head_dim * elem_bytes(cache);
@@ -402,7 +475,7 @@ pa_status pa_fork_blocks(const int32_t* src, const int32_t* seq_lens, int32_t* b
     for (int32_t l = 0; l < num_layers; ++l) {
         for (int which = 0; which < 2; ++which) {
             void* c = which ? v_caches[l] : k_caches[l];
-            if (!current_device_memory(c) || !aligned(c, elem_bytes(cache))) return PA_ERR_INVALID_ARG;
+            if (!dev.memory(c) || !aligned(c, elem_bytes(cache))) return PA_ERR_INVALID_ARG;
             while (vec > 2 && !aligned(c, vec)) vec >>= 1;
             bases[2 * l + which] = reinterpret_cast<uintptr_t>(c);
         }
@@ -412,8 +485,8 @@ pa_status pa_fork_blocks(const int32_t* src, const int32_t* seq_lens, int32_t* b
     for (int32_t x = 1; x < 2 * num_layers; ++x)
         if (bases[x] - bases[x - 1] < cache_bytes) return PA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t err = launch_cluster(fork_blocks_kernel, dim3(kPoolMaxCluster), dim3(kPoolThreads),
-                                     kPoolMaxCluster, 0, st, a);
+    const unsigned ctas = pool_ctas(num_seqs, max_blocks_per_seq, 8);
+    cudaError_t err = launch_cluster(fork_blocks_kernel, dim3(ctas), dim3(kPoolThreads), ctas, 0, st, a);
     for (int32_t l0 = 0; err == cudaSuccess && num_seqs > 0 && l0 < num_layers; l0 += kForkLayers) {
         const int32_t nl = std::min(kForkLayers, num_layers - l0);
         err = nl <= 16 ? launch_fork_copy<16>(a, cache, k_caches + l0, v_caches + l0, nl, vec, st)

@@ -301,22 +301,33 @@ __device__ __forceinline__ void row_sums(uint4* ring, const RowShare<E>& x, cons
     if constexpr (TWO) y.ends(sy);
 }
 
-// 8 elements of a row as they are stored.
+// 8 elements of a share: neighbours where rows are aligned to 16 bytes (WIDE), else
+// kVerifyThreads apart, so that a warp's loads are neighbours.
+template <bool WIDE>
+struct Eight {
+    static constexpr int32_t kApart = WIDE ? 1 : kVerifyThreads, kNext = 8 * kVerifyThreads;
+    static __device__ __forceinline__ int32_t first(int32_t lo) {
+        return lo + (int32_t)threadIdx.x * (WIDE ? 8 : 1);
+    }
+};
+
+// Them as they are stored.
 template <typename E, bool WIDE>
 struct Octet {
     static constexpr int N = RowVec<E>::kCount;
     RowVec<E> v[8 / N];
-    // from p on, -inf past `count`
-    __device__ __forceinline__ void load(const E* p, int32_t count) {
-        if (WIDE && count >= 8) {
+    // of a row, from element o on; -inf from `hi` on
+    __device__ __forceinline__ void load(const E* row, int32_t o, int32_t hi) {
+        if (WIDE && hi - o >= 8) {
 #pragma unroll
-            for (int u = 0; u < 8 / N; ++u) v[u].load(p + u * N);
+            for (int u = 0; u < 8 / N; ++u) v[u].load(row + o + u * N);
         } else {
 #pragma unroll
             for (int u = 0; u < 8 / N; ++u) v[u].clear();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (i < count) reinterpret_cast<E*>(&v[i / N])[i % N] = p[i];
+                if (o + i * Eight<WIDE>::kApart < hi)
+                    reinterpret_cast<E*>(&v[i / N])[i % N] = row[o + i * Eight<WIDE>::kApart];
         }
     }
     __device__ __forceinline__ uint64_t pair(int i) const { return v[2 * i / N].pair(i % (N / 2)); }
@@ -432,9 +443,9 @@ struct RaceField {
         Octet<float, WIDE> e;
     };
     __device__ __forceinline__ void load(Tokens& t, int32_t o) const {
-        t.x.load(row + o, hi - o);
-        t.e.load(noise + o, hi - o);
-        if (DRAFT && share != 0.f) t.y.load(drow + o, hi - o);
+        t.x.load(row, o, hi);
+        t.e.load(noise, o, hi);
+        if (DRAFT && share != 0.f) t.y.load(drow, o, hi);
     }
     // Their keys, with `share` times `bound`.
     __device__ __forceinline__ void keys(const Tokens& t, int32_t o, float bound, float (&key)[8]) const {
@@ -458,17 +469,17 @@ struct RaceField {
                 const int32_t at = node[j].token - o;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (at == i) key[i] = 0.f;
+                    if (at == i * Eight<WIDE>::kApart) key[i] = 0.f;
             }
     }
     __device__ __forceinline__ Race run() const {
         constexpr float kMost = (1.f - kOpen) / (1.f + kOpen), kLeast = (1.f + kOpen) / (1.f - kOpen);
-        constexpr int32_t kStep = 8 * kVerifyThreads;
+        constexpr int32_t kStep = Eight<WIDE>::kNext;
         float first = 0.f, second = 0.f;
         int32_t at = -1;                // group of the largest
-        int32_t o = lo + 8 * (int32_t)threadIdx.x;
-        // (the next 8 are on their way meanwhile; fp32 rows have no registers for that)
-        constexpr bool kNext = sizeof(E) == 2;
+        int32_t o = Eight<WIDE>::first(lo);
+        // (the next 8 are on their way meanwhile, where registers hold them)
+        constexpr bool kNext = WIDE && sizeof(E) == 2;
         Tokens t;
         if (kNext && o < hi) load(t, o);
         while (o < hi) {
@@ -495,7 +506,7 @@ struct RaceField {
             keys(t, at, kLeast, low);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                r.take(fmaxf(key[i], 0.f), low[i] * (1.f - 2.f * kOpen), at + i);
+                r.take(fmaxf(key[i], 0.f), low[i] * (1.f - 2.f * kOpen), at + i * Eight<WIDE>::kApart);
         }
         r.second = fmaxf(r.second, second);
         return r;
@@ -783,11 +794,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
             float sum = 0.f;
             const float top = s.step.top, draft_top = s.step.draft_top, inv = s.step.inv;
             const float share = s.step.spent * s.step.draft_inv;
-            for (int32_t o = lo + 8 * tid; o < hi; o += 8 * kVerifyThreads) {
+            for (int32_t o = Eight<WIDE>::first(lo); o < hi; o += Eight<WIDE>::kNext) {
                 Octet<E, WIDE> x, y;
                 float up[8], down[8];
-                x.load(row + o, hi - o);
-                y.load(drow + o, hi - o);
+                x.load(row, o, hi);
+                y.load(drow, o, hi);
                 x.powers(top, scale, up);
                 y.powers(draft_top, scale, down);
 #pragma unroll
