@@ -47,7 +47,7 @@ struct VerifyArgs {
 
 constexpr int kVerifyThreads = 256;                 // one a node
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyMaxCluster = 16;
+constexpr int kVerifyMaxCluster = 8;
 static_assert(kVerifyThreads >= PA_MAX_TREE_NODES, "a thread per node");
 
 // What a warp tells the CTAs: the largest logit of its share and the sum of
@@ -262,36 +262,55 @@ __device__ __forceinline__ void row_sums(uint4* ring, const RowShare<E>& x, cons
     const int32_t tid = threadIdx.x;
     const int32_t most = TWO ? max(x.pieces, y.pieces) : x.pieces;
     uint4* mine = ring + tid;
-    auto issue = [&](int32_t at, uint4* slot) {
+    // step k has x's pieces k X T + u T + tid; where all threads have all of theirs
+    // (`whole` steps), nothing is asked
+    const int32_t whole = (TWO ? min(x.pieces, y.pieces) : x.pieces) / (X * T);
+    const int32_t steps = (most + X * T - 1) / (X * T);
+    const E* px = x.body + (int64_t)tid * N;
+    const E* py = TWO ? y.body + (int64_t)tid * N : nullptr;
+    auto issue = [&](int32_t k, int32_t d) {
+        const uint32_t slot = smem_u32(mine) + d * (4 * T * 16);
+        if (k < whole) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const RowShare<E>& r = u < X ? x : y;
-            const int32_t p = at + (u < X ? u : u - X) * T;
-            if (p < r.pieces) cp_async16(smem_u32(slot + u * T), r.body + (int64_t)p * N, 16);
-        }
-        cp_async_commit();
-    };
-    int32_t ahead = tid;
+            for (int u = 0; u < 4; ++u) cp_async16(slot + u * T * 16, u < X ? px + u * T * N : py + (u - X) * T * N, 16);
+        } else {
+            const int32_t at = k * X * T + tid;
 #pragma unroll
-    for (int d = 0; d < kVerifyDepth; ++d, ahead += X * T) issue(ahead, mine + d * 4 * T);
-    int d = 0;
-    for (int32_t at = tid; at < most; at += X * T, ahead += X * T) {
-        cp_async_wait<kVerifyDepth - 1>();
-        uint4* slot = mine + d * 4 * T;
-        RowVec<E> a[X], b[TWO ? 2 : 1];
-#pragma unroll
-        for (int u = 0; u < X; ++u) {
-            a[u].clear();
-            if (at + u * T < x.pieces) a[u].r = slot[u * T];
-        }
-        if constexpr (TWO) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                b[u].clear();
-                if (at + u * T < y.pieces) b[u].r = slot[(X + u) * T];
+            for (int u = 0; u < 4; ++u) {
+                const int32_t p = at + (u < X ? u : u - X) * T;
+                if (p < (u < X ? x.pieces : y.pieces))
+                    cp_async16(slot + u * T * 16, u < X ? px + u * T * N : py + (u - X) * T * N, 16);
             }
         }
-        issue(ahead, slot);
+        px += X * T * N;
+        if (TWO) py += X * T * N;
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int d = 0; d < kVerifyDepth; ++d) issue(d, d);
+    int d = 0;
+    for (int32_t k = 0; k < steps; ++k) {
+        cp_async_wait<kVerifyDepth - 1>();
+        const uint4* slot = mine + d * 4 * T;
+        RowVec<E> a[X], b[TWO ? 2 : 1];
+#pragma unroll
+        for (int u = 0; u < X; ++u) a[u].r = slot[u * T];
+        if constexpr (TWO) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) b[u].r = slot[(X + u) * T];
+        }
+        if (k >= whole) {               // (what is behind the rows is whatever was there)
+            const int32_t at = k * X * T + tid;
+#pragma unroll
+            for (int u = 0; u < X; ++u)
+                if (at + u * T >= x.pieces) a[u].clear();
+            if constexpr (TWO) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (at + u * T >= y.pieces) b[u].clear();
+            }
+        }
+        issue(k + kVerifyDepth, d);
         d = d + 1 == kVerifyDepth ? 0 : d + 1;
         sx.take(a);
         if constexpr (TWO) sy.take(b);

@@ -337,6 +337,50 @@ def test_noise_at_its_edges(cuda_device):
     assert int(token[3]) == verify_reference(_only(b, [3]))[0][1]
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("vocab,a,b", [(40, 5, 6), (3001, 8, 2900), (131072, 100, 131071),
+                                       (131072, 70000, 70001), (100003, 50000, 99999)])
+def test_near_ties_of_the_next_token(cuda_device, dtype, vocab, a, b):
+    """Two tokens of one weight whose noise is equal, or differs in its last bits:
+    the lower index, or the smaller noise."""
+    for child in (False, True):
+        c = VerifyBatch([1 + child] * 3, vocab, dtype, seed=18, kind="chain", spread=0.1)
+        row = c.start[:-1].long()
+        c.logits[row] = c.logits[row].clamp(max=0.5)
+        c.logits[row[:, None], torch.tensor([a, b])] = 8.0
+        c.noise[:, [a, b]] = 1e-3
+        c.noise[1, b] = torch.nextafter(torch.tensor(1e-3), torch.tensor(0.0))
+        c.noise[2, a] = torch.nextafter(torch.tensor(1e-3), torch.tensor(0.0))
+        if child:
+            # a draft that leaves both tokens their weights: it fails on another one
+            c.draft[row] = -20.0
+            c.draft[row, 20] = 8.0
+            c.logits[row, 20] = -30.0
+            c.tokens[row + 1], c.uniforms[row + 1] = 20, 0.9
+        leaf, token = c.run(pa, cuda_device)
+        p = torch.softmax(c.logits[row].double(), 1)
+        if child:
+            p = (p - torch.softmax(c.draft[row].double(), 1)).clamp(min=0)
+        race = p / c.noise.double()
+        first = [int((r == r.max()).nonzero()[0, 0]) for r in race]
+        # (of 131072 tokens a third one may have noise small enough to win)
+        assert sum(x == y for x, y in zip(first, (a, b, a))) >= 2
+        assert leaf.tolist() == [0] * 3 and token.tolist() == first, child
+
+
+@pytest.mark.parametrize("vocab", [50, 4100, 131072])
+def test_a_rest_that_rounding_leaves_empty(cuda_device, vocab):
+    """A draft equal to the target, all tries failed (uniforms of one): nothing is
+    left of P, and the next token is drawn from P itself."""
+    for dtype in (F32, BF):
+        b = VerifyBatch([3, 4], vocab, dtype, seed=19, kind="star", sure=1.0)
+        b.draft = b.logits.clone()
+        b.uniforms[:] = 1.0
+        leaf, token = b.run(pa, cuda_device)
+        p = torch.softmax(b.logits[b.start[:-1].long()].double(), 1)
+        assert leaf.tolist() == [0, 0] and token.tolist() == (p / b.noise.double()).argmax(1).tolist()
+
+
 @pytest.mark.parametrize("draft", [True, False])
 def test_tokens_are_distributed_as_the_targets(cuda_device, draft):
     """The first token behind the root over 40000 sequences, within five standard
