@@ -692,7 +692,8 @@ pa_status pa_rope_write(const void* q, const void* k, const void* v, int64_t q_s
  *                  that cannot be drawn; only rows on the walk are read.
  * tokens           device or pinned int32 [total_q]; node 0's is not read.
  * uniforms         device or pinned float [total_q].
- * noise            device or pinned float [num_seqs][vocab_size], rows noise_stride apart.
+ * noise            device or pinned float [num_seqs][vocab_size], rows noise_stride apart;
+ *                  below 2^-126 it counts as zero.
  * temperature      device or pinned float [num_seqs], or NULL for 1.
  * leaf, next_tokens  device or pinned int32 [num_seqs]; a sequence without nodes gets -1
  *                  in both.

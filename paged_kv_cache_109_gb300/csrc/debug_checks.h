@@ -252,5 +252,46 @@ inline pa_status check_tree(const int32_t* query_start, int32_t num_seqs, const 
     return PA_OK;
 }
 
+// Released blocks: every dropped entry a block of the pool that is not in the free
+// queue, dropped no more often than its count (without counts: once).
+inline pa_status check_release(const int32_t* seq_lens, const int32_t* held, int32_t num_seqs,
+                               const int32_t* tables, int32_t max_blocks, const int32_t* free_blocks,
+                               int32_t num_free, const int32_t* head, const int32_t* ref_cnt,
+                               int32_t num_blocks, int32_t block_size, cudaStream_t st) {
+    std::vector<int32_t> len, hld, tab, f, h, cnt((size_t)num_blocks, 1);
+    if (!fetch(len, seq_lens, (size_t)num_seqs, st) || !fetch(hld, held, (size_t)num_seqs, st) ||
+        !fetch(tab, tables, (size_t)num_seqs * max_blocks, st) || !fetch(h, head, 1, st) ||
+        !fetch(f, free_blocks, (size_t)num_free, st) ||
+        (ref_cnt && !fetch(cnt, ref_cnt, (size_t)num_blocks, st)))
+        return PA_ERR_CUDA;
+    std::vector<char> queued((size_t)num_blocks, 0);
+    for (int32_t j = std::max(0, h[0]); j < num_free; ++j)
+        if (f[j] >= 0 && f[j] < num_blocks) queued[f[j]] = 1;
+    for (int32_t i = 0; i < num_seqs; ++i) {
+        const int64_t keep = ((int64_t)len[i] + block_size - 1) / block_size;
+        if (len[i] < 0 || hld[i] < keep || hld[i] > max_blocks)
+            return fail("kept tokens do not fit the blocks held (sequence, held)", i, hld[i]);
+        for (int64_t b = keep; b < hld[i]; ++b) {
+            const int32_t id = tab[(size_t)i * max_blocks + b];
+            if (id < 0 || id >= num_blocks) return fail("released entry outside the pool (sequence, id)", i, id);
+            if (queued[id]) return fail("released block is in the free queue (sequence, id)", i, id);
+            if (--cnt[id] < 0) return fail("block released more often than held (sequence, id)", i, id);
+        }
+    }
+    return PA_OK;
+}
+
+// Forks: sources that are rows and no forks, into rows without blocks.
+inline pa_status check_fork(const int32_t* src, const int32_t* held, int32_t num_seqs, cudaStream_t st) {
+    std::vector<int32_t> s, h;
+    if (!fetch(s, src, (size_t)num_seqs, st) || !fetch(h, held, (size_t)num_seqs, st)) return PA_ERR_CUDA;
+    for (int32_t i = 0; i < num_seqs; ++i) {
+        if (s[i] < 0) continue;
+        if (s[i] >= num_seqs || s[s[i]] >= 0) return fail("fork of no row or of a fork (row, source)", i, s[i]);
+        if (h[i] != 0) return fail("fork into a row that holds blocks (row, held)", i, h[i]);
+    }
+    return PA_OK;
+}
+
 }  // namespace debug
 }  // namespace pa

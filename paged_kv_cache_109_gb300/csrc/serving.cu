@@ -429,6 +429,13 @@ pa_status pa_release_blocks(const int32_t* seq_lens, const int32_t* block_tables
         (ref_cnt && !dev.memory(ref_cnt)))
         return PA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (debug::enabled()) {
+        const pa_status r = debug_pass([&] {
+            return debug::check_release(a.seq_lens, a.blocks_held, num_seqs, block_tables, max_blocks_per_seq,
+                                        a.free_blocks, num_free, a.free_head, ref_cnt, num_blocks, block_size, st);
+        });
+        if (r != PA_OK) return r;
+    }
     const cudaError_t err = ref_cnt ? launch_release<true>(a, st) : launch_release<false>(a, st);
     return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -485,6 +492,14 @@ pa_status pa_fork_blocks(const int32_t* src, const int32_t* seq_lens, int32_t* b
     for (int32_t x = 1; x < 2 * num_layers; ++x)
         if (bases[x] - bases[x - 1] < cache_bytes) return PA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (debug::enabled()) {
+        const pa_status r = debug_pass([&] {
+            const pa_status x = debug::check_fork(a.src, a.blocks_held, num_seqs, st);
+            return x != PA_OK ? x
+                              : debug::check_free(a.free_blocks, num_free, a.free_head, cache->num_blocks, st);
+        });
+        if (r != PA_OK) return r;
+    }
     const unsigned ctas = pool_ctas(num_seqs, max_blocks_per_seq, 8);
     cudaError_t err = launch_cluster(fork_blocks_kernel, dim3(ctas), dim3(kPoolThreads), ctas, 0, st, a);
     for (int32_t l0 = 0; err == cudaSuccess && num_seqs > 0 && l0 < num_layers; l0 += kForkLayers) {

@@ -939,3 +939,92 @@ def test_a_serving_loop_of_all_calls(cuda_device):
     counted = {i for i, c in enumerate(ref.tolist()) if c > 0}
     queue = free.tolist()[int(head):]
     assert len(set(queue)) == len(queue) and not counted & set(queue) and len(counted) + len(queue) == nb
+
+
+# ---- the calls that fit nowhere above ---------------------------------------------------------
+
+def test_empty_batches(cuda_device):
+    e = lambda *shape, dtype=F32: torch.empty(shape, dtype=dtype, device=cuda_device)
+    n32 = e(0, dtype=torch.int32)
+    k = torch.zeros(4, 2, 4, 8, device=cuda_device)
+    out = pa.rope_write(e(0, 4, 8), e(0, 2, 8), e(0, 2, 8), n32, e(4), e(0, dtype=torch.int64), k, k.clone())
+    assert out.shape == (0, 4, 8)
+    leaf, token = pa.verify_tree(e(0, 50), n32, n32, i32([0], cuda_device), e(0), e(0, 50), 0)
+    assert leaf.numel() == token.numel() == 0
+    free, head, counts = i32([3, 1], cuda_device), i32([1], cuda_device), i32([0] * 4, cuda_device)
+    for ref in (None, counts):
+        held, after = pa.release_blocks(n32, e(0, 5, dtype=torch.int32), n32, free, head, 4, 4, ref_cnt=ref)
+        assert held.numel() == 0 and after.tolist() == [1]
+    got = pa.fork_blocks(n32, n32, e(0, 5, dtype=torch.int32), n32, counts, free, head, k, k.clone())
+    assert got[2].tolist() == [1] and pa.last_device_error() == 0
+    # sequences, but none with nodes: no logits at all
+    leaf, token = pa.verify_tree(e(0, 50), n32, n32, i32([0, 0, 0], cuda_device), e(0), torch.ones(2, 50, device=cuda_device), 0)
+    assert leaf.tolist() == token.tolist() == [-1, -1]
+
+
+def test_pinned_logits(cuda_device):
+    for dtype, vocab in ((BF, 5003), (F32, 8192)):
+        b = VerifyBatch([5, 9, 2], vocab, dtype, seed=20, temps=[1.0, 0.0])
+        want = b.run(pa, cuda_device)
+        leaf, token = torch.empty(3, dtype=torch.int32, device=cuda_device), torch.empty(3, dtype=torch.int32, device=cuda_device)
+        pin = lambda t: t.pin_memory()
+        lib, dev = pa.load_library(), lambda t: t.to(cuda_device)
+        t = [pin(b.logits), pin(b.draft), dev(b.tokens), dev(b.parents), dev(b.start), dev(b.uniforms), dev(b.noise),
+             dev(b.temps)]
+        st = lib.pa_verify_tree(t[0].data_ptr(), t[1].data_ptr(), vocab, vocab, vocab,
+                                pa.PA_F32 if dtype == F32 else pa.PA_BF16, *(x.data_ptr() for x in t[2:5]), 3, 16, 9,
+                                t[5].data_ptr(), t[6].data_ptr(), vocab, t[7].data_ptr(), leaf.data_ptr(),
+                                token.data_ptr(), None)
+        torch.cuda.synchronize()
+        assert st == pa.PA_OK and torch.equal(leaf.cpu(), want[0]) and torch.equal(token.cpu(), want[1])
+
+
+def test_debug_checks(cuda_device, monkeypatch):
+    """PA_DEBUG refuses what the kernels cannot see or would report later."""
+    monkeypatch.setenv("PA_DEBUG", "1")
+    dev = lambda x: i32(x, cuda_device)
+    st = PoolState([9, 6], 4, 12, 4, seed=9)
+    state = lambda: [dev([0, 6]), st.tables.to(cuda_device), dev(st.held), dev(st.free), dev([st.head]), 12, 4]
+    assert pa.release_blocks(*state())[0].tolist() == [0, 2]
+    twice, queued, outside = st.tables.clone(), st.tables.clone(), st.tables.clone()
+    twice[0, 1], queued[0, 1], outside[0, 1] = twice[0, 0], st.free[-1], 12
+    for tables in (twice, queued, outside):
+        args = state()
+        args[1] = tables.to(cuda_device)
+        with pytest.raises(pa.PaError):
+            pa.release_blocks(*args)
+    with pytest.raises(pa.PaError):
+        pa.release_blocks(*state(), ref_cnt=dev([0] * 12))
+    k = torch.zeros(12, 1, 4, 8, device=cuda_device)
+    fork = lambda src, held: pa.fork_blocks(dev(src), dev([9, 6, 0]), dev([[0, 1, 2], [3, 4, -1], [-1] * 3]), dev(held),
+                                            dev([1] * 5 + [0] * 7), dev([-1] * 5 + [5, 6]), dev([5]), k, k.clone())
+    assert fork([-1, -1, 0], [3, 2, 0])[1].tolist() == [3, 2, 3]
+    for src, held in (([-1, 0, -1], [3, 2, 0]), ([-1, -1, 3], [3, 2, 0]), ([-1, -1, 2], [3, 2, 0])):
+        with pytest.raises(pa.PaError):
+            fork(src, held)
+    b = RopeBatch(6, 2, 1, 16, 4, F32, seed=21)
+    b.slots[3] = b.slots[1]
+    with pytest.raises(pa.PaError):
+        b.run(pa, cuda_device)
+    v = VerifyBatch([3, 2], 30, F32, seed=22, kind="chain")
+    v.parents[1] = 2
+    with pytest.raises(pa.PaError):
+        v.run(pa, cuda_device)
+
+
+@pytest.mark.parametrize("n,heads,d,dtype", [(2433, 4, 128, BF), (5000, 3, 80, F32), (40000, 1, 32, BF)])
+def test_rope_of_many_tokens(cuda_device, n, heads, d, dtype):
+    """More tokens than warps fit at once, against a call for each part."""
+    b = RopeBatch(n, heads, 1, d, 16, dtype, seed=23, far=100000, skip=tuple(range(0, n, 97)))
+    q, k, v = (x.to(cuda_device) for x in b.split(b.qkv))
+    kc, vc = b.k_cache.to(cuda_device), b.v_cache.to(cuda_device)
+    kc2, vc2 = kc.clone(), vc.clone()
+    move = lambda t: t.to(cuda_device)
+    pos, inv, slots, kw = move(b.pos), move(b.inv), move(b.slots), dict(q_weight=move(b.qw), k_weight=move(b.kw), **b.args)
+    out = pa.rope_write(q, k, v, pos, inv, slots, kc, vc, out=move(b.out), **kw)
+    parts = move(b.out)
+    for i in range(0, n, 501):
+        c = slice(i, i + 501)
+        pa.rope_write(q[c], k[c], v[c], pos[c], inv, slots[c], kc2, vc2, out=parts[c], **kw)
+    assert torch.equal(out, parts) and torch.equal(kc, kc2) and torch.equal(vc, vc2)
+    assert pa.last_device_error() == 0
