@@ -12,6 +12,7 @@ been built, and the calls only accept CUDA tensors.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -778,6 +779,14 @@ def accept_tree(leaf, parents, query_start_loc, seq_lens, k_caches, v_caches, bl
 
 # ---- around the attention -----------------------------------------------------------
 
+@functools.lru_cache(maxsize=256)
+def _descriptors(cache: tuple, rope: tuple, sections: tuple):
+    """The C structs of a cache's and a rotation's plain values (a model's layers
+    pass the same ones every step)."""
+    return (ctypes.byref(CacheDesc(*cache)),
+            ctypes.byref(RopeDesc(rope[0], rope[1], (ctypes.c_int32 * 3)(*sections), *rope[2:])))
+
+
 def _token_rows(t, d: int, what: str):
     """(tokens, heads, elements from token to token) of [n, heads, D] rows whose
     heads follow one another; tokens may be apart (slices of a projection)."""
@@ -785,6 +794,8 @@ def _token_rows(t, d: int, what: str):
     if len(shape) != 3 or shape[2] != d:
         raise ValueError(f"{what} must be [num_tokens, heads, {d}]")
     n, heads, _ = shape
+    if stride[2] == 1 and stride[1] == d and stride[0] >= heads * d:
+        return n, heads, stride[0]
     if (d > 1 and stride[2] != 1) or (heads > 1 and stride[1] != d) \
             or (n > 1 and stride[0] < heads * d):
         raise ValueError(f"the heads of {what} must follow one another, tokens without overlap")
@@ -843,14 +854,14 @@ def rope_write(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, q_w
     elif out.shape != q.shape or out.dtype is not dtype:
         raise ValueError("out must have q's shape and dtype")
     _contiguous(k_cache, v_cache, positions, inv_freq, slot_mapping, out)
-    desc = CacheDesc(blocks, block, heads, d, _DTYPES[dtype])
-    rope = RopeDesc(2 * inv_freq.numel(), axes, (ctypes.c_int32 * 3)(*(sections or ())),
-                    bool(cyclic), bool(neighbours), scale, eps)
+    desc, rope = _descriptors((blocks, block, heads, d, _DTYPES[dtype]),
+                              (2 * inv_freq.numel(), axes, bool(cyclic), bool(neighbours),
+                               float(scale), float(eps)), () if sections is None else tuple(sections))
     st = load_library().pa_rope_write(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, n, hq,
         positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight), _ptr(k_weight),
-        ctypes.byref(rope), slot_mapping.data_ptr(), out.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), ctypes.byref(desc), _raw_stream(stream, device))
+        rope, slot_mapping.data_ptr(), out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), desc,
+        _raw_stream(stream, device))
     if st != PA_OK:
         raise PaError(st, "pa_rope_write")
     return out
