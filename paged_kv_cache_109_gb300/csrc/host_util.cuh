@@ -2,9 +2,12 @@
 // NVTX ranges.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <mutex>
 #include <utility>
 
 #include "decode_config.cuh"
@@ -132,6 +135,36 @@ struct CallDevice {
         cudaPointerAttributes at;
         return p && attributes(p, at) &&
                (at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == id));
+    }
+};
+
+// CallDevice::memory for many pointers of one call (a model's layers): those inside
+// an allocation that was already looked at are not looked up again.
+struct CallMemory {
+    const CallDevice& dev;
+    uintptr_t lo = 0, hi = 0;       // the last allocation found to be the device's
+    explicit CallMemory(const CallDevice& d) : dev(d) {}
+    bool memory(const void* p) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(p);
+        if (x >= lo && x < hi) return true;
+        if (!dev.memory(p)) return false;
+        static PFN_cuMemGetAddressRange_v3020 range = nullptr;
+        static std::once_flag once;
+        std::call_once(once, [] {
+            void* f = nullptr;
+            cudaDriverEntryPointQueryResult q;
+            if (cudaGetDriverEntryPointByVersion("cuMemGetAddressRange", &f, 3020, cudaEnableDefault, &q) ==
+                    cudaSuccess &&
+                q == cudaDriverEntryPointSuccess)
+                range = reinterpret_cast<PFN_cuMemGetAddressRange_v3020>(f);
+        });
+        CUdeviceptr base = 0;
+        size_t bytes = 0;
+        if (range && range(&base, &bytes, (CUdeviceptr)x) == CUDA_SUCCESS) {
+            lo = (uintptr_t)base;
+            hi = lo + bytes;
+        }
+        return true;
     }
 };
 

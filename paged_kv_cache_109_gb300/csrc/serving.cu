@@ -479,10 +479,11 @@ pa_status pa_fork_blocks(const int32_t* src, const int32_t* seq_lens, int32_t* b
     int vec = 16;
     while (vec > 2 && row % vec) vec >>= 1;
     uintptr_t bases[2 * kForkMaxLayers];
+    CallMemory known[2] = {CallMemory(dev), CallMemory(dev)};
     for (int32_t l = 0; l < num_layers; ++l) {
         for (int which = 0; which < 2; ++which) {
             void* c = which ? v_caches[l] : k_caches[l];
-            if (!dev.memory(c) || !aligned(c, elem_bytes(cache))) return PA_ERR_INVALID_ARG;
+            if (!known[which].memory(c) || !aligned(c, elem_bytes(cache))) return PA_ERR_INVALID_ARG;
             while (vec > 2 && !aligned(c, vec)) vec >>= 1;
             bases[2 * l + which] = reinterpret_cast<uintptr_t>(c);
         }
