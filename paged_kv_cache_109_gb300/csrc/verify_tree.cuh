@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
     if (tid == 0 && nodes > 0 && DRAFT && inner && !(heat <= 0.f))
         RowShare<E>(draft + (int64_t)q0 * a.draft_stride, lo, hi).prefetch();
     if (rank == 0) {
-        s.parent[tid] = parent;
+        if (tid < PA_MAX_TREE_NODES) s.parent[tid] = parent;
         __syncthreads();
         VerifyNode n{token, -1, -1, uniform};
         for (int32_t j = nodes - 1; j > tid; --j) {
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
             if (p == tid) n.child = j;
             if (p == parent) n.sibling = j;
         }
-        s.node[tid] = n;
+        if (tid < PA_MAX_TREE_NODES) s.node[tid] = n;
     }
 
     uint32_t turn = 0;                  // exchanges so far
