@@ -451,8 +451,8 @@ pa_status pa_check_wait_timeout(int32_t expected, int32_t arrivals, int64_t limi
  * layers and the cache write (pa_write_kv with the plan's slots).  One such
  * step can be captured in a CUDA graph and replayed: lengths, blocks held and
  * the queue's front are device buffers that each call reads and leaves for
- * the next.  The queue itself only shrinks there: pa_plan_step takes from its
- * front, and a finished sequence's blocks are put back by the host, between
+ * the next.  pa_plan_step takes from the queue's front; a finished sequence's
+ * blocks are put back in front of it by pa_release_blocks, or by the host between
  * steps: free_blocks written anew so that the queue ends with the array, free_head
  * at its first.
  */

@@ -672,11 +672,20 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
                 take_better(v, best, y != y ? INFINITY : y, at);
             };
             if (tid < x.front) one(lo + tid);
-            for (int32_t u = tid; u < x.pieces; u += kVerifyThreads) {
-                RowVec<E> w;
-                w.load(x.body + (int64_t)u * RowVec<E>::kCount);
-                if (!(w.top_or_nan() <= v)) {
-                    const int32_t at = lo + x.front + u * RowVec<E>::kCount;
+            constexpr int U = 8;        // pieces under way
+            for (int32_t u0 = tid; u0 < x.pieces; u0 += U * kVerifyThreads) {
+                RowVec<E> w[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    w[u].clear();
+                    if (u0 + u * kVerifyThreads < x.pieces)
+                        w[u].load(x.body + (int64_t)(u0 + u * kVerifyThreads) * RowVec<E>::kCount);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (w[u].top_or_nan() <= v) continue;
+                    const int32_t at = lo + x.front + (u0 + u * kVerifyThreads) * RowVec<E>::kCount;
+#pragma unroll 1
                     for (int i = 0; i < RowVec<E>::kCount; ++i) one(at + i);
                 }
             }
