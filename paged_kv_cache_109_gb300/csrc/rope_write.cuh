@@ -14,6 +14,12 @@
 // as a 64-bit fraction of a turn, F = inv_freq / 2 pi * 2^64 (whole numbers only:
 // the 24 bits of inv_freq times 1 / 2 pi to 96 bits), and p * F modulo 2^64 drops the
 // whole turns without a rounding; what is left is off by p * 2^-64 turns.
+//
+// Bound: each row read and written once.  Measured (GPU time): 16384 tokens of 64 + 8
+// heads of 128 on bf16, 671 MB, 101 us (98% of the copy rate); 2303 tokens of 32 + 8 with
+// norms, 57 MB, 13.6 us, of which the rate allows 8.3 and a launch takes 2.5; 5001 tokens
+// of 15 + 5 heads of 80 on fp32 with norms, 80 MB, 16.0 us (11.8), where instructions bound
+// it; one token 4.0 us.
 #pragma once
 
 #include "common.cuh"
