@@ -17,9 +17,10 @@
 //
 // Bound: each row read and written once.  Measured (GPU time): 16384 tokens of 64 + 8
 // heads of 128 on bf16, 671 MB, 101 us (98% of the copy rate); 2303 tokens of 32 + 8 with
-// norms, 57 MB, 13.6 us, of which the rate allows 8.3 and a launch takes 2.5; 5001 tokens
-// of 15 + 5 heads of 80 on fp32 with norms, 80 MB, 16.0 us (11.8), where instructions bound
-// it; one token 4.0 us.
+// norms, 57 MB, 13.2 us from L2, 16.8 from memory (the rate allows 8.3, and a launch takes
+// 2.5): few warps a SM then, and a row after the other in each; more rows under way
+// changed nothing.  5001 tokens of 15 + 5 heads of 80 on fp32 with norms, 80 MB, 15.4 us
+// (11.8), where instructions bound it; one token 3.6 us.
 #pragma once
 
 #include "common.cuh"
@@ -115,8 +116,8 @@ struct RopeVec {
 // is D / (2 VEC) pairs of VEC-element pieces, whose rotated pairs lie inside a piece
 // (neighbours) or between its two pieces (halves); `lanes` lanes share a row (as many as
 // it has piece pairs, so that other dims than powers of two leave few lanes idle: 5001 tokens of
-// 15 + 5 heads of 80 on fp32 take 16.1 us in 10 lanes a row, 20.3 in 16) and a lane has up to C of its piece pairs.
-constexpr int kRopeWarps = 8;
+// 15 + 5 heads of 80 on fp32 take 15.4 us in 10 lanes a row, 20.3 in 16) and a lane has up to C of its piece pairs.
+constexpr int kRopeWarps = 4;
 constexpr int kRopeThreads = 32 * kRopeWarps;
 constexpr int kRopeMaxDim = 256;
 
@@ -265,7 +266,7 @@ struct RopeRows {
 constexpr int kRopeDepth = 3;
 
 template <typename E, int VEC, int C, bool NEIGHBOURS>
-__global__ void __launch_bounds__(kRopeThreads, sizeof(E) == 2 && VEC == 8 ? 3 : 4) rope_write_kernel(const RopeArgs a, int32_t splits,
+__global__ void __launch_bounds__(kRopeThreads, (sizeof(E) == 2 && VEC == 8 ? 24 : 32) / kRopeWarps) rope_write_kernel(const RopeArgs a, int32_t splits,
                                                                     int32_t lanes) {
     constexpr bool kRing = VEC * sizeof(E) == 16;
     using Rows = RopeRows<E, VEC, C, NEIGHBOURS>;

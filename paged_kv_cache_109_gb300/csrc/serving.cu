@@ -95,11 +95,17 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
     constexpr int C = std::max(1, 4 / VEC);
     const int32_t pieces = VEC == 1 ? (a.head_dim + 1) / 2 : a.head_dim / (2 * VEC);
     const int32_t per = (pieces + 31) / 32, lanes = (pieces + per - 1) / per;
-    // warps of a token: more while the GPU has room for them and they find a row each
+    // warps of a token: more while 8 a SM hold them and they find a row each (32 + 8 heads
+    // of 128 on bf16, 1, 2, 4 and 8 warps a token, rows from memory: 150 tokens 9.3, 6.4, 5.4,
+    // 5.0 us, 600 tokens 9.7, 7.4, 7.9, 9.3, 1200 tokens 11.2, 11.2, 12.7, 14.2)
     const int32_t rows = std::max(a.num_q_heads, a.num_kv_heads), groups = 32 / lanes;
-    const int64_t room = (int64_t)std::max(1, device_sm_count()) * 2 * kRopeWarps;
+    const int64_t room = (int64_t)std::max(1, device_sm_count()) * 8;
     int32_t splits = 1;
-    while (splits < 16 && (int64_t)a.num_tokens * splits < room && splits * groups < rows) splits *= 2;
+    while (splits < 16 && 2 * splits * (int64_t)a.num_tokens <= room && splits * groups < rows) splits *= 2;
+    // two also where one would leave a third of the 24 a SM that 16-byte pieces of bf16 have
+    // (2303 tokens 17.8 us with one, 16.8 with two, from L2 16.0 and 13.0; 3000 tokens 18.6,
+    // 18.9; fp32, of 32 a SM: 2303 tokens of 15 + 5 heads of 80 9.7, 10.3)
+    if (splits == 1 && sizeof(E) == 2 && VEC == 8 && a.num_tokens <= 2 * room && groups < rows) splits = 2;
     const size_t ring = VEC * sizeof(E) == 16 ? (size_t)kRopeDepth * 2 * kRopeThreads * 16 : 0;
     const size_t smem = ring + (size_t)kRopeWarps * (a.rot_dim / 2) * sizeof(float2);
     const int64_t ctas = ((int64_t)a.num_tokens * splits + kRopeWarps - 1) / kRopeWarps;
