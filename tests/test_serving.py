@@ -2,6 +2,7 @@
 against their plain 64-bit forms, at the sizes and values where they can go wrong,
 and a serving loop of all of them."""
 import math
+import threading
 
 import pytest
 import torch
@@ -1028,3 +1029,50 @@ def test_rope_of_many_tokens(cuda_device, n, heads, d, dtype):
         pa.rope_write(q[c], k[c], v[c], pos[c], inv, slots[c], kc2, vc2, out=parts[c], **kw)
     assert torch.equal(out, parts) and torch.equal(kc, kc2) and torch.equal(vc, vc2)
     assert pa.last_device_error() == 0
+
+
+def test_rope_captured_and_replayed_on_other_tokens(cuda_device):
+    b = RopeBatch(70, 8, 2, 128, 16, BF, seed=24, axes=2, sections=(24, 40), skip=(69,))
+    c = RopeBatch(70, 8, 2, 128, 16, BF, seed=25, axes=2, sections=(24, 40), skip=(3, 68))
+    dev = lambda t: t.to(cuda_device)
+    qkv, pos, slots, out = dev(b.qkv), dev(b.pos), dev(b.slots), dev(b.out)
+    kc, vc, inv, qw, kw = (dev(t) for t in (b.k_cache, b.v_cache, b.inv, b.qw, b.kw))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q, k, v = b.split(qkv)
+        pa.rope_write(q, k, v, pos, inv, slots, kc, vc, q_weight=qw, k_weight=kw, out=out, **b.args)
+    for t, x in ((qkv, c.qkv), (pos, c.pos), (slots, c.slots), (out, c.out), (kc, c.k_cache), (vc, c.v_cache),
+                 (qw, c.qw), (kw, c.kw)):
+        t.copy_(x)
+    graph.replay()
+    torch.cuda.synchronize()
+    c.check(out.cpu(), kc.cpu(), vc.cpu())
+
+
+def test_calls_from_several_host_threads(cuda_device):
+    """Shapes of different instances of the kernels, each thread on a stream of its
+    own."""
+    ropes = [RopeBatch(40, 4, 2, d, 8, t, seed=26 + i, **kw) for i, (d, t, kw) in enumerate(
+        [(128, BF, {}), (80, F32, dict(neighbours=True)), (36, BF, dict(rot=20)), (256, F32, {})])]
+    trees = [VerifyBatch([4, 7, 1], v, t, seed=30 + i, draft=d) for i, (v, t, d) in enumerate(
+        [(5000, BF, True), (20000, F32, False), (333, F32, True), (40003, BF, False)])]
+    want = [(r.run(pa, cuda_device), t.run(pa, cuda_device)) for r, t in zip(ropes, trees)]
+    wrong = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(10):
+                    got = ropes[i].run(pa, cuda_device), trees[i].run(pa, cuda_device)
+                    same = all(torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+                               for a, b in zip(got, want[i]) for x, y in zip(a, b))
+                    if not same:
+                        wrong.append(i)
+        except Exception as e:                          # a thread's error must reach the test
+            wrong.append((i, repr(e)))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and pa.last_device_error() == 0
