@@ -359,6 +359,10 @@ struct Octet {
                     reinterpret_cast<E*>(&v[i / N])[i % N] = row[o + i * Eight<WIDE>::kApart];
         }
     }
+    __device__ __forceinline__ void load_all(const E* p) {
+#pragma unroll
+        for (int u = 0; u < 8 / N; ++u) v[u].load(p + u * N);
+    }
     __device__ __forceinline__ uint64_t pair(int i) const { return v[2 * i / N].pair(i % (N / 2)); }
     // exponentials relative to the largest
     __device__ __forceinline__ void powers(float top, float scale, float (&w)[8]) const {
@@ -482,6 +486,11 @@ struct RaceField {
         t.e.load(noise, o, hi);
         if (DRAFT && share != 0.f) t.y.load(drow, o, hi);
     }
+    __device__ __forceinline__ void load_all(Tokens& t, int32_t o) const {
+        t.x.load_all(row + o);
+        t.e.load_all(noise + o);
+        if (DRAFT && share != 0.f) t.y.load_all(drow + o);
+    }
     // Their keys, with `share` times `bound`.
     __device__ __forceinline__ void keys(const Tokens& t, int32_t o, float bound, float (&key)[8]) const {
         float up[8];
@@ -512,15 +521,7 @@ struct RaceField {
         constexpr int32_t kStep = Eight<WIDE>::kNext;
         float first = 0.f, second = 0.f;
         int32_t at = -1;                // group of the largest
-        int32_t o = Eight<WIDE>::first(lo);
-        // (the next 8 are on their way meanwhile, where registers hold them)
-        constexpr bool kNext = WIDE && sizeof(E) == 2;
-        Tokens t;
-        if (kNext && o < hi) load(t, o);
-        while (o < hi) {
-            Tokens next;
-            if (!kNext) load(t, o);
-            if (kNext && o + kStep < hi) load(next, o + kStep);
+        auto take = [&](const Tokens& t, int32_t o) {
             float key[8];
             keys(t, o, kMost, key);
             // (a NaN, as of no weight and no noise, is left out)
@@ -529,9 +530,32 @@ struct RaceField {
             second = fmaxf(second, fminf(first, m));
             if (m > first) at = o;
             first = fmaxf(first, m);
-            if (kNext) t = next;
-            o += kStep;
+        };
+        int32_t o = Eight<WIDE>::first(lo);
+        if constexpr (WIDE && sizeof(E) == 2) {
+            // all threads have all of their 8: the next ones are on their way meanwhile
+            // (fp32 rows have no registers for that)
+            const int32_t whole = (hi - lo) / kStep;
+            Tokens a, b;
+            if (whole > 0) load_all(a, o);
+            int32_t k = 0;
+            for (; k + 2 <= whole; k += 2, o += 2 * kStep) {
+                load_all(b, o + kStep);
+                take(a, o);
+                if (k + 2 < whole) load_all(a, o + 2 * kStep);
+                take(b, o + kStep);
+            }
+            if (k < whole) {
+                take(a, o);
+                o += kStep;
+            }
         }
+        for (; o < hi; o += kStep) {
+            Tokens t;
+            load(t, o);
+            take(t, o);
+        }
+        Tokens t;
         Race r;
         r.start();
         if (at >= 0) {
