@@ -50,10 +50,11 @@
  * call first synchronises its stream, copies its index arrays to the host and
  * checks them as a whole.  Duplicate slots, two copies into one block (or,
  * inside one pool, onto a source), entries or slots outside the pool, lengths
- * past their bounds, query rows out of order and appends into a block that
- * another table also reaches are then refused with
- * PA_ERR_INVALID_ARG before launch (the first violation is printed to
- * stderr).  This is slow and is not for use under stream capture.
+ * past their bounds, query rows out of order, appends into a block that
+ * another table also reaches, and blocks released that are free or held less
+ * often are then refused with PA_ERR_INVALID_ARG before launch (the first
+ * violation is printed to stderr).  This is slow and is not for use under stream
+ * capture.
  *
  * Tracing: each call is an NVTX range of its own name (pa_write_kv,
  * pa_decode, ...) around its checks and launches.

@@ -51,9 +51,6 @@ __device__ __forceinline__ void cluster_store(uint32_t at, uint32_t x) {
 __device__ __forceinline__ void cluster_store(uint32_t at, int32_t x) {
     cluster_store(at, (uint32_t)x);
 }
-__device__ __forceinline__ void cluster_store(uint32_t at, float x) {
-    cluster_store(at, __float_as_uint(x));
-}
 __device__ __forceinline__ void cluster_store(uint32_t at, float2 x) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(x.x), "f"(x.y) : "memory");
 }

@@ -357,9 +357,9 @@ __global__ void __launch_bounds__(kRopeThreads, (sizeof(E) == 2 && VEC == 8 ? 24
                 }
             }
             taken = taken + 1 == kRopeDepth ? 0 : taken + 1;
-            fetch();
             f(lo, hi);
             if (h < heads) rows.store(lo, hi, dst + h * apart);
+            fetch();                    // (the slots have been read: their values are used)
         }
     };
     auto turned = [&](const E* src, E* dst, int64_t apart, int32_t heads, const E* weight) {

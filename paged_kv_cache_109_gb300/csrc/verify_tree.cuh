@@ -26,8 +26,8 @@
 // practice the walk, whose steps wait for one another.  A step of 131072 tokens on bf16 in
 // 8 CTAs takes some 7500 clocks alone: 4300 for the two rows, 1050 for the barrier, 1200
 // for the decision, the rest for the warps' sums; three times as many CTAs on an SM make
-// it 11000.  Measured (GPU time): 64 chains of 5 nodes, 115 MB, 47 us (the copy rate:
-// 17); 128 trees of up to 40, 243 MB, 81 us (36); 48 trees on fp32 with 100003 tokens and
+// it 11000.  Measured (GPU time): 64 chains of 5 nodes, 115 MB, 46 us (the copy rate:
+// 17); 128 trees of up to 40, 243 MB, 80 us (36); 48 trees on fp32 with 100003 tokens and
 // no draft rows, 63 MB, 34 us from memory (9.3); one chain of 6 at 32000 tokens 18 us, a
 // launch and 6 steps.  Half of the issue slots are in use then; deeper copies, a fetch of
 // the likely next rows ahead, 16 CTAs a sequence or 512 threads a CTA did not help.
@@ -320,10 +320,10 @@ __device__ __forceinline__ void row_sums(uint4* ring, const RowShare<E>& x, cons
                     if (at + u * T >= y.pieces) b[u].clear();
             }
         }
-        issue(k + kVerifyDepth, d);
-        d = d + 1 == kVerifyDepth ? 0 : d + 1;
         sx.take(a);
         if constexpr (TWO) sy.take(b);
+        issue(k + kVerifyDepth, d);     // (the slots have been read: their values are used)
+        d = d + 1 == kVerifyDepth ? 0 : d + 1;
     }
     cp_async_wait<0>();
     x.ends(sx);
