@@ -729,7 +729,10 @@ pa_status pa_verify_tree(const void* logits, const void* draft_logits, int64_t l
  *   free_blocks[F - m .. F), F = *free_head,  *free_head_out = F - m,
  *   blocks_held_out[i] = K_i
  * (the entries themselves stay as they were).  So pa_plan_step takes them next, and
- * an array with room for every block of the pool always has room in front.
+ * an array with room for every block of the pool always has room in front.  With
+ * ref_cnt, the calls that took the blocks must have counted them in it
+ * (pa_plan_step, pa_fork_blocks).  Where seq_lens[i] was zeroed for a finished request
+ * it is 0 for the next pa_plan_step too, which refuses tokens without blocks.
  *
  * All or nothing: where seq_lens[i] < 0, h_i outside [K_i, max_blocks_per_seq]
  * (PA_DEVERR_SEQ_LEN), m > F or F outside [0, num_free] (PA_DEVERR_POOL), or a count
@@ -765,7 +768,9 @@ pa_status pa_release_blocks(const int32_t* seq_lens, const int32_t* block_tables
  *   *free_head_out = *free_head + fresh blocks
  *   block_pairs[i] = (p's block, the fresh one) or (-1, -1)
  * block_pairs are pairs of pa_copy_blocks once the rows of -1 are left out, for
- * further caches of the same tables.
+ * further caches of the same tables.  The sources' blocks must be counted in ref_cnt
+ * already (pa_plan_step with the same ref_cnt): a block at none would be freed with
+ * its fork, while the source still holds it.
  *
  * All or nothing: where src[i] is not a row, is itself forked by this call, or row i
  * holds blocks (PA_DEVERR_FORK), where seq_lens[p] < 0 or blocks_held[p] is outside

@@ -944,8 +944,9 @@ def release_blocks(seq_lens, block_tables, blocks_held, free_blocks, free_head, 
     blocks of its first seq_lens[i] tokens (0 for a finished request); the others
     of its blocks_held[i] lose a reference in ``ref_cnt`` (int32 [num_blocks]; None:
     no block is shared), and those at none are put in front of the queue, in the
-    order of sequences and table entries.  Returns (blocks_held, free_head) after
-    it, new tensors or the given ones, which may be the inputs.  All or nothing,
+    order of sequences and table entries.  The counts are those that ``plan_step`` and
+    ``fork_blocks`` were given; a finished request's length is 0 for the next
+    ``plan_step`` too.  Returns (blocks_held, free_head) after it, new tensors or the given ones, which may be the inputs.  All or nothing,
     with a bit of ``last_device_error`` (DEVERR_SEQ_LEN, DEVERR_POOL,
     DEVERR_SHARED)."""
     device = _current(block_tables)
@@ -982,7 +983,8 @@ def fork_blocks(src, seq_lens, block_tables, blocks_held, ref_cnt, free_blocks, 
                 block_pairs=None, stream=None):
     """Sequences that start as copies of others, on the device
     (``BlockPool.fork``): row i with src[i] >= 0, which holds no blocks, shares the
-    full blocks of sequence src[i] (``ref_cnt`` int32 [num_blocks] counts them) and
+    full blocks of sequence src[i] (``ref_cnt`` int32 [num_blocks] counts them: the
+    same that ``plan_step`` counts the blocks it takes in) and
     gets a fresh block of the queue with a copy of its partly filled one, in every
     layer of ``k_caches`` and ``v_caches`` (as in ``accept_tree``).  Rows of
     ``block_tables`` are written in place.  Returns (seq_lens, blocks_held,

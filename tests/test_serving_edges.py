@@ -1,0 +1,80 @@
+"""Calls around the attention that the documentation allows and that the other tests
+do not make: one token in place, the documented loop, releases that do not fit in
+shared memory, reports of a greedy walk, what PA_DEBUG refuses and what it does not."""
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_109_gb300 as pa
+from tests._serving import (PoolState, RopeBatch, VerifyBatch, i32)
+from tests.conftest import ROOT
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def clear_device_error(cuda_device):
+    pa.last_device_error()
+    yield
+
+
+# ---- the documented loop -----------------------------------------------------------------
+
+def _documented_step():
+    """The drafted step as README.md gives it."""
+    with open(os.path.join(ROOT, "README.md")) as f:
+        text = f.read()
+    begin = text.index("# one drafted (speculative) step")
+    return text[begin:text.index("```", begin)]
+
+
+def test_the_documented_step_runs_as_a_loop(cuda_device):
+    """README's drafted step, run as it stands for several steps: a request that
+    ends, a fork into its row, and at the end every block back in the queue."""
+    dev = lambda x: i32(x, cuda_device)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, device=cuda_device, generator=g)
+    n, hq, hkv, d, bs, blocks, width, vocab, most = 4, 4, 2, 32, 4, 48, 8, 50, 20
+    lens, held = [9, 5, 6, 0], [3, 2, 2, 0]
+    table = [[0, 1, 2] + [-1] * 5, [3, 4] + [-1] * 6, [5, 6] + [-1] * 6, [-1] * 8]
+    s = dict(pa=pa, torch=torch, seq_lens=dev(lens), blocks_held=dev(held), block_tables=dev(table),
+             free_blocks=dev([-1] * 7 + list(range(7, blocks))), free_head=dev([7]),
+             ref_cnt=dev([1] * 7 + [0] * (blocks - 7)), num_blocks=blocks, block_size=bs, max_rows=most,
+             inv_freq=(1000.0 ** (-torch.arange(0, d, 2) / d)).to(cuda_device),
+             k_cache=rand(blocks, hkv, bs, d), v_cache=rand(blocks, hkv, bs, d), wq=rand(d), wk=rand(d),
+             max_q_len=4, max_seq_len=width * bs)
+    s["k_caches"], s["v_caches"] = s["k_cache"], s["v_cache"]
+    step = compile(_documented_step(), "README.md", "exec")
+    # nodes of each row's chain, rows that go on, sources of the rows that fork
+    for nodes, running, src in (([4, 3, 4, 0], [1, 0, 1, 0], [-1, 0, -1, -1]),
+                                ([3, 4, 1, 0], [1, 1, 1, 0], [-1, -1, -1, 1]),
+                                ([2, 2, 4, 4], [1, 1, 0, 1], [-1, -1, -1, -1]),
+                                ([0, 3, 0, 2], [0, 0, 0, 0], [-1, -1, -1, -1])):
+        before = s["seq_lens"].tolist()
+        parents = [j - 1 for m in nodes for j in range(m)]
+        s.update(new_tokens=dev(nodes), parents=dev(parents + [-1] * (most - len(parents))),
+                 q=rand(most, hq, d), k=rand(most, hkv, d), v=rand(most, hkv, d),
+                 positions=dev([t % 7 for t in range(most)]), logits=rand(most, vocab),
+                 draft_logits=rand(most, vocab), tokens=dev([t % vocab for t in range(most)]),
+                 uniforms=torch.rand(most, device=cuda_device, generator=g),
+                 noise=rand(n, vocab).exponential_(generator=g),
+                 temperature=torch.ones(n, device=cuda_device), running=dev(running), src=dev(src))
+        exec(step, s)
+        assert pa.last_device_error() == 0
+        leaf = s["leaf"].tolist()
+        want = [(c + l + 1) * r for c, l, r in zip(before, leaf, running)]
+        want = [want[p] if p >= 0 else t for t, p in zip(want, src)]
+        assert s["seq_lens"].tolist() == want
+        assert s["blocks_held"].tolist() == [-(-t // bs) for t in want]
+        # each block is in the queue or counted, as often as rows hold it
+        rows, count = s["block_tables"].tolist(), [0] * blocks
+        for row, h in zip(rows, s["blocks_held"].tolist()):
+            for b in row[:h]:
+                count[b] += 1
+        assert s["ref_cnt"].tolist() == count
+        assert sorted(s["free_blocks"].tolist()[int(s["free_head"]):]) == [b for b in range(blocks) if not count[b]]
+    assert int(s["free_head"]) == 0
