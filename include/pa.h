@@ -51,10 +51,10 @@
  * checks them as a whole.  Duplicate slots, two copies into one block (or,
  * inside one pool, onto a source), entries or slots outside the pool, lengths
  * past their bounds, query rows out of order, appends into a block that
- * another table also reaches, and blocks released that are free or held less
- * often are then refused with PA_ERR_INVALID_ARG before launch (the first
- * violation is printed to stderr).  This is slow and is not for use under stream
- * capture.
+ * another table also reaches, blocks released that are free or held less often, and
+ * forks of blocks that no count holds are then refused with PA_ERR_INVALID_ARG
+ * before launch (the first violation is printed to stderr).  This is slow and is not
+ * for use under stream capture.
  *
  * Tracing: each call is an NVTX range of its own name (pa_write_kv,
  * pa_decode, ...) around its checks and launches.
@@ -770,7 +770,7 @@ pa_status pa_release_blocks(const int32_t* seq_lens, const int32_t* block_tables
  * block_pairs are pairs of pa_copy_blocks once the rows of -1 are left out, for
  * further caches of the same tables.  The sources' blocks must be counted in ref_cnt
  * already (pa_plan_step with the same ref_cnt): a block at none would be freed with
- * its fork, while the source still holds it.
+ * its fork, while the source still holds it (PA_DEBUG=1 refuses that).
  *
  * All or nothing: where src[i] is not a row, is itself forked by this call, or row i
  * holds blocks (PA_DEVERR_FORK), where seq_lens[p] < 0 or blocks_held[p] is outside

@@ -10,8 +10,8 @@
 // first violation to stderr and the call returns PA_ERR_INVALID_ARG without
 // launching.
 //
-// Ref counts are not the library's: a write into a block that sequences share
-// is refused by the host block pool before the call.
+// The writes of pa_write_kv know no counts: one into a block that sequences share
+// is refused by the host block pool, or by pa_plan_step with ref_cnt, before the call.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -281,14 +281,26 @@ inline pa_status check_release(const int32_t* seq_lens, const int32_t* held, int
     return PA_OK;
 }
 
-// Forks: sources that are rows and no forks, into rows without blocks.
-inline pa_status check_fork(const int32_t* src, const int32_t* held, int32_t num_seqs, cudaStream_t st) {
-    std::vector<int32_t> s, h;
-    if (!fetch(s, src, (size_t)num_seqs, st) || !fetch(h, held, (size_t)num_seqs, st)) return PA_ERR_CUDA;
+// Forks: sources that are rows and no forks, into rows without blocks, and every
+// block of a source's tokens counted (one at none would be freed with its fork).
+inline pa_status check_fork(const int32_t* src, const int32_t* seq_lens, const int32_t* held,
+                            int32_t num_seqs, const int32_t* tables, int32_t max_blocks,
+                            const int32_t* ref_cnt, const pa_cache_desc* c, cudaStream_t st) {
+    std::vector<int32_t> s, len, h, tab, cnt;
+    if (!fetch(s, src, (size_t)num_seqs, st) || !fetch(len, seq_lens, (size_t)num_seqs, st) ||
+        !fetch(h, held, (size_t)num_seqs, st) || !fetch(tab, tables, (size_t)num_seqs * max_blocks, st) ||
+        !fetch(cnt, ref_cnt, (size_t)c->num_blocks, st))
+        return PA_ERR_CUDA;
     for (int32_t i = 0; i < num_seqs; ++i) {
         if (s[i] < 0) continue;
         if (s[i] >= num_seqs || s[s[i]] >= 0) return fail("fork of no row or of a fork (row, source)", i, s[i]);
         if (h[i] != 0) return fail("fork into a row that holds blocks (row, held)", i, h[i]);
+        const int64_t need = std::max<int64_t>(0, ((int64_t)len[s[i]] + c->block_size - 1) / c->block_size);
+        for (int64_t b = 0; b < std::min<int64_t>(need, max_blocks); ++b) {
+            const int32_t id = tab[(size_t)s[i] * max_blocks + b];
+            if (id >= 0 && id < c->num_blocks && cnt[id] <= 0)
+                return fail("fork of a block without a count (source, id)", s[i], id);
+        }
     }
     return PA_OK;
 }

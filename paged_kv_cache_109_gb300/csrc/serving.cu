@@ -501,7 +501,8 @@ pa_status pa_fork_blocks(const int32_t* src, const int32_t* seq_lens, int32_t* b
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (debug::enabled()) {
         const pa_status r = debug_pass([&] {
-            const pa_status x = debug::check_fork(a.src, a.blocks_held, num_seqs, st);
+            const pa_status x = debug::check_fork(a.src, a.seq_lens, a.blocks_held, num_seqs, block_tables,
+                                                  max_blocks_per_seq, ref_cnt, cache, st);
             return x != PA_OK ? x
                               : debug::check_free(a.free_blocks, num_free, a.free_head, cache->num_blocks, st);
         });

@@ -78,3 +78,24 @@ def test_the_documented_step_runs_as_a_loop(cuda_device):
         assert s["ref_cnt"].tolist() == count
         assert sorted(s["free_blocks"].tolist()[int(s["free_head"]):]) == [b for b in range(blocks) if not count[b]]
     assert int(s["free_head"]) == 0
+
+
+# ---- PA_DEBUG --------------------------------------------------------------------------------
+
+def test_debug_refuses_forks_of_blocks_without_counts(cuda_device, monkeypatch):
+    """A shared block's count says who holds it: one that no row counts would be freed
+    by the fork's release, under its source."""
+    monkeypatch.setenv("PA_DEBUG", "1")
+    dev = lambda x: i32(x, cuda_device)
+    st = PoolState([9, 0], 4, 12, 4, seed=6)
+    k, v = torch.zeros(12, 1, 4, 8, device=cuda_device), torch.zeros(12, 1, 4, 8, device=cuda_device)
+
+    def fork(counts):
+        return pa.fork_blocks(dev([-1, 0]), dev(st.lens), st.tables.to(cuda_device), dev(st.held), counts, dev(st.free),
+                              dev([st.head]), k, v)
+    assert fork(st.counts().to(cuda_device))[1].tolist() == [3, 3]
+    for b in st.tables[0, :3].tolist():
+        counts = st.counts()
+        counts[b] = 0
+        with pytest.raises(pa.PaError):
+            fork(counts.to(cuda_device))
