@@ -653,7 +653,7 @@ typedef struct {
  *                the token's query is computed, nothing is cached.  A slot past the pool
  *                is reported (PA_DEVERR_SLOT) and treated so.
  * out            device or pinned [num_tokens][num_q_heads][head_dim]; may be q itself
- *                where q_stride is a row (num_q_heads * head_dim).
+ *                where q_stride is a row (num_q_heads * head_dim) or one token is all.
  * head_dim up to 256 (else PA_ERR_UNSUPPORTED); any alignment of whole elements.
  */
 pa_status pa_rope_write(const void* q, const void* k, const void* v, int64_t q_stride,

@@ -794,7 +794,7 @@ def _token_rows(t, d: int, what: str):
     if len(shape) != 3 or shape[2] != d:
         raise ValueError(f"{what} must be [num_tokens, heads, {d}]")
     n, heads, _ = shape
-    if stride[2] == 1 and stride[1] == d and stride[0] >= heads * d:
+    if n > 1 and stride[2] == 1 and stride[1] == d and stride[0] >= heads * d:
         return n, heads, stride[0]
     if (d > 1 and stride[2] != 1) or (heads > 1 and stride[1] != d) \
             or (n > 1 and stride[0] < heads * d):

@@ -276,6 +276,10 @@ pa_status pa_rope_write(const void* q, const void* k, const void* v, int64_t q_s
     if (!q || !k || !v || !positions || (half > 0 && !inv_freq) || !slot_mapping || !out ||
         !k_cache || !v_cache || q_stride < q_row || k_stride < kv_row || v_stride < kv_row)
         return PA_ERR_INVALID_ARG;
+    if (num_tokens == 1) {              // (no other token is anywhere)
+        q_stride = q_row;
+        k_stride = v_stride = kv_row;
+    }
     const int eb = elem_bytes(cache);
     const int64_t most = INT64_MAX / 16 / num_tokens;
     if (q_stride > most || k_stride > most || v_stride > most) return PA_ERR_INVALID_ARG;

@@ -80,6 +80,44 @@ def test_the_documented_step_runs_as_a_loop(cuda_device):
     assert int(s["free_head"]) == 0
 
 
+# ---- rope_write ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("pad_row", [0, 1, 24])
+def test_one_token_of_a_projection_in_place(cuda_device, dtype, pad_row):
+    """One token's heads follow one another, however wide the row that they were cut
+    from: its queries may be rotated where they are."""
+    b = RopeBatch(1, 8, 2, 64, 8, dtype, seed=1, pad_row=pad_row)
+    q, k, v = b.split(b.qkv.to(cuda_device))
+    kc, vc = b.k_cache.to(cuda_device), b.v_cache.to(cuda_device)
+    move = lambda t: t.to(cuda_device)
+    got = pa.rope_write(q, k, v, move(b.pos), move(b.inv), move(b.slots), kc, vc, q_weight=move(b.qw),
+                        k_weight=move(b.kw), out=q, **b.args)
+    assert got is q
+    b.check(q.cpu(), kc.cpu(), vc.cpu())
+    # cut from all heads at once, so that torch's stride is the projection's
+    heads = b.qkv.to(cuda_device)[:, :12 * 64].view(1, 12, 64)
+    q2, kc, vc = heads[:, :8], b.k_cache.to(cuda_device), b.v_cache.to(cuda_device)
+    assert q2.stride(0) == 12 * 64
+    got = pa.rope_write(q2, heads[:, 8:10], heads[:, 10:], move(b.pos), move(b.inv), move(b.slots), kc, vc,
+                        q_weight=move(b.qw), k_weight=move(b.kw), out=q2, **b.args)
+    assert torch.equal(q2, q)
+    b.check(q2.cpu(), kc.cpu(), vc.cpu())
+    # the C call with the row's own stride
+    q2, k2, v2 = b.split(b.qkv.to(cuda_device))
+    kc, vc = b.k_cache.to(cuda_device), b.v_cache.to(cuda_device)
+    pos, inv, slots, qw, kw = (move(t) for t in (b.pos, b.inv, b.slots, b.qw, b.kw))
+    desc = pa.CacheDesc(kc.shape[0], 8, 2, 64, pa.PA_BF16 if dtype is BF else pa.PA_F32)
+    rope = pa.RopeDesc(64, 1, (pa.ctypes.c_int32 * 3)(), 0, 0, 1.0, 1e-5)
+    width = b.qkv.shape[1]
+    st = pa.load_library().pa_rope_write(
+        q2.data_ptr(), k2.data_ptr(), v2.data_ptr(), width, width, width, 1, 8, pos.data_ptr(), inv.data_ptr(),
+        qw.data_ptr(), kw.data_ptr(), pa.ctypes.byref(rope), slots.data_ptr(), q2.data_ptr(), kc.data_ptr(),
+        vc.data_ptr(), pa.ctypes.byref(desc), None)
+    torch.cuda.synchronize()
+    assert st == pa.PA_OK and torch.equal(q2.cpu(), q.cpu())
+
+
 # ---- PA_DEBUG --------------------------------------------------------------------------------
 
 def test_debug_refuses_forks_of_blocks_without_counts(cuda_device, monkeypatch):
