@@ -776,7 +776,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
                 return;
             }
             int32_t j = s.node[cur].child;
-            while (j >= 0 && s.node[j].token != best) j = s.node[j].sibling;
+            bool out = false;           // a token outside the vocabulary was met
+            while (j >= 0 && s.node[j].token != best) {
+                out |= s.node[j].token < 0 || s.node[j].token >= vocab;
+                j = s.node[j].sibling;
+            }
+            if (out && rank == 0 && tid == 0) raise_error(PA_DEVERR_TREE);
             if (j < 0) {
                 finish(0, cur, best);
                 return;

@@ -118,6 +118,27 @@ def test_one_token_of_a_projection_in_place(cuda_device, dtype, pad_row):
     assert st == pa.PA_OK and torch.equal(q2.cpu(), q.cpu())
 
 
+# ---- verify_tree ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_greedy_walks_report_tokens_outside_the_vocabulary(cuda_device, draft, dtype):
+    b = VerifyBatch([4, 4, 4, 4], 300, dtype, seed=3, kind="star", draft=draft, temps=[0.0])
+    best = b.logits[b.start[:-1].long()].float().argmax(1).tolist()
+    # met before the child that holds, met without one, behind the one that holds
+    b.tokens[:] = i32([0, 300, best[0], 1, 0, -1, 2 ** 31 - 1, -(2 ** 31), 0, best[2], 300, 1, 0, best[3], 0, 0])
+    want = ([2, 0, 1, 1], [0, 1])
+    for keep, bit in (([0, 1, 2, 3], pa.DEVERR_TREE), ([2, 3], 0)):
+        rows = torch.cat([torch.arange(4 * i, 4 * i + 4) for i in keep])
+        c = VerifyBatch([4] * len(keep), 300, dtype, seed=3, kind="star", draft=draft, temps=[0.0])
+        c.tokens, c.logits, c.parents = b.tokens[rows], b.logits[rows], b.parents[rows]
+        c.draft = b.draft[rows] if draft else None
+        leaf, token = c.run(pa, cuda_device)
+        assert pa.last_device_error() == bit
+        assert leaf.tolist() == [want[0][i] for i in keep]
+        assert int(token[keep.index(2)]) == int(b.logits[9].float().argmax())
+
+
 # ---- PA_DEBUG --------------------------------------------------------------------------------
 
 def test_debug_refuses_forks_of_blocks_without_counts(cuda_device, monkeypatch):
