@@ -88,7 +88,7 @@ struct VerifyShared {
     float2 logit[PA_MAX_TREE_NODES];                 // of a node's token: target, draft
     int32_t parent[PA_MAX_TREE_NODES];
     VerifyStep step;
-    int4 tree;                                       // first row, nodes (-1: refused), temperature
+    int4 tree;                                       // first row, nodes (-1: refused), temperature, scale
 };
 
 // ---- packed pairs of floats ------------------------------------------------------------
@@ -694,7 +694,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
             logit.x = Elem<E>::to_float(row[token]);
             if (DRAFT) logit.y = Elem<E>::to_float(drow[token]);
         }
-        VerifyPart mine{kLowest, 0.f, kLowest, 0.f};
+        // (the sum of a CTA that sees no sequence: where the first one sees one, somebody
+        // writes the inputs, and all refuse it)
+        VerifyPart mine{kLowest, NAN, kLowest, 0.f};
         const float scale = fine.hi;
         if (nodes > 0 && cold) {
             // the first largest logit; a NaN counts as an infinity
@@ -747,7 +749,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
                 cluster_store(cluster_map(&s.node[j], r), *reinterpret_cast<const int4*>(&s.node[j]));
             }
             if (tid < (int32_t)ctas)
-                cluster_store(cluster_map(&s.tree, tid), make_int4(q0, nodes, __float_as_int(heat), 0));
+                cluster_store(cluster_map(&s.tree, tid), make_int4(q0, nodes, __float_as_int(heat), __float_as_int(fine.hi)));
         }
         for (uint32_t m = __ballot_sync(0xffffffffu, told); m != 0; m &= m - 1) {
             const int32_t l = __ffs(m) - 1;
@@ -799,6 +801,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
                     // (up to four parts a lane)
                     VerifyPart x[kVerifyMaxCluster * kVerifyWarps / 32];
                     RowSum sx, sy;
+                    const float scale = __int_as_float(s.tree.w);   // (as told: all decide by the same)
                     sx.start(scale);
                     sy.start(scale);
 #pragma unroll
