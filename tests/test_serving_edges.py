@@ -139,6 +139,85 @@ def test_greedy_walks_report_tokens_outside_the_vocabulary(cuda_device, draft, d
         assert int(token[keep.index(2)]) == int(b.logits[9].float().argmax())
 
 
+# ---- release, fork ---------------------------------------------------------------------------
+
+def _wide_pool(n, width, seed, counted):
+    """Rows of random lengths up to ``width`` blocks over a pool of all their blocks;
+    with counts, each third row starts with the leading blocks of the row before it."""
+    rng = np.random.default_rng(seed)
+    held = rng.integers(width // 2, width + 1, n).astype(np.int32)
+    total = int(held.sum())
+    perm = rng.permutation(total).astype(np.int32)
+    tables = np.full((n, width), -1, np.int32)
+    tables[np.arange(width) < held[:, None]] = perm
+    if counted:
+        for i in range(3, n, 3):
+            k = int(min(held[i], held[i - 1])) // 2
+            tables[i, :k] = tables[i - 1, :k]
+    counts = np.bincount(tables[tables >= 0], minlength=total).astype(np.int32)
+    idle = np.flatnonzero(counts == 0).astype(np.int32)       # blocks of no row: the queue
+    head = total - len(idle)
+    free = np.full(total, -1, np.int32)
+    free[head:] = idle
+    return held, tables, counts, free, head
+
+
+def _wide_release(held, keep, tables, counts, free, head):
+    """The release on the host: counts, queue, front after it."""
+    col = np.arange(tables.shape[1])
+    drops = tables[(col >= keep[:, None]) & (col < held[:, None])]
+    drops = drops[(drops >= 0) & (drops < len(free))]
+    if counts is None:
+        freed = drops
+    else:
+        counts = counts - np.bincount(drops, minlength=len(free)).astype(np.int32)
+        _, last = np.unique(drops[::-1], return_index=True)
+        last = np.sort(len(drops) - 1 - last)
+        freed = drops[last]
+        freed = freed[counts[freed] == 0]
+    free, head = free.copy(), head - len(freed)
+    free[head:head + len(freed)] = freed
+    return counts, free, head
+
+
+@pytest.mark.parametrize("n,width", [(260, 6100), (5003, 300)])
+@pytest.mark.parametrize("counted", [True, False])
+def test_release_of_more_entries_than_shared_memory_keeps(cuda_device, n, width, counted):
+    """Some 1.1 million entries, in one round of sequences and in two: each pass reads
+    the tables again.  As a whole, and refused as a whole."""
+    bs = 4
+    held, tables, counts, free, head = _wide_pool(n, width, seed=n, counted=counted)
+    keep = np.where(np.arange(n) % 17 == 5, held // 2, 0).astype(np.int32)
+    tables[7, 3], tables[n - 2, 5] = -1, len(free)            # passed over
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(cuda_device)
+    args = lambda head, free_d: (dev(keep * bs), dev(tables), dev(held), free_d, i32([head], cuda_device),
+                                 len(free), bs)
+    assert int((held - keep).sum()) > 16 * 40960
+
+    def run(head, counts):
+        free_d, ref = dev(free), dev(counts) if counted else None
+        got = pa.release_blocks(*args(head, free_d), ref_cnt=ref)
+        return got[0].cpu().numpy(), int(got[1]), free_d.cpu().numpy(), ref.cpu().numpy() if counted else None
+    want_counts, want_free, want_head = _wide_release(held, keep, tables, counts if counted else None, free, head)
+    got = run(head, counts)
+    assert pa.last_device_error() == pa.DEVERR_TABLE_ENTRY
+    assert (got[0] == keep).all() and got[1] == want_head and (got[2] == want_free).all()
+    if counted:
+        assert (got[3] == want_counts).all()
+    # no room in front of the queue for the last block
+    short = head - want_head - 1
+    got = run(short, counts)
+    assert pa.last_device_error() & pa.DEVERR_POOL
+    assert (got[0] == held).all() and got[1] == short and (got[2] == free).all()
+    assert not counted or (got[3] == counts).all()
+    if counted:
+        less = counts.copy()
+        less[tables[n - 1, held[n - 1] - 1]] -= 1               # dropped once more than held
+        got = run(head, less)
+        assert pa.last_device_error() & pa.DEVERR_SHARED
+        assert (got[0] == held).all() and got[1] == head and (got[2] == free).all() and (got[3] == less).all()
+
+
 # ---- PA_DEBUG --------------------------------------------------------------------------------
 
 def test_debug_refuses_forks_of_blocks_without_counts(cuda_device, monkeypatch):
