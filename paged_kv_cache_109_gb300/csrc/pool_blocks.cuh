@@ -334,8 +334,10 @@ __global__ void __launch_bounds__(kPoolThreads) release_blocks_kernel(const Rele
         each([&](int32_t e, int32_t id, bool) {
             const bool own = owns(e, id);
             const uint32_t mask = __ballot_sync(0xffffffffu, own);
+            const int32_t to = at + __popc(mask & ((1u << lane) - 1));
             if (own) {
-                a.free_blocks[at + __popc(mask & ((1u << lane) - 1))] = id;
+                // (behind the front only where somebody writes the inputs meanwhile)
+                if (to < head) a.free_blocks[to] = id;
                 if (COUNTED) a.ref_cnt[id] = 0;
             }
             at += __popc(mask);
@@ -428,7 +430,7 @@ __global__ void __launch_bounds__(kPoolThreads) fork_blocks_kernel(const ForkArg
     // (what a row becomes is read before any output is written: they may be the inputs)
     auto becomes = [&](int32_t i, int32_t& len, int32_t& held) {
         const int32_t p = a.src[i];
-        const int32_t from = bad || p < 0 ? i : p;
+        const int32_t from = bad || p < 0 || p >= a.num_seqs ? i : p;
         len = a.seq_lens[from];
         held = from == i ? a.blocks_held[i] : (int32_t)(((int64_t)len + a.block_size - 1) / a.block_size);
     };
@@ -458,7 +460,8 @@ __global__ void __launch_bounds__(kPoolThreads) fork_blocks_kernel(const ForkArg
                 old[u] = id[u] = -1;
                 if (!bad && q[u].tail) {
                     old[u] = a.block_tables[(int64_t)q[u].src * a.max_blocks + q[u].full];
-                    id[u] = a.free_blocks[at++];
+                    id[u] = at < a.num_free ? a.free_blocks[at] : -1;
+                    ++at;
                 }
             }
 #pragma unroll
@@ -541,8 +544,8 @@ fork_copy_kernel(const ForkArgs a, int32_t num_kv_heads, int32_t row_bytes,
     griddep_launch_dependents();
     const int32_t i = blockIdx.x;
     const int64_t src = a.block_pairs[2 * (int64_t)i], dst = a.block_pairs[2 * (int64_t)i + 1];
-    if (src < 0 || dst < 0) return;
-    const int32_t rows = a.seq_lens_out[i] % a.block_size;
+    if (src < 0 || dst < 0 || src >= a.num_blocks || dst >= a.num_blocks) return;
+    const int32_t rows = max(a.seq_lens_out[i], 0) % a.block_size;
     uint8_t* cache = (blockIdx.y & 1) ? caches.v[blockIdx.y >> 1] : caches.k[blockIdx.y >> 1];
     const int64_t head_bytes = (int64_t)a.block_size * row_bytes;
     const int64_t block_bytes = num_kv_heads * head_bytes;
