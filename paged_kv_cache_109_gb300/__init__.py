@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import operator
 import os
 
 import torch
@@ -856,7 +857,8 @@ def rope_write(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, q_w
     _contiguous(k_cache, v_cache, positions, inv_freq, slot_mapping, out)
     desc, rope = _descriptors((blocks, block, heads, d, _DTYPES[dtype]),
                               (2 * inv_freq.numel(), axes, bool(cyclic), bool(neighbours),
-                               float(scale), float(eps)), () if sections is None else tuple(sections))
+                               float(scale), float(eps)),
+                              () if sections is None else tuple(map(operator.index, sections)))
     st = load_library().pa_rope_write(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, n, hq,
         positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight), _ptr(k_weight),

@@ -118,6 +118,20 @@ def test_one_token_of_a_projection_in_place(cuda_device, dtype, pad_row):
     assert st == pa.PA_OK and torch.equal(q2.cpu(), q.cpu())
 
 
+def test_sections_that_change_between_calls(cuda_device):
+    """What a call does follows from the values of its sections, not from the objects
+    that hold them."""
+    sections = [torch.tensor(8), torch.tensor(24)]
+    for first in (8, 20):
+        sections[0].fill_(first)
+        sections[1].fill_(32 - first)
+        b = RopeBatch(5, 2, 1, 64, 8, F32, seed=2, axes=2, sections=(first, 32 - first))
+        b.args["sections"] = sections
+        out = b.run(pa, cuda_device)
+        b.args["sections"] = (first, 32 - first)
+        b.check(*out)
+
+
 # ---- verify_tree ---------------------------------------------------------------------------
 
 @pytest.mark.parametrize("draft", [True, False])
