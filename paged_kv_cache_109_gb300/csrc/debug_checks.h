@@ -65,6 +65,17 @@ inline pa_status check_slots(const int64_t* slot_mapping, int32_t n, int64_t num
     return check_slot_list(std::move(s), num_slots);
 }
 
+// The same of those tokens that are not skipped (position below zero).
+inline pa_status check_live_slots(const int64_t* slot_mapping, const int32_t* positions, int32_t n,
+                                  int64_t num_slots, cudaStream_t st) {
+    std::vector<int64_t> s;
+    std::vector<int32_t> pos;
+    if (!fetch(s, slot_mapping, (size_t)n, st) || !fetch(pos, positions, (size_t)n, st)) return PA_ERR_CUDA;
+    for (int32_t j = 0; j < n; ++j)
+        if (pos[j] < 0) s[j] = -1;
+    return check_slot_list(std::move(s), num_slots);
+}
+
 // Slots from (sequence, position) through the block tables, as the write
 // kernel computes them; an entry the kernel would report is an error here.
 inline pa_status check_positions(const int32_t* seq_ids, const int32_t* positions, int32_t n,

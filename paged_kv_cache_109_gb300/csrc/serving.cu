@@ -336,7 +336,7 @@ pa_status pa_rope_write(const void* q, const void* k, const void* v, int64_t q_s
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (debug::enabled()) {
         const pa_status r = debug_pass(
-            [&] { return debug::check_slots(a.slot_mapping, num_tokens, a.num_slots, st); });
+            [&] { return debug::check_live_slots(a.slot_mapping, a.positions, num_tokens, a.num_slots, st); });
         if (r != PA_OK) return r;
     }
     const int vec = rope_vec(a, eb);

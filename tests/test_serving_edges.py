@@ -234,6 +234,19 @@ def test_release_of_more_entries_than_shared_memory_keeps(cuda_device, n, width,
 
 # ---- PA_DEBUG --------------------------------------------------------------------------------
 
+def test_debug_passes_tokens_that_are_skipped(cuda_device, monkeypatch):
+    """A token with a negative position writes nothing: its slot is not looked at."""
+    monkeypatch.setenv("PA_DEBUG", "1")
+    for axes, sections in ((1, None), (2, (20, 12))):
+        b = RopeBatch(6, 2, 1, 64, 4, F32, seed=5, skip=(1, 4, 5), axes=axes, sections=sections)
+        b.slots[1], b.slots[4], b.slots[5] = b.slots[0], b.slots[0], 2 ** 40
+        b.check(*b.run(pa, cuda_device))
+        assert pa.last_device_error() == 0
+        b.pos.view(axes, -1)[0, 4] = 0
+        with pytest.raises(pa.PaError):
+            b.run(pa, cuda_device)
+
+
 def test_debug_refuses_forks_of_blocks_without_counts(cuda_device, monkeypatch):
     """A shared block's count says who holds it: one that no row counts would be freed
     by the fork's release, under its source."""
