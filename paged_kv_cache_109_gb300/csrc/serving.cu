@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <iterator>
 
 #include "common.cuh"
 #include "debug_checks.h"
@@ -502,6 +503,14 @@ pa_status pa_fork_blocks(const int32_t* src, const int32_t* seq_lens, int32_t* b
     const size_t cache_bytes = (size_t)cache->num_blocks * cache->num_kv_heads * cache->block_size * (size_t)row;
     for (int32_t x = 1; x < 2 * num_layers; ++x)
         if (bases[x] - bases[x - 1] < cache_bytes) return PA_ERR_INVALID_ARG;
+    // ... nor with the other arrays: the last cache that starts before an array's end
+    auto inside = [&](const Span& x) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(x.p);
+        const uintptr_t* last = std::lower_bound(bases, bases + 2 * num_layers, p + x.bytes);
+        return last != bases && overlap(x.p, x.bytes, reinterpret_cast<const void*>(last[-1]), cache_bytes);
+    };
+    if (std::any_of(std::begin(in), std::end(in), inside) || std::any_of(std::begin(outs), std::end(outs), inside))
+        return PA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (debug::enabled()) {
         const pa_status r = debug_pass([&] {

@@ -232,6 +232,23 @@ def test_release_of_more_entries_than_shared_memory_keeps(cuda_device, n, width,
         assert (got[0] == held).all() and got[1] == head and (got[2] == free).all() and (got[3] == less).all()
 
 
+def test_fork_outputs_over_a_cache_are_refused(cuda_device):
+    dev = lambda x: i32(x, cuda_device)
+    st = PoolState([9, 0], 4, 12, 4, seed=4)
+    k, v = torch.zeros(12, 1, 4, 8, device=cuda_device), torch.zeros(12, 1, 4, 8, device=cuda_device)
+    tables, lens, held, ref = st.tables.to(cuda_device), dev(st.lens), dev(st.held), st.counts().to(cuda_device)
+    free, head = dev(st.free), dev([st.head])
+    inside = lambda c, m: c.view(-1).view(torch.int32)[-m:]
+    call = lambda k=k, v=v, tables=tables, **kw: pa.fork_blocks(
+        dev([-1, 0]), lens, tables, held, ref, free, head, k, v, **kw)
+    for kw in (dict(seq_lens_out=inside(k, 2)), dict(blocks_held_out=inside(v, 2)), dict(free_head_out=inside(v, 1)),
+               dict(block_pairs=inside(k, 8).view(torch.int64).view(2, 2)), dict(tables=inside(v, 8).view(2, 4))):
+        with pytest.raises(pa.PaError) as e:
+            call(**kw)
+        assert e.value.status == pa.PA_ERR_INVALID_ARG
+    assert call()[1].tolist() == [3, 3] and pa.last_device_error() == 0
+
+
 # ---- PA_DEBUG --------------------------------------------------------------------------------
 
 def test_debug_passes_tokens_that_are_skipped(cuda_device, monkeypatch):
