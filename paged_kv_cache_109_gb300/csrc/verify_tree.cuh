@@ -406,16 +406,12 @@ struct FineScale {
     }
 };
 
+// 1 / x, off by a unit in the last place at most (the instruction's documented bound;
+// subnormal numbers are zero).
 __device__ __forceinline__ float rcp_approx(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
-}
-
-// 1 / x of a sum from 0.5 up, to a unit in the last place.
-__device__ __forceinline__ float rcp_newton(float x) {
-    const float r = rcp_approx(x);
-    return fmaf(r, fmaf(-x, r, 1.f), r);
 }
 
 // The race for the next token: the largest key, its place and least value, and the
@@ -821,8 +817,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
                     sy.sum = pack2(dsum, 0.f);
                     step = VerifyStep{kVerifyNext, any ? s.node[cur].child : -1, 0.f, 0.f, 0.f, 0.f, 0.f, 1.f, 0.f};
                     reduce_sums(sx, sy, step.top, sum, step.draft_top, dsum);
-                    step.inv = rcp_newton(sum);
-                    step.draft_inv = DRAFT && any ? rcp_newton(dsum) : 0.f;
+                    step.inv = rcp_approx(sum);
+                    step.draft_inv = DRAFT && any ? rcp_approx(dsum) : 0.f;
                     // (NaN, an infinity, or nothing to choose from)
                     if (!(sum >= 0.5f) || (DRAFT && any && !(dsum >= 0.5f))) step.verdict = kVerifyDone;
                 } else {

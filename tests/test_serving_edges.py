@@ -153,6 +153,30 @@ def test_greedy_walks_report_tokens_outside_the_vocabulary(cuda_device, draft, d
         assert int(token[keep.index(2)]) == int(b.logits[9].float().argmax())
 
 
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("vocab", [1, 2, 300, 4099, 20000])
+def test_a_token_of_all_the_probability_holds(cuda_device, vocab, dtype, draft):
+    """P(t) is one, then a power of two (equal tokens): the largest uniform below P(t) / q(t)
+    holds, P(t) / q(t) itself does not."""
+    below = 1 - 2.0 ** -24
+    for rest in (-float("inf"), -300.0, torch.finfo(dtype).min):
+        for alike in (1, 2, 4):
+            if alike > vocab or (draft and alike > 1):
+                continue
+            b = VerifyBatch([2, 2], vocab, dtype, seed=4, kind="chain", draft=draft)
+            b.logits[:] = rest
+            b.logits[:, vocab - alike:] = 3.0
+            if draft:
+                b.draft[:] = b.logits
+            b.tokens[:] = vocab - 1
+            b.uniforms[:] = below / alike
+            b.uniforms[3] = 1.0 / alike
+            leaf, _ = b.run(pa, cuda_device)
+            assert pa.last_device_error() == 0
+            assert leaf.tolist() == [1, 0], (rest, alike)
+
+
 # ---- release, fork ---------------------------------------------------------------------------
 
 def _wide_pool(n, width, seed, counted):
