@@ -10,8 +10,8 @@
 
 namespace pa {
 
-// Device error word (PA_DEVERR_* bits).  One per library; kernels OR bits in,
-// pa_last_device_error() reads and clears it.
+// Device error word (PA_DEVERR_* bits), one for the kernels of each source file:
+// they OR bits in, pa_last_device_error() reads and clears all.
 __device__ unsigned int g_device_error;
 
 __device__ __forceinline__ void raise_error(unsigned int bit) {

@@ -979,11 +979,11 @@ pa_status pa_check_wait_timeout(int32_t expected, int32_t arrivals, int64_t limi
 }
 
 int32_t pa_last_device_error(void) {
-    unsigned int bits = 0, zero = 0;
+    unsigned int bits = 0, more = 0;          // ..., serving.cu's word
+    const unsigned int zero = 0;
     if (cudaDeviceSynchronize() != cudaSuccess) return -1;
     if (cudaMemcpyFromSymbol(&bits, pa::g_device_error, sizeof(bits)) != cudaSuccess) return -1;
-    if (cudaMemcpyToSymbol(pa::g_device_error, &zero, sizeof(zero)) != cudaSuccess) return -1;
-    unsigned int more = 0;                    // the word of serving.cu's kernels
+    if (bits && cudaMemcpyToSymbol(pa::g_device_error, &zero, sizeof(zero)) != cudaSuccess) return -1;
     if (!pa::take_serving_error(&more)) return -1;
     return (int32_t)(bits | more);
 }

@@ -20,7 +20,7 @@ namespace pa {
 bool take_serving_error(unsigned int* bits) {
     const unsigned int zero = 0;
     return cudaMemcpyFromSymbol(bits, g_device_error, sizeof(*bits)) == cudaSuccess &&
-           cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero)) == cudaSuccess;
+           (*bits == 0 || cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero)) == cudaSuccess);
 }
 
 namespace {

@@ -273,6 +273,24 @@ def test_fork_outputs_over_a_cache_are_refused(cuda_device):
     assert call()[1].tolist() == [3, 3] and pa.last_device_error() == 0
 
 
+# ---- the error word ----------------------------------------------------------------------------
+
+def test_every_reported_bit_is_read_once(cuda_device):
+    """The kernels of both source files have a word of their own; a read takes and clears
+    both."""
+    k = torch.zeros(4, 1, 4, 8, device=cuda_device)
+    rows, past = torch.zeros(1, 1, 8, device=cuda_device), torch.tensor([16], device=cuda_device)
+    write = lambda: pa.write_kv(rows, rows, past, k, k.clone())
+    one, zero = i32([1], cuda_device), i32([0], cuda_device)
+    release = lambda: pa.release_blocks(zero, i32([[2]], cuda_device), one, i32([0, 0], cuda_device), zero, 4, 4)
+    for calls, bits in (((write,), pa.DEVERR_SLOT), ((release,), pa.DEVERR_POOL),
+                        ((write, release), pa.DEVERR_SLOT | pa.DEVERR_POOL), ((), 0)):
+        for call in calls:
+            call()
+        assert pa.last_device_error() == bits
+        assert pa.last_device_error() == 0
+
+
 # ---- PA_DEBUG --------------------------------------------------------------------------------
 
 def test_debug_passes_tokens_that_are_skipped(cuda_device, monkeypatch):
