@@ -15,19 +15,6 @@
 namespace pa {
 namespace {
 
-// Lets `kern` use `bytes` of shared memory on the current device: asked for once
-// per instance (its slot in `done`, a bit a device), with the most it ever uses.
-template <typename Kern>
-bool allow_smem(std::atomic<uint64_t>& done, Kern kern, size_t bytes) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return set_smem(kern, bytes);
-    const uint64_t bit = 1ull << dev;
-    if (done.load(std::memory_order_acquire) & bit) return true;
-    if (!set_smem(kern, bytes)) return false;
-    done.fetch_or(bit, std::memory_order_release);
-    return true;
-}
-
 pa_status plan_impl(PlanArgs a, cudaStream_t st) {
     const bool small = a.num_seqs <= kPlanSmallSeqs && a.max_tokens <= kPlanSmallTokens;
     cudaError_t err = launch_pdl(small ? plan_scan_kernel<true> : plan_scan_kernel<false>, dim3(1),
@@ -423,13 +410,14 @@ pa_status pa_plan_step(const int32_t* seq_lens, const int32_t* new_tokens,
             if (!same && overlap(out[x].p, out[x].bytes, y.p, y.bytes)) return PA_ERR_INVALID_ARG;
         }
     }
-    if (!map_current_arg(a.seq_lens) || !map_current_arg(a.new_tokens) || !map_current_arg(a.blocks_held) ||
-        !map_current_arg(a.free_blocks) || !map_current_arg(a.free_head) ||
-        !map_current_arg(a.seq_lens_out) || !map_current_arg(a.blocks_held_out) ||
-        !map_current_arg(a.free_head_out) || !map_current_arg(a.query_start) ||
-        !map_current_arg(a.block_start) || !map_current_arg(a.slot_mapping) ||
-        !map_current_arg(a.positions) || !map_current_arg(a.seq_ids) ||
-        (block_tables && !current_device_memory(block_tables)) || (ref_cnt && !current_device_memory(ref_cnt)))
+    const CallDevice dev;
+    if (!dev.map(a.seq_lens) || !dev.map(a.new_tokens) || !dev.map(a.blocks_held) ||
+        !dev.map(a.free_blocks) || !dev.map(a.free_head) ||
+        !dev.map(a.seq_lens_out) || !dev.map(a.blocks_held_out) ||
+        !dev.map(a.free_head_out) || !dev.map(a.query_start) ||
+        !dev.map(a.block_start) || !dev.map(a.slot_mapping) ||
+        !dev.map(a.positions) || !dev.map(a.seq_ids) ||
+        (block_tables && !dev.memory(block_tables)) || (ref_cnt && !dev.memory(ref_cnt)))
         return PA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (debug::enabled()) {
@@ -496,14 +484,15 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
         !aligned(query_start_loc, 4) || !aligned(parents, 4) || !aligned(block_tables, 4) ||
         !aligned(seq_lens, 4))
         return PA_ERR_INVALID_ARG;
-    if (!map_current_arg(q) || !map_current_arg(query_start_loc) || !map_current_arg(parents) ||
-        !map_current_arg(block_tables) || !map_current_arg(seq_lens) || !map_current_arg(out) ||
-        !current_device_memory(k_cache) || !current_device_memory(v_cache))
+    const CallDevice dev;
+    if (!dev.map(q) || !dev.map(query_start_loc) || !dev.map(parents) ||
+        !dev.map(block_tables) || !dev.map(seq_lens) || !dev.map(out) ||
+        !dev.memory(k_cache) || !dev.memory(v_cache))
         return PA_ERR_INVALID_ARG;
     const size_t need = pa_decode_tree_workspace_bytes(num_seqs, total_q, num_q_heads, max_q_len,
                                                        max_seq_len, cache);
     if (need > 0 && (!workspace || workspace_bytes_given < need || !aligned(workspace, 256) ||
-                     !current_device_memory(workspace)))
+                     !dev.memory(workspace)))
         return PA_ERR_WORKSPACE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (debug::enabled()) {
@@ -540,7 +529,7 @@ pa_status pa_decode_tree(const void* q, const int32_t* query_start_loc, const in
     a.scale_log2 = scale * kLog2e;
     // the tcgen05 kernel takes a row's maximum before it scales, and masks with
     // -inf: scale > 0; its copies of q are TMA, from device memory
-    const bool ws = tree_ws_shape(cache) && aligned(q, 16) && current_device_memory(q) &&
+    const bool ws = tree_ws_shape(cache) && aligned(q, 16) && dev.memory(q) &&
                     aligned(out, 16) && aligned(k_cache, 16) && aligned(v_cache, 16) && scale > 0.f;
     const bool caches16 = aligned(k_cache, 16) && aligned(v_cache, 16);
     const bool mma = !ws && tree_mma_shape(cache) && caches16;
@@ -624,9 +613,10 @@ pa_status pa_accept_tree(const int32_t* leaf, const int32_t* parents,
     AcceptArgs a{leaf, parents, query_start_loc, seq_lens, block_tables, new_lens, accepted_rows,
                  total_q, max_q_len, max_blocks_per_seq, cache->num_blocks, cache->block_size,
                  cache->num_kv_heads, cache->head_dim * elem_bytes(cache)};
-    if (!map_current_arg(a.leaf) || !map_current_arg(a.parents) || !map_current_arg(a.query_start) ||
-        !map_current_arg(a.seq_lens) || !map_current_arg(a.block_tables) ||
-        !map_current_arg(a.new_lens) || !map_current_arg(a.accepted_rows))
+    const CallDevice dev;
+    if (!dev.map(a.leaf) || !dev.map(a.parents) || !dev.map(a.query_start) ||
+        !dev.map(a.seq_lens) || !dev.map(a.block_tables) ||
+        !dev.map(a.new_lens) || !dev.map(a.accepted_rows))
         return PA_ERR_INVALID_ARG;
     int vec = 16;
     while (vec > 2 && a.row_bytes % vec) vec >>= 1;
@@ -636,7 +626,7 @@ pa_status pa_accept_tree(const int32_t* leaf, const int32_t* parents,
     for (int32_t l = 0; l < num_layers; ++l) {
         for (int which = 0; which < 2; ++which) {
             void* c = which ? v_caches[l] : k_caches[l];
-            if (!current_device_memory(c) || !aligned(c, elem_bytes(cache)))
+            if (!dev.memory(c) || !aligned(c, elem_bytes(cache)))
                 return PA_ERR_INVALID_ARG;
             while (vec > 2 && !aligned(c, vec)) vec >>= 1;
             bases[2 * l + which] = reinterpret_cast<uintptr_t>(c);

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <atomic>
 #include <mutex>
 #include <utility>
 
@@ -45,6 +46,26 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+template <typename Kern>
+bool set_smem(Kern kern, size_t bytes) {
+    if (bytes <= 48 * 1024) return true;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)bytes) == cudaSuccess;
+}
+
+// Lets `kern` use `bytes` of shared memory on the current device: asked for once
+// per instance (its slot in `done`, a bit a device), with the most it ever uses.
+template <typename Kern>
+bool allow_smem(std::atomic<uint64_t>& done, Kern kern, size_t bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return set_smem(kern, bytes);
+    const uint64_t bit = 1ull << dev;
+    if (done.load(std::memory_order_acquire) & bit) return true;
+    if (!set_smem(kern, bytes)) return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
+}
+
 // An NVTX range over one library call (host side: argument checks and
 // launches), so profilers can attribute the kernels to the call that made them.
 struct CallRange {
@@ -55,38 +76,6 @@ struct CallRange {
 };
 
 // ---- memory of the arguments ---------------------------------------------------
-
-// Device memory of the current device (or managed memory).
-bool current_device_memory(const void* p) {
-    if (!p) return false;
-    cudaPointerAttributes at;
-    int dev = -1;
-    if (cudaPointerGetAttributes(&at, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    return at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == dev);
-}
-
-// A step argument: replaces p by the address that kernels of the current device
-// use; false for memory they may not touch (allowed: the device's own, managed or
-// page-locked memory; nullptr passes).
-template <typename T>
-bool map_current_arg(T*& p) {
-    if (!p) return true;
-    cudaPointerAttributes at;
-    int dev = -1;
-    if (cudaPointerGetAttributes(&at, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    if (at.type == cudaMemoryTypeDevice) return at.device == dev;
-    if (at.type == cudaMemoryTypeHost && at.devicePointer) {
-        p = static_cast<T*>(at.devicePointer);
-        return true;
-    }
-    return at.type == cudaMemoryTypeManaged;
-}
 
 // A debug pass, whose host copies may throw: no exception leaves the library.
 template <typename F>
@@ -104,7 +93,7 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return a && b && na && nb && x < y + nb && y < x + na;
 }
 
-// The same checks of one call, the current device asked for once.
+// The memory checks of one call, the current device asked for once.
 struct CallDevice {
     int id = -1;
     CallDevice() {
@@ -118,7 +107,9 @@ struct CallDevice {
         cudaGetLastError();
         return false;
     }
-    // map_current_arg, current_device_memory
+    // Replaces p by the address that kernels of the current device use; false for memory
+    // they may not touch (allowed: the device's own, managed or page-locked memory;
+    // nullptr passes).
     template <typename T>
     bool map(T*& p) const {
         cudaPointerAttributes at;
@@ -131,6 +122,7 @@ struct CallDevice {
         }
         return at.type == cudaMemoryTypeManaged;
     }
+    // Device memory of the current device (or managed memory).
     bool memory(const void* p) const {
         cudaPointerAttributes at;
         return p && attributes(p, at) &&

@@ -148,14 +148,6 @@ cudaError_t launch_merge(const DecodeArgs& a, cudaStream_t st, int32_t typical_p
                                : launch_merge_w<E, 1>(warps, grid, st, a);
 }
 
-
-template <typename Kern>
-bool set_smem(Kern kern, size_t bytes) {
-    if (bytes <= 48 * 1024) return true;
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)bytes) == cudaSuccess;
-}
-
 template <int D, bool G16, bool CAS>
 cudaError_t launch_fast(dim3 grid, const CUtensorMap& mk, const CUtensorMap& mv,
                         const DecodeArgs& a, cudaStream_t st) {

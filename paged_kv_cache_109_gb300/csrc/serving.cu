@@ -25,20 +25,6 @@ bool take_serving_error(unsigned int* bits) {
 
 namespace {
 
-// Lets `kern` use `bytes` of dynamic shared memory on the current device: asked for once
-// per instance (`done`, a bit a device).
-template <typename Kern>
-bool allow_smem(std::atomic<uint64_t>& done, Kern kern, size_t bytes) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (done.load(std::memory_order_acquire) & bit) return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
-        return false;
-    done.fetch_or(bit, std::memory_order_release);
-    return true;
-}
-
 // launch_pdl of a grid whose CTAs form clusters of `ctas` along x.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, unsigned ctas, size_t smem,
