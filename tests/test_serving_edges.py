@@ -323,3 +323,110 @@ def test_debug_refuses_forks_of_blocks_without_counts(cuda_device, monkeypatch):
         counts[b] = 0
         with pytest.raises(pa.PaError):
             fork(counts.to(cuda_device))
+
+
+# ---- sizes past 32 bits ------------------------------------------------------------------------
+
+def test_rows_and_blocks_past_32_bits(cuda_device):
+    """Slots, tails and strides behind 2^31 elements."""
+    nb, hkv, bs, d = 33000, 8, 64, 128                  # 2.2e9 elements, 4.3 GB a cache
+    b = RopeBatch(5, 16, hkv, d, bs, BF, seed=7)
+    kc, vc = (torch.zeros(nb, hkv, bs, d, dtype=BF, device=cuda_device) for _ in range(2))
+    last = [nb - 1, nb - 2, 1]
+    b.slots[:] = torch.tensor([last[0] * bs + 3, last[0] * bs + 63, last[1] * bs, last[2] * bs + 5, 0])
+    width, far = b.qkv.shape[1], 550_000_000            # tokens 1.1 GB apart
+    wide = torch.empty(4 * far + width, dtype=BF, device=cuda_device)
+    rows = wide.as_strided((5, width), (far, 1))
+    rows.copy_(b.qkv)
+    move = lambda t: t.to(cuda_device)
+    out = pa.rope_write(*b.split(rows), move(b.pos), move(b.inv), move(b.slots), kc, vc, q_weight=move(b.qw),
+                        k_weight=move(b.kw), out=move(b.out), **b.args)
+    # the same rows into a cache of the four blocks alone
+    near = RopeBatch(5, 16, hkv, d, bs, BF, seed=7)
+    near.k_cache, near.v_cache = torch.zeros(4, hkv, bs, d, dtype=BF), torch.zeros(4, hkv, bs, d, dtype=BF)
+    near.slots[:] = torch.tensor([3 * bs + 3, 3 * bs + 63, 2 * bs, bs + 5, 0])
+    want = near.run(pa, cuda_device)
+    near.check(*want)
+    at = [0, 1, nb - 2, nb - 1]
+    assert torch.equal(out.cpu(), want[0]) and torch.equal(kc[at].cpu(), want[1]) and torch.equal(vc[at].cpu(), want[2])
+    assert int(kc.view(torch.int16).count_nonzero()) == int(want[1].view(torch.int16).count_nonzero())
+    del wide, rows
+    # a fork's tail between the last blocks
+    got = pa.fork_blocks(i32([-1, 0], cuda_device), i32([bs + 1, 0], cuda_device),
+                         i32([[5, nb - 2], [-1, -1]], cuda_device), i32([2, 0], cuda_device),
+                         torch.ones(nb, dtype=torch.int32, device=cuda_device), i32([nb - 3], cuda_device),
+                         i32([0], cuda_device), kc, vc)
+    assert got[3].tolist() == [[-1, -1], [nb - 2, nb - 3]] and pa.last_device_error() == 0
+    assert torch.equal(kc[nb - 3, :, 0], kc[nb - 2, :, 0]) and torch.equal(vc[nb - 3, :, 0], vc[nb - 2, :, 0])
+    assert int(kc[nb - 3, :, 1:].count_nonzero()) == 0 and int(kc[nb - 3].count_nonzero()) > 0
+
+
+def test_tables_past_32_bits(cuda_device):
+    """The last rows of a table of 2^31 entries and more."""
+    n, width, bs, nb = 65535, 33000, 4, 1000
+    tables = torch.full((n, width), -1, dtype=torch.int32, device=cuda_device)
+    lens, held = torch.zeros(n, dtype=torch.int32), torch.zeros(n, dtype=torch.int32)
+    lens[n - 1], held[n - 1], held[40000] = 9, 3, 2
+    tables[n - 1, :3], tables[40000, :2] = i32([10, 11, 12], cuda_device), i32([20, 21], cuda_device)
+    src = torch.full((n,), -1, dtype=torch.int32)
+    src[n - 2] = n - 1
+    counts = torch.zeros(nb, dtype=torch.int32, device=cuda_device)
+    counts[[10, 11, 12, 20, 21]] = 1
+    free, head = torch.arange(nb, dtype=torch.int32, device=cuda_device), i32([30], cuda_device)
+    k, v = torch.randn(nb, 1, bs, 8, device=cuda_device), torch.randn(nb, 1, bs, 8, device=cuda_device)
+    dev = lambda t: t.to(cuda_device)
+    lens2, held2, head2, pairs = pa.fork_blocks(dev(src), dev(lens), tables, dev(held), counts, free, head, k, v)
+    assert pa.last_device_error() == 0
+    assert tables[n - 2, :4].tolist() == [10, 11, 30, -1] and pairs[n - 2].tolist() == [12, 30] and head2.tolist() == [31]
+    assert counts[[10, 11, 12, 30]].tolist() == [2, 2, 1, 1] and torch.equal(k[30, :, :1], k[12, :, :1])
+    held3, head3 = pa.release_blocks(dev(lens), tables, held2, free, head2, nb, bs, ref_cnt=counts)
+    assert pa.last_device_error() == 0
+    assert head3.tolist() == [28] and free[28:31].tolist() == [20, 21, 30]
+    assert counts.sum() == 3 and held3[[40000, n - 2, n - 1]].tolist() == [0, 0, 3]
+
+
+def test_logits_past_32_bits(cuda_device):
+    """Rows of logits, draft and noise behind 2^31 elements, and a far stride."""
+    n, vocab = 3, 5003
+    for dtype, draft in ((BF, True), (F32, False)):
+        b = VerifyBatch([4, 5, 3], vocab, dtype, seed=8, draft=draft, temps=[1.0, 0.0, 0.7])
+        want = b.run(pa, cuda_device)
+        total, far = b.logits.shape[0], 250_000_000     # 12 rows: 2.75e9 elements
+        dev = lambda t: t.to(cuda_device)
+
+        def apart(t, step):
+            big = torch.empty((t.shape[0] - 1) * step + t.shape[1], dtype=t.dtype, device=cuda_device)
+            rows = big.as_strided(t.shape, (step, 1))
+            rows.copy_(t)
+            return rows
+        got = pa.verify_tree(apart(b.logits, far), dev(b.tokens), dev(b.parents), dev(b.start), dev(b.uniforms),
+                             apart(b.noise, 1_200_000_000), b.max_q,
+                             draft_logits=apart(b.draft, far + 1) if draft else None, temperature=dev(b.temps))
+        assert pa.last_device_error() == 0
+        assert torch.equal(got[0].cpu(), want[0]) and torch.equal(got[1].cpu(), want[1])
+        del got
+        torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("vocab", [1 << 30, (1 << 30) - 5])
+def test_the_largest_vocabulary(cuda_device, vocab):
+    """One row of 2^30 tokens: greedy, sampled, and a drafted token of half the weight."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    logits = torch.full((2, vocab), -30.0, dtype=BF, device=cuda_device)
+    spots = [0, 7, vocab // 2 + 1, vocab - 2, vocab - 1]
+    logits[0, spots] = torch.tensor([1.0, 0.0, 2.0, 4.0, 3.0], dtype=BF, device=cuda_device)
+    logits[1, spots[2]] = 9.0
+    noise = torch.full((1, vocab), 1.0, device=cuda_device)
+    noise[0, spots] = torch.rand(5, device=cuda_device, generator=g) * 0.2 + 0.1
+    child, start, par = i32([0, vocab - 2], cuda_device), i32([0, 2], cuda_device), i32([-1, 0], cuda_device)
+    call = lambda u, heat: [int(x) for x in pa.verify_tree(
+        logits, child, par, start, torch.tensor([0.0, u], device=cuda_device), noise, 2,
+        temperature=torch.tensor([heat], device=cuda_device))]
+    assert call(0.5, 0.0) == [1, spots[2]]
+    # 2^30 weights of e^-34 are 1.8e-6 of the largest
+    p = torch.softmax(torch.tensor([1.0, 0.0, 2.0, 4.0, 3.0]).double(), 0)
+    assert call(float(p[3]) - 1e-4, 1.0) == [1, spots[2]]
+    race = p / noise[0, spots].cpu().double()
+    race[3] = 0.0
+    assert call(float(p[3]) + 1e-4, 1.0) == [0, spots[int(race.argmax())]]
+    assert pa.last_device_error() == 0
