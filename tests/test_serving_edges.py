@@ -2,6 +2,8 @@
 do not make: one token in place, the documented loop, releases that do not fit in
 shared memory, reports of a greedy walk, what PA_DEBUG refuses and what it does not."""
 import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -430,3 +432,42 @@ def test_the_largest_vocabulary(cuda_device, vocab):
     race[3] = 0.0
     assert call(float(p[3]) + 1e-4, 1.0) == [0, spots[int(race.argmax())]]
     assert pa.last_device_error() == 0
+
+
+# ---- the first calls of a process ----------------------------------------------------------------
+
+FIRST = """
+import torch
+import paged_kv_cache_109_gb300 as pa
+dev = torch.device("cuda:0")
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+kc, vc = (torch.zeros(16, 2, 4, 64, device=dev) for _ in range(2))
+q, k, v = (torch.randn(3, h, 64, device=dev) for h in (4, 2, 2))
+pos, inv, slots = i32([0, 1, 2]), torch.ones(32, device=dev), torch.arange(3, device=dev)
+logits, noise, u = torch.randn(4, 50, device=dev), torch.rand(2, 50, device=dev) + 0.1, torch.rand(4, device=dev)
+tokens, parents, start = i32([0, 1, 0, 2]), i32([-1, 0, -1, 0]), i32([0, 2, 4])
+src, lens, held = i32([-1, 0]), i32([6, 0]), i32([2, 0])
+table, counts, free, head = i32([[0, 1], [-1, -1]]), i32([1, 1] + [0] * 14), i32(range(16)), i32([2])
+def step():
+    out = pa.rope_write(q, k, v, pos, inv, slots, kc, vc)
+    leaf, token = pa.verify_tree(logits, tokens, parents, start, u, noise, 2, draft_logits=logits)
+    _, held2, head2, pairs = pa.fork_blocks(src, lens, table, held, counts, free, head, kc, vc)
+    held3, head3 = pa.release_blocks(lens, table, held2, free, head2, 16, 4, ref_cnt=counts)
+    return [out, leaf, token, pairs, held3, head3]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+assert pa.last_device_error() == 0 and got[3].tolist() == [[-1, -1], [1, 2]] and got[5].tolist() == [2]
+for x, y in zip(got, step()):
+    assert torch.equal(x, y)
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured(cuda_device):
+    done = subprocess.run([sys.executable, "-c", FIRST], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and done.stdout.split() == ["same"], done.stderr[-2000:]
