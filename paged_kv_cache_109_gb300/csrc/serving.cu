@@ -89,10 +89,14 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
     const int64_t room = (int64_t)std::max(1, device_sm_count()) * 8;
     int32_t splits = 1;
     while (splits < 16 && 2 * splits * (int64_t)a.num_tokens <= room && splits * groups < rows) splits *= 2;
-    // two also where one would leave a third of the 24 a SM that 16-byte pieces of bf16 have
-    // (2303 tokens 17.8 us with one, 16.8 with two, from L2 16.0 and 13.0; 3000 tokens 18.6,
-    // 18.9; fp32, of 32 a SM: 2303 tokens of 15 + 5 heads of 80 9.7, 10.3)
-    if (splits == 1 && sizeof(E) == 2 && VEC == 8 && a.num_tokens <= 2 * room && groups < rows) splits = 2;
+    // two also where one would leave a third of the 24 a SM that 16-byte pieces of bf16 have,
+    // and has 8 turns of query rows or more.  One and two warps, rows from memory, with norms:
+    // 2303 tokens of 64 + 8 heads of 128 27.0, 22.8 us, of 32 + 8 17.7, 16.5, 1300 of them 11.6,
+    // 11.4; but 1000 10.6, 11.1 and 3000 18.4, 18.7, and with 4 turns, 2303 of 16 + 4 heads of
+    // 128 11.2, 12.7, of 32 + 8 heads of 64 10.5, 11.5.  (fp32, of 32 a SM: 2303 tokens of 15 + 5
+    // heads of 80 9.9, 10.0.)
+    if (sizeof(E) == 2 && VEC == 8 && a.num_tokens > room && a.num_tokens <= 2 * room && rows >= 8 * groups)
+        splits = 2;
     const size_t ring = VEC * sizeof(E) == 16 ? (size_t)kRopeDepth * 2 * kRopeThreads * 16 : 0;
     const size_t smem = ring + (size_t)kRopeWarps * (a.rot_dim / 2) * sizeof(float2);
     const int64_t ctas = ((int64_t)a.num_tokens * splits + kRopeWarps - 1) / kRopeWarps;
