@@ -774,12 +774,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
                 return;
             }
             int32_t j = s.node[cur].child;
-            bool out = false;           // a token outside the vocabulary was met
             while (j >= 0 && s.node[j].token != best) {
-                out |= s.node[j].token < 0 || s.node[j].token >= vocab;
+                const uint32_t t = s.node[j].token;     // (outside the vocabulary: met here)
+                if (t >= (uint32_t)vocab && rank == 0 && tid == 0) raise_error(PA_DEVERR_TREE);
                 j = s.node[j].sibling;
             }
-            if (out && rank == 0 && tid == 0) raise_error(PA_DEVERR_TREE);
             if (j < 0) {
                 finish(0, cur, best);
                 return;
