@@ -694,7 +694,7 @@ pa_status pa_rope_write(const void* q, const void* k, const void* v, int64_t q_s
  * tokens           device or pinned int32 [total_q]; node 0's is not read.
  * uniforms         device or pinned float [total_q].
  * noise            device or pinned float [num_seqs][vocab_size], rows noise_stride apart;
- *                  below 2^-126 it counts as zero.
+ *                  below 2^-126 it counts as zero, above 2^126 as infinite.
  * temperature      device or pinned float [num_seqs], or NULL for 1.
  * leaf, next_tokens  device or pinned int32 [num_seqs]; a sequence without nodes gets -1
  *                  in both.
@@ -705,6 +705,14 @@ pa_status pa_rope_write(const void* q, const void* k, const void* v, int64_t q_s
  * outside [-1, own node) is reported (PA_DEVERR_TREE) and read as -1; a child whose
  * token is outside the vocabulary is reported when it is met (PA_DEVERR_TREE) and
  * passed over.
+ * Precision: weights are exponentials in 32 bits relative to the row's largest (zero
+ * below 2^-126 of it), within 2^-16 of themselves down to 2^-64; sums, S and c are in 32
+ * bits too.  A decision is the formula's unless its sides are closer than
+ * 2^-16 (P(t) + (c + u + u S) q(t)), u = uniforms[r], q = 1 without draft rows: where tries
+ * have left little of P, S is as inexact as that difference.  Next tokens whose
+ * quotients are closer than 2^-16 (P + c q) / noise are compared again with the
+ * exponents' roundings taken in, not to the last bit; equal logits (and draft logits)
+ * with equal noise give the lowest x.
  * The result is reproducible for fixed arguments on a fixed device.
  */
 pa_status pa_verify_tree(const void* logits, const void* draft_logits, int64_t logit_stride,
@@ -734,8 +742,8 @@ pa_status pa_verify_tree(const void* logits, const void* draft_logits, int64_t l
  * (pa_plan_step, pa_fork_blocks).  Where seq_lens[i] was zeroed for a finished request
  * it is 0 for the next pa_plan_step too, which refuses tokens without blocks.
  *
- * All or nothing: where seq_lens[i] < 0, h_i outside [K_i, max_blocks_per_seq]
- * (PA_DEVERR_SEQ_LEN), m > F or F outside [0, num_free] (PA_DEVERR_POOL), or a count
+ * All or nothing: where seq_lens[i] < 0, h_i outside [K_i, max_blocks_per_seq], 2^30
+ * entries or more are dropped (PA_DEVERR_SEQ_LEN), m > F or F outside [0, num_free] (PA_DEVERR_POOL), or a count
  * would drop below zero (PA_DEVERR_SHARED), nothing changes and both outputs are the
  * inputs.  An entry outside [0, num_blocks) is passed over (PA_DEVERR_TABLE_ENTRY).
  *
@@ -774,7 +782,8 @@ pa_status pa_release_blocks(const int32_t* seq_lens, const int32_t* block_tables
  *
  * All or nothing: where src[i] is not a row, is itself forked by this call, or row i
  * holds blocks (PA_DEVERR_FORK), where seq_lens[p] < 0 or blocks_held[p] is outside
- * [ceil(T / B), max_blocks_per_seq] (PA_DEVERR_SEQ_LEN), or the queue is too short
+ * [ceil(T / B), max_blocks_per_seq], 2^30 entries or more are shared
+ * (PA_DEVERR_SEQ_LEN), or the queue is too short
  * (PA_DEVERR_POOL), nothing changes: the outputs are the inputs, all pairs -1.  An entry
  * outside [0, num_blocks) is reported (PA_DEVERR_TABLE_ENTRY): a shared one is
  * taken over without a count, a tail's is not copied, a fresh one becomes -1.

@@ -132,7 +132,9 @@ cudaError_t launch_verify(const VerifyArgs& a, int32_t num_seqs, cudaStream_t st
     // costs count once a CTA.  1, 2, 4 and 8 CTAs, chains of 5 nodes on bf16: one of 16000
     // tokens 18.2, 13.8, 11.8, 11.4 us, one of 131072 84, 47, 29, 19; 128 of 8000 18.3,
     // 17.7, 22.1, 34.5, of 32000 35, 30, 30, 40; 400 of 32000 83, 69, 76, 109, of 131072
-    // 295, 241, 217, 211.
+    // 295, 241, 217, 211.  Sequences of one node, from memory: 64 of 131072 32.6, 22.7, 18.7, 18.2,
+    // 256 of 128256 57, 62, 56, 58 (greedy 47, 42, 45, 51), 400 of 32000 25, 28, 33, 53: more CTAs
+    // than these need, as chains of 5 want them.
     const int64_t room = (int64_t)std::max(1, device_sm_count()) * 4;
     unsigned ctas = 1;
     while (ctas < 8 && a.vocab / (2 * (int32_t)ctas) >= ((int64_t)num_seqs * 2 * ctas <= room ? 2048 : 8192)) ctas *= 2;

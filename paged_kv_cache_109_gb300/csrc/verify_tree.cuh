@@ -26,11 +26,13 @@
 // practice the walk, whose steps wait for one another.  A step of 131072 tokens on bf16 in
 // 8 CTAs takes some 7500 clocks alone: 4300 for the two rows, 1050 for the barrier, 1200
 // for the decision, the rest for the warps' sums; three times as many CTAs on an SM make
-// it 11000.  Measured (GPU time): 64 chains of 5 nodes, 115 MB, 46 us (the copy rate:
-// 17); 128 trees of up to 40, 243 MB, 80 us (36); 48 trees on fp32 with 100003 tokens and
+// it 11000.  Measured (GPU time): 64 chains of 5 nodes, 115 MB, 45 us (the copy rate:
+// 17); 128 trees of up to 40, 243 MB, 79 us (36); 48 trees on fp32 with 100003 tokens and
 // no draft rows, 63 MB, 34 us from memory (9.3); one chain of 6 at 32000 tokens 18 us, a
-// launch and 6 steps.  Half of the issue slots are in use then; deeper copies, a fetch of
-// the likely next rows ahead, 16 CTAs a sequence or 512 threads a CTA did not help.
+// launch and 6 steps; sampling alone (one node) 64 rows of 131072, 50 MB, 18 us from memory
+// (7.4).  Half of the issue slots are in use then; deeper copies, a fetch of
+// the likely next rows ahead, 16 CTAs a sequence or 512 threads a CTA did not help.  64
+// registers, for 4 CTAs an SM; five of the eight instances spill 20 to 92 bytes.
 #pragma once
 
 #include "cluster.cuh"
@@ -166,7 +168,10 @@ struct RowVec {
     }
 };
 
-// The running maximum of a share and its sum of exponentials.  A NaN or +inf makes
+// The running maximum of a share and its sum of exponentials, in 32 bits: all terms are
+// positive and at most V / 8192 + 30 additions follow one another, each off by 2^-24 of
+// itself, so 131072 tokens' sum is off by 2^-18 with the exponentials' own 2^-20 to 2^-22
+// (sums in 64 bits and exp2f made 64 chains 272 us).  A NaN or +inf makes
 // the sum NaN; -inf counts as nothing.  The maximum starts at the lowest finite value:
 // a row of nothing but that has weights of one, and no -inf is subtracted from another.
 constexpr float kLowest = -3.402823466e38f;
