@@ -1,6 +1,7 @@
 """Calls around the attention that the documentation allows and that the other tests
-do not make: one token in place, the documented loop, releases that do not fit in
-shared memory, reports of a greedy walk, what PA_DEBUG refuses and what it does not."""
+do not make: the documented loop, one token in place, reports of a greedy walk, the
+largest sizes, releases that do not fit in shared memory, first calls in a graph, what
+PA_DEBUG refuses and what it does not."""
 import os
 import subprocess
 import sys
@@ -10,7 +11,7 @@ import pytest
 import torch
 
 import paged_kv_cache_109_gb300 as pa
-from tests._serving import (PoolState, RopeBatch, VerifyBatch, i32)
+from tests._serving import PoolState, RopeBatch, VerifyBatch, i32
 from tests.conftest import ROOT
 
 pytestmark = pytest.mark.gpu
@@ -27,7 +28,7 @@ def clear_device_error(cuda_device):
 # ---- the documented loop -----------------------------------------------------------------
 
 def _documented_step():
-    """The drafted step as README.md gives it."""
+    """The drafted step as the documentation gives it."""
     with open(os.path.join(ROOT, "README.md")) as f:
         text = f.read()
     begin = text.index("# one drafted (speculative) step")
@@ -35,7 +36,7 @@ def _documented_step():
 
 
 def test_the_documented_step_runs_as_a_loop(cuda_device):
-    """README's drafted step, run as it stands for several steps: a request that
+    """The drafted step, run as it stands for several steps: a request that
     ends, a fork into its row, and at the end every block back in the queue."""
     dev = lambda x: i32(x, cuda_device)
     g = torch.Generator(device="cuda").manual_seed(1)
